@@ -15,6 +15,10 @@ Functions mirror the C ABI in ``include/wq.h``:
   wq_linear_batch(weights, xs, out_dtypes=None, fuse_rht=True, workspace=None) -> [y]
   wq_linear_batch_noalloc(weights, xs, out_dtypes=None, fuse_rht=True, out=None) -> [y]
   wq_embed(table, ids, out_dtype=float16, out=None)  -> dequantised table rows
+  wq_kv_write(cache, k, v, slots)                    -> None (rows coded into the KVCache)
+  wq_kv_read(cache, slots, out=None)                 -> (k, v) rows as fp16
+  wq_attn_decode(cache, q, table, lens, max_len=None, window=0, scale=None, ...) -> out
+  wq_rope(xs, cos, sin, positions, head_dim, pair_axis=None, adjacent=False, out=None) -> [y]
 """
 
 from __future__ import annotations
@@ -33,6 +37,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "libwq.so")
 WQ_OK, WQ_E_ARG, WQ_E_UNSUPPORTED, WQ_E_ALIGN, WQ_E_WORKSPACE, WQ_E_HIP = 0, -1, -2, -3, -4, -5
 WQ_F16, WQ_F32 = 1, 2
 WQ_FUSE_RHT = 1
+WQ_ROPE_ADJACENT = 1
 WQ_MAX_BATCH = 8
 STATUS_NAMES = {0: "WQ_OK", -1: "WQ_E_ARG", -2: "WQ_E_UNSUPPORTED", -3: "WQ_E_ALIGN",
                 -4: "WQ_E_WORKSPACE", -5: "WQ_E_HIP"}
@@ -48,6 +53,12 @@ class WqWeight(ctypes.Structure):
                 ("block_bits", _vp), ("block_off", _vp),
                 ("rht_signs", _vp), ("rht_block", ctypes.c_int32),
                 ("block_bits_host", _vp)]
+
+
+class WqKvCache(ctypes.Structure):
+    _fields_ = [("bits", _i32), ("head_dim", _i32), ("kv_heads", _i32), ("page_size", _i32),
+                ("pages", _i64), ("k", _vp), ("v", _vp), ("k_params", _vp), ("v_params", _vp),
+                ("rht_signs", _vp), ("rht_block", _i32)]
 
 
 SIGNATURES = {
@@ -68,6 +79,14 @@ SIGNATURES = {
     "wq_linear_batch_noalloc": (_i32, [_i32, ctypes.POINTER(WqWeight), ctypes.POINTER(_vp),
                                        ctypes.POINTER(_i64), _i64, ctypes.POINTER(_vp), ctypes.POINTER(_i32),
                                        ctypes.POINTER(_i64), _u32, _vp]),
+    "wq_kv_write": (_i32, [ctypes.POINTER(WqKvCache), _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "wq_kv_read": (_i32, [ctypes.POINTER(WqKvCache), _vp, _i64, _vp, _i64, _vp, _i64, _vp]),
+    "wq_attn_decode_workspace": (_sz, [ctypes.POINTER(WqKvCache), _i64, _i32, _i64, _i64]),
+    "wq_attn_decode": (_i32, [ctypes.POINTER(WqKvCache), _vp, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _i64,
+                              ctypes.c_float, _vp, _i64, _vp, _sz, _vp]),
+    "wq_rope": (_i32, [_i32, ctypes.POINTER(_vp), ctypes.POINTER(_i64), ctypes.POINTER(_vp),
+                       ctypes.POINTER(_i64), ctypes.POINTER(_i32), _i64, _i32, _i32, _vp, _vp, _i64, _vp,
+                       _i64, _i32, _vp, _u32, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 64 << 20   # WQ_NOALLOC_SCRATCH_BYTES
 
@@ -315,6 +334,186 @@ def wq_embed(table: QWeight, ids: torch.Tensor, out_dtype=torch.float16, out: Op
                                       WQ_F32 if out_dtype == torch.float32 else WQ_F16,
                                       y.stride(0) if count else table.k, _stream()))
     return y
+
+
+def _rows(t: torch.Tensor, cols: int, name: str) -> torch.Tensor:
+    """fp16 GPU rows [n][cols], any row stride."""
+    if not t.is_cuda or t.dtype != torch.float16:
+        raise ValueError(f"{name} must be a float16 GPU tensor")
+    if t.dim() != 2 or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
+        raise ValueError(f"{name} must be [rows][{cols}] with contiguous rows, got {tuple(t.shape)}")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride; torch leaves that of a single row arbitrary."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+@dataclass
+class KVCache:
+    """One layer's paged key-value cache in libwq's layout (``wq_kv_cache``
+    of include/wq.h); ``KVCache.new`` allocates one."""
+    bits: int                     # 4, 8 (codes) or 16 (fp16 values)
+    head_dim: int                 # 64, 128 or 256
+    kv_heads: int
+    page_size: int                # tokens per page
+    k: torch.Tensor               # uint8 (float16 for 16 bits) [pages][kv_heads][page_size * units]
+    v: torch.Tensor
+    k_params: Optional[torch.Tensor] = None    # float16 [pages][kv_heads][page_size][2]
+    v_params: Optional[torch.Tensor] = None
+    signs: Optional[torch.Tensor] = None       # int32 view of uint32 [kv_heads * head_dim / 32]
+
+    def __post_init__(self):
+        if self.bits not in (4, 8, 16):
+            raise ValueError(f"bits={self.bits} (4, 8 or 16)")
+        units = self.head_dim // 2 if self.bits == 4 else self.head_dim
+        dt = torch.float16 if self.bits == 16 else torch.uint8
+        pages = self.k.shape[0]
+        for name, t in (("k", self.k), ("v", self.v)):
+            _dev(t, dt, name)
+            if t.numel() != pages * self.kv_heads * self.page_size * units:
+                raise ValueError(f"{name}: {t.numel()} units do not make {pages} pages of {self.kv_heads} heads x "
+                                 f"{self.page_size} tokens x {units}")
+        for name, t in (("k_params", self.k_params), ("v_params", self.v_params)):
+            if self.bits == 16:
+                continue
+            if t is None:
+                raise ValueError(f"{name} is needed for {self.bits} bits")
+            _dev(t, torch.float16, name)
+            if t.numel() != pages * self.kv_heads * self.page_size * 2:
+                raise ValueError(f"{name}: {t.numel()} values do not make {pages} pages of {self.kv_heads} heads x "
+                                 f"{self.page_size} pairs")
+        if self.signs is not None:
+            _dev(self.signs, torch.int32, "signs")
+            if self.signs.numel() * 32 != self.kv_heads * self.head_dim:
+                raise ValueError(f"signs: {self.signs.numel()} words for {self.kv_heads * self.head_dim} channels")
+        self._c = WqKvCache(self.bits, self.head_dim, self.kv_heads, self.page_size, pages, _ptr(self.k),
+                            _ptr(self.v), _ptr(self.k_params), _ptr(self.v_params), _ptr(self.signs),
+                            128 if self.signs is not None else 0)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def new(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int,
+            signs: Optional[torch.Tensor] = None, device="cuda") -> "KVCache":
+        """A cache of ``pages`` empty pages."""
+        units = head_dim // 2 if bits == 4 else head_dim
+        dt = torch.float16 if bits == 16 else torch.uint8
+        k, v = (torch.zeros((pages, kv_heads, page_size * units), dtype=dt, device=device) for _ in range(2))
+        kp, vp = (None if bits == 16 else
+                  torch.zeros((pages, kv_heads, page_size, 2), dtype=torch.float16, device=device)
+                  for _ in range(2))
+        return cls(bits, head_dim, kv_heads, page_size, k, v, kp, vp, signs)
+
+
+def wq_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Code the rows of ``k`` and ``v`` (fp16 [tokens][kv_heads * head_dim]) into
+    the cache at ``slots`` (int32 [tokens]; outside the cache: skipped)."""
+    cols = cache.kv_heads * cache.head_dim
+    _rows(k, cols, "k")
+    _rows(v, cols, "v")
+    _dev(slots, torch.int32, "slots")
+    n = slots.numel()
+    if k.shape[0] != n or v.shape[0] != n:
+        raise ValueError(f"{k.shape[0]} key and {v.shape[0]} value rows for {n} slots")
+    _check("wq_kv_write", lib().wq_kv_write(cache._ref, k.data_ptr(), _ld(k), v.data_ptr(), _ld(v),
+                                            slots.data_ptr(), n, _stream()))
+
+
+def wq_kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None):
+    """The cached rows at ``slots`` as fp16: (k, v), each [tokens][kv_heads * head_dim]."""
+    _dev(slots, torch.int32, "slots")
+    n, cols = slots.numel(), cache.kv_heads * cache.head_dim
+    if out is None:
+        k = torch.empty((n, cols), dtype=torch.float16, device=slots.device)
+        v = torch.empty_like(k)
+    else:
+        k, v = _rows(out[0], cols, "out[0]"), _rows(out[1], cols, "out[1]")
+        if k.shape[0] != n or v.shape[0] != n:
+            raise ValueError(f"out: {k.shape[0]} and {v.shape[0]} rows for {n} slots")
+    _check("wq_kv_read", lib().wq_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), _ld(k), v.data_ptr(),
+                                          _ld(v), _stream()))
+    return k, v
+
+
+def wq_attn_decode_workspace(cache: KVCache, seqs: int, q_heads: int, max_len: int, window: int = 0) -> int:
+    size = lib().wq_attn_decode_workspace(cache._ref, seqs, q_heads, max_len, window)
+    if size == ctypes.c_size_t(-1).value:
+        raise WqError("wq_attn_decode_workspace", WQ_E_ARG, lib().wq_last_error().decode())
+    return size
+
+
+def wq_attn_decode(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                   max_len: Optional[int] = None, window: int = 0, scale: Optional[float] = None,
+                   workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """Attention of one new token per sequence: ``q`` fp16 [seqs][q_heads *
+    head_dim] over the pages ``table`` (int32 [seqs][pages]) and lengths
+    ``lens`` (int32 [seqs]) name.  ``max_len``: an upper bound of the lengths
+    (default: what the table's pages hold); ``scale``: default
+    head_dim ** -0.5."""
+    seqs, cols = q.shape
+    _rows(q, cols, "q")
+    if cols % cache.head_dim:
+        raise ValueError(f"q: {cols} columns are not heads of {cache.head_dim}")
+    if not (table.is_cuda and lens.is_cuda) or table.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise ValueError("table and lens must be int32 GPU tensors")
+    if table.dim() != 2 or table.shape[0] != seqs or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"table must be [{seqs}][pages] with contiguous rows, got {tuple(table.shape)}")
+    if lens.shape != (seqs,) or (seqs > 1 and lens.stride(0) != 1):
+        raise ValueError(f"lens must be [{seqs}], got {tuple(lens.shape)}")
+    held = table.shape[1] * cache.page_size
+    if max_len is None:
+        max_len = held
+    elif max_len > held:
+        raise ValueError(f"max_len={max_len}: {table.shape[1]} pages of {cache.page_size} tokens hold {held}")
+    y = torch.empty((seqs, cols), dtype=torch.float16, device=q.device) if out is None else _rows(out, cols, "out")
+    if y.shape[0] != seqs:
+        raise ValueError(f"out: {y.shape[0]} rows for {seqs} sequences")
+    heads = cols // cache.head_dim
+    if workspace is None:
+        need = wq_attn_decode_workspace(cache, seqs, heads, max_len, window)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    _check("wq_attn_decode", lib().wq_attn_decode(
+        cache._ref, q.data_ptr(), _ld(q), heads, seqs, table.data_ptr(), table.stride(0) if seqs > 1 else table.shape[1],
+        lens.data_ptr(), max_len, window, cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), _ld(y),
+        wp, wn, _stream()))
+    return y
+
+
+def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
+            head_dim: int, pair_axis: Optional[Sequence[int]] = None, adjacent: bool = False,
+            out: Optional[Sequence[torch.Tensor]] = None):
+    """Rotary positions on every array of ``xs`` (fp16 [tokens][heads *
+    head_dim]) in one launch; ``cos``, ``sin`` fp32 [rows][rot / 2],
+    ``positions`` int32 [axes][tokens] (or [tokens]), ``pair_axis`` the axis
+    of each pair.  ``out`` may be ``xs`` itself (in place)."""
+    _dev(cos, torch.float32, "cos")
+    _dev(sin, torch.float32, "sin")
+    _dev(positions, torch.int32, "positions")
+    if cos.dim() != 2 or cos.shape != sin.shape:
+        raise ValueError(f"cos and sin must be [rows][rot / 2], got {tuple(cos.shape)} and {tuple(sin.shape)}")
+    rows, half = cos.shape
+    axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
+    if pair_axis is not None and len(pair_axis) != half:
+        raise ValueError(f"pair_axis: {len(pair_axis)} entries for {half} pairs")
+    ys = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs] if out is None else list(out)
+    if len(ys) != len(xs):
+        raise ValueError(f"out: {len(ys)} arrays for {len(xs)}")
+    for t in [*xs, *ys]:
+        _rows(t, t.shape[-1], "xs and out")
+        if t.shape[0] != tokens or t.shape[1] % head_dim:
+            raise ValueError(f"an array of {tuple(t.shape)} is not [{tokens}][heads * {head_dim}]")
+    if any(x.shape != y.shape for x, y in zip(xs, ys)):
+        raise ValueError("out must have the shapes of xs")
+    c = len(ys)
+    _check("wq_rope", lib().wq_rope(
+        c, (_vp * c)(*[x.data_ptr() for x in xs]), (_i64 * c)(*[_ld(x) for x in xs]),
+        (_vp * c)(*[y.data_ptr() for y in ys]), (_i64 * c)(*[_ld(y) for y in ys]),
+        (_i32 * c)(*[x.shape[1] // head_dim for x in xs]), tokens, head_dim, 2 * half, cos.data_ptr(),
+        sin.data_ptr(), rows, positions.data_ptr(), tokens, axes,
+        None if pair_axis is None else bytes(pair_axis), WQ_ROPE_ADJACENT if adjacent else 0, _stream()))
+    return ys
 
 
 def stream_read(src: torch.Tensor, sink: torch.Tensor, nbytes: Optional[int] = None) -> None:

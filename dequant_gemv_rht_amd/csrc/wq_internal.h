@@ -149,6 +149,47 @@ hipError_t launch_gemm_batch(int count, const wq_weight *w, const uint16_t *cons
                              int64_t m, void *const *y, const int *out_f32, const int64_t *ldy,
                              const int *ksplit, float *const *part, bool pair_order, hipStream_t s);
 
+// Paged key-value cache (kvcache.hip) and attention over it
+// (attn_decode.hip), rotary positions (rope.hip); checks in kv_api.cpp.
+hipError_t launch_kv_write(const wq_kv_cache &c, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                           const int32_t *slots, int64_t tokens, hipStream_t s);
+hipError_t launch_kv_read(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, uint16_t *k, int64_t ldk,
+                          uint16_t *v, int64_t ldv, hipStream_t s);
+
+struct AttnArgs {
+  const void *k, *v;
+  const uint32_t *k_params, *v_params;   // (scale, zero) fp16 pairs
+  const uint32_t *signs;
+  const uint16_t *q;
+  uint16_t *out;
+  const int32_t *table, *lens;
+  float *partial;               // workspace
+  int64_t ldq, ldo, ld_table;
+  int64_t seqs;
+  int32_t pages, kv_heads, group;   // group: query heads per key-value head
+  int32_t page_shift;
+  int32_t max_len, window;      // window 0: none
+  float scale;
+};
+size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window);
+hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, hipStream_t s);
+
+struct RopeArray {
+  const uint16_t *x;
+  uint16_t *y;
+  int64_t ldx, ldy;
+  int32_t heads;
+};
+struct RopeArgs {
+  RopeArray arr[kMaxBatch];
+  const float *cos, *sin;
+  const int32_t *positions;
+  int64_t ld_pos, tokens;
+  int32_t count, head_dim, rot, axes, table_rows, adjacent;
+  uint8_t pair_axis[128];       // axis of each pair
+};
+hipError_t launch_rope(const RopeArgs &a, hipStream_t s);
+
 }  // namespace wq
 
 // ---------------------------------------------------------------------------

@@ -295,6 +295,143 @@ wq_status wq_linear_batch_noalloc(int32_t count, const wq_weight *w,
 wq_status wq_embed(const wq_weight *w, const int32_t *ids, int64_t count, void *out,
                    wq_dtype out_dtype, int64_t ldo, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The attention side of a decoder block: a paged key-value cache in the
+ * library's code format, attention of one new token over it, and rotary
+ * positions.
+ *
+ * A cache holds the keys and values of one layer, in pages of page_size
+ * tokens; a page may belong to any sequence, and slot i is token
+ * i % page_size of page i / page_size.  A row is the head_dim values of one
+ * token and key-value head.  With bits 4 or 8 a row is integer codes with
+ * one fp16 scale and one fp16 zero point (the grouped-affine format of the
+ * weights, one group per row): value = (code - zero) * scale.  With bits 16
+ * it is fp16 values as given.
+ *
+ * With rht_signs the cache holds rotated rows R x, R the block-128 random
+ * Hadamard transform of rht_apply, one sign per key-value channel: an
+ * outlier channel is spread over 128 before it is coded.  R is orthogonal,
+ * so a rotated query meets rotated keys with the same score
+ * ((R q).(R k) = q.k), and the values' weighted sum is rotated back once.
+ * The calls below do all of this; callers never see a rotated row.
+ *
+ * Device arrays (U = units of a row: head_dim fp16 values, head_dim bytes
+ * for 8 bits, head_dim / 2 bytes for 4 bits, where a byte holds channels 2i
+ * (low half) and 2i + 1):
+ *  - k: [pages][kv_heads][page_size * U units].  In a page and head, blocks
+ *    of 16 tokens; a block is its rows cut into panels of P = min(U, 64
+ *    bytes): unit u of the block's token t is at (u / P) * 16 P + t P +
+ *    u % P.
+ *  - v: the same size; in a page and head, quads of 4 tokens, a quad's
+ *    units with the four tokens side by side: unit u of the quad's token t
+ *    is at 4 u + t.
+ *  - k_params, v_params: fp16 [pages][kv_heads][page_size][2], a row's
+ *    scale and zero (not read or written for 16 bits; may be NULL).
+ * The layouts hand the attention kernel's matrix instructions their
+ * operands in whole 16-byte loads.  int32 arrays (slots, tables, lengths,
+ * positions) need 4-byte alignment only. */
+typedef struct wq_kv_cache {
+  int32_t bits;                 /* 4, 8 or 16 */
+  int32_t head_dim;             /* 64, 128 or 256 */
+  int32_t kv_heads;
+  int32_t page_size;            /* a power of two, at least 16 */
+  int64_t pages;                /* pages * page_size at most 2^31 - 1 */
+  void *k, *v;
+  uint16_t *k_params, *v_params;
+  const uint32_t *rht_signs;    /* [kv_heads * head_dim / 32] sign bits, or NULL for no rotation */
+  int32_t rht_block;            /* 128 when rht_signs != NULL (head_dim a multiple of it), else 0 */
+} wq_kv_cache;
+
+/* Store new tokens' keys and values in the cache, coded as they are written:
+ *   x' = R x in fp32 (x itself without rht_signs),
+ *   lo = min(min x', 0), hi = max(max x', 0),
+ *   scale = fp16(min((hi - lo) / qmax, 65504)) (1 if that is 0),
+ *   zero = clamp(rint(-lo / scale), 0, qmax),
+ *   code = clamp(rint(x' / scale + zero), 0, qmax),
+ * in fp32 with rint rounding half to even, qmax = 2^bits - 1 (wq_quantize's
+ * rule, in single precision).  bits 16: fp16(x').
+ *   k, v   fp16 [tokens][ldk], [tokens][ldv]: kv_heads rows of head_dim
+ *   slots  device int32 [tokens]: where each token goes.  A slot outside
+ *          [0, pages * page_size) skips its token.  Two tokens with one slot
+ *          in one call leave an unspecified mix of both there.
+ * A row that holds an infinity or a NaN is stored with unspecified codes
+ * (8 and 4 bits); other rows are not affected.  tokens 0 does nothing.
+ * Errors: WQ_E_ARG (NULL pointer, tokens < 0, ldk or ldv < kv_heads *
+ * head_dim, a bad cache descriptor), WQ_E_ALIGN (also ldk, ldv not a
+ * multiple of 8), WQ_E_UNSUPPORTED (bits, head_dim, page_size or rht_block
+ * not supported, tokens above 2^31 - 1, sizes past 2^31 - 1), WQ_E_HIP. */
+wq_status wq_kv_write(const wq_kv_cache *cache, const uint16_t *k, int64_t ldk, const uint16_t *v,
+                      int64_t ldv, const int32_t *slots, int64_t tokens, void *stream);
+
+/* Cached rows back as fp16: x = fp16(R^T x'), x' = (code - zero) * scale,
+ * for the tokens in `slots` (a slot outside the cache gives zeros).
+ *   k, v   out: fp16 [tokens][ldk], [tokens][ldv]; columns past kv_heads *
+ *          head_dim are not written
+ * Errors as for wq_kv_write. */
+wq_status wq_kv_read(const wq_kv_cache *cache, const int32_t *slots, int64_t tokens, uint16_t *k,
+                     int64_t ldk, uint16_t *v, int64_t ldv, void *stream);
+
+/* Attention of one new token per sequence over its cached tokens:
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . key_t) value_t
+ * over positions t of sequence b: 0 <= t < lens[b], and with window > 0
+ * only the last `window` of them.  Query head h uses key-value head
+ * h / (q_heads / kv_heads).  Position t is token t % page_size of page
+ * table[b][t / page_size].  The new token's own key and value are expected
+ * in the cache already (wq_kv_write first, lens counting it).  Scores,
+ * softmax and sums are fp32; the queries (rotated where the cache is) and
+ * the softmax weights enter the products as fp16.
+ *   q        fp16 [seqs][ldq]: q_heads rows of head_dim; q_heads a multiple
+ *            of kv_heads
+ *   table    device int32 [seqs][ld_table] page numbers; only entries of
+ *            attended positions are read.  A page outside [0, pages) takes
+ *            no part: its positions count as masked.
+ *   lens     device int32 [seqs].  A length above max_len counts as
+ *            max_len; a sequence with nothing to attend to (length 0 or
+ *            less, or only pages that take no part) gives zeros.
+ *   max_len  an upper bound of the lengths known on the host: it sizes the
+ *            launch and the workspace; at most ld_table * page_size
+ *   out      fp16 [seqs][ldo]
+ *   workspace  device scratch of wq_attn_decode_workspace bytes (partial
+ *            results where a sequence is split over workgroups; NULL when
+ *            that is 0); no initialisation needed, contents not preserved
+ * What is stored past a sequence's length, NaN and infinity included, never
+ * reaches its output.  Results do not depend on timing: the same inputs
+ * give the same bits.  seqs 0 does nothing.
+ * Errors (before anything is launched): WQ_E_ARG, WQ_E_ALIGN (ldq, ldo not
+ * a multiple of 8), WQ_E_UNSUPPORTED (as above; seqs * heads past 2^31 - 1),
+ * WQ_E_WORKSPACE; WQ_E_HIP. */
+size_t wq_attn_decode_workspace(const wq_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_len,
+                                int64_t window);
+wq_status wq_attn_decode(const wq_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads,
+                         int64_t seqs, const int32_t *table, int64_t ld_table, const int32_t *lens,
+                         int64_t max_len, int64_t window, float scale, uint16_t *out, int64_t ldo,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Rotary positions, on up to WQ_MAX_BATCH arrays (queries and keys) in one
+ * launch.  A head's first `rot` channels form rot / 2 pairs; pair i is
+ * channels (i, i + rot / 2), or (2 i, 2 i + 1) with WQ_ROPE_ADJACENT, and
+ *   (a, b) -> (a c - b s, b c + a s),  c = cos[p][i], s = sin[p][i],
+ * in fp32, rounded once to fp16, at the position p of the token on the
+ * pair's axis.  Channels from `rot` on are copied.  One axis is text; with
+ * several (time, height, width) pair_axis deals the pairs to them in any
+ * order.
+ *   x, y       fp16 [tokens][ldx[i]], [tokens][ldy[i]], heads[i] rows of
+ *              head_dim; y[i] may equal x[i] (in place) when ldy == ldx
+ *   cos, sin   device fp32 [table_rows][rot / 2], one entry per position
+ *              and pair (any base or scaling rule is the caller's)
+ *   positions  device int32 [axes][ld_pos]; a position outside
+ *              [0, table_rows) leaves its pairs unchanged
+ *   pair_axis  HOST uint8 [rot / 2], each below axes, read during the call
+ *              only; NULL: every pair on axis 0
+ * head_dim a multiple of 8 up to 256, rot a multiple of 16 up to head_dim,
+ * axes 1 to 4.  Errors as above. */
+#define WQ_ROPE_ADJACENT 1u
+#define WQ_ROPE_MAX_AXES 4
+wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, uint16_t *const *y,
+                  const int64_t *ldy, const int32_t *heads, int64_t tokens, int32_t head_dim, int32_t rot,
+                  const float *cos, const float *sin, int64_t table_rows, const int32_t *positions,
+                  int64_t ld_pos, int32_t axes, const uint8_t *pair_axis, uint32_t flags, void *stream);
+
 /* Message for the last failed call on this thread ("" if none). */
 const char *wq_last_error(void);
 

@@ -29,8 +29,9 @@ Modules:
   pack      - bit placement of codes into 32-bit words (uniform and mixed)
   linear    - dequantisation and the plain triple-loop contraction (C)
   embed     - rows of a quantised table, dequantised (tied-embedding gather)
+  kvcache   - paged key-value cache, attention of one new token, rotary positions
 
 Every function carries a pin in ``tests/test_oracle_*.py``.
 """
 
-from . import hadamard, rtn, pack, linear, embed  # noqa: F401
+from . import hadamard, rtn, pack, linear, embed, kvcache  # noqa: F401
