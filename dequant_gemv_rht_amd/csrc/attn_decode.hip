@@ -1,9 +1,33 @@
 // Attention of one new token per sequence over a paged, coded key-value
 // cache (gfx950):  out = R^T sum_t softmax_t(scale (R q).k_t) v_t.
 //
-// One workgroup per (sequence, query head), 256 tokens at a time: a thread
-// scores one token, the tile's largest score and sum update the running
-// softmax (m, l), and thread d adds up channel d of the values.
+// A workgroup takes one (sequence, key-value head) and a run of its tokens
+// (a split); its four waves take 32 tokens at a time in turn, each with its
+// own running softmax, and join in LDS at the end.  Where a sequence has
+// more than one split, the splits' sums go to the workspace and a second
+// kernel joins them.
+//
+// Both products run on the matrix cores with the tokens' side as the first
+// operand, so that the query heads that share the key-value head (padded to
+// 16) are the columns everywhere:
+//   S^T = K Q^T   16 tokens x 16 heads per v_mfma_f32_16x16x32_f16
+//   O^T = V^T P^T 16 channels x 16 heads, 32 tokens deep
+// A lane then holds scores of one head (its column) for tokens 4 g + i of
+// each 16 (g = lane / 16), which is what the second product wants of P as
+// its own operand, in the token order {4 g + i, 16 + 4 g + i}: the weights
+// never leave their lane.  The cache's layout gives V in that order (quads
+// of tokens side by side) and K as panels, both in whole 16-byte loads.
+//
+// Codes become fp16 by placing them in the significand of 1024 (0x6400 | c)
+// and subtracting: c - 8 or c - 128 for keys, c - zero for values, all
+// exact.  The keys' scale and zero are applied to the score in fp32:
+//   s (dot(q, c - mid) + (mid - z) sum(q)).
+// The values' scale goes into the weight, p s, before it is rounded to
+// fp16; the running reference m therefore tracks max(u + log2 s), so that
+// p s of the largest term stays near 2^kGain and weights down to 2^-20 of
+// it keep fp16's 11 bits whatever the scales are.  m moves only when a term
+// exceeds 2^kSlack above it, which after the first steps is rare: the
+// cross-lane maximum and the rescaling of the sums run only then.
 #include "wq_internal.h"
 
 #include <cmath>
@@ -13,145 +37,546 @@ using namespace dev;
 
 namespace {
 
-constexpr int kAttnThreads = 256;
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef const __attribute__((address_space(4))) int32_t *const_i32;   // scalar loads
+
+constexpr int kAttnThreads = 256, kWaves = 4;
+constexpr int kStep = 32;            // tokens per wave and step
+constexpr int kMinSplit = kWaves * kStep;
+constexpr int kMaxSplit = 2048;
+constexpr float kInvSqrt128 = 0.08838834764831845f;
+constexpr float kNone = -1e30f;      // no term seen yet
+constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
 
 template <int BITS, int D>
-__device__ __forceinline__ float code_at(const void *base, int64_t unit, int ch) {
-  if constexpr (BITS == 16) return half_bits_to_float(static_cast<const uint16_t *>(base)[unit]);
-  const uint32_t b = static_cast<const uint8_t *>(base)[unit];
-  return (float)(BITS == 4 ? (b >> (4 * (ch & 1))) & 15u : b);
+struct Fmt {
+  static constexpr int kRow = D * BITS / 8;        // bytes of a row
+  static constexpr int kWords = kRow / 16;         // 32-bit words a lane holds of 16 tokens (keys; values)
+  static constexpr int kPiece = kWords < 4 ? kWords : 4;   // words per load
+  static constexpr int kKeyMfma = D / 32, kOutMfma = D / 16;
+  static constexpr int kMid = BITS == 8 ? 128 : 8;
+  // first of the 8 channels of key operand m in lane group g
+  __device__ static constexpr int key_channel(int m, int g) {
+    if (BITS == 16) return 32 * m + 8 * g;
+    if (BITS == 8) return 64 * (m >> 1) + 16 * g + 8 * (m & 1);
+    return D == 64 ? 16 * g + 8 * m : 128 * (m >> 2) + 32 * g + 8 * (m & 3);
+  }
+  // the channel of output row r = 4 g + i of product n
+  __device__ static constexpr int out_channel(int n, int r) {
+    if (BITS == 16) return 32 * (n >> 1) + 2 * r + (n & 1);
+    if (BITS == 8) return 64 * (n >> 2) + 4 * r + (n & 3);
+    return D == 64 ? 4 * r + n : 128 * (n >> 3) + 8 * r + (n & 7);
+  }
+};
+
+template <int BITS, int D>
+struct Step {
+  uint32_t k[2][Fmt<BITS, D>::kWords], v[2][Fmt<BITS, D>::kWords];
+  u32x4 kp[2], vp[2];
+};
+
+__device__ __forceinline__ half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
+__device__ __forceinline__ uint32_t as_u32(half2_t h) { return __builtin_bit_cast(uint32_t, h); }
+__device__ __forceinline__ half2_t both(float v) { return half2_t{(_Float16)v, (_Float16)v}; }
+
+struct Quad {
+  uint32_t w[4];
+};
+__device__ __forceinline__ half8_t as_half8(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(half8_t, Quad{{a, b, c, d}});
+}
+
+// two 8-bit codes -> 1024 + code
+__device__ __forceinline__ half2_t bytes01(uint32_t w) {
+  return as_half2(__builtin_amdgcn_perm(0x64646464u, w, 0x04010400u));
+}
+__device__ __forceinline__ half2_t bytes23(uint32_t w) {
+  return as_half2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u));
+}
+// 4-bit codes at bits 0 and 16 -> 1024 + code; at bits 4 and 20 -> 1024 + 16 code
+__device__ __forceinline__ half2_t low_nibbles(uint32_t w) { return as_half2((w & 0x000F000Fu) | 0x64006400u); }
+__device__ __forceinline__ half2_t high_nibbles(uint32_t w) { return as_half2((w & 0x00F000F0u) | 0x64006400u); }
+
+// key operand m of a block
+template <int BITS, int D>
+__device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>::kWords], int m) {
+  if constexpr (BITS == 16) {
+    return as_half8(k[4 * m], k[4 * m + 1], k[4 * m + 2], k[4 * m + 3]);
+  } else if constexpr (BITS == 8) {
+    const half2_t c = both(1024.0f + 128.0f);
+    return as_half8(as_u32(bytes01(k[2 * m]) - c), as_u32(bytes23(k[2 * m]) - c), as_u32(bytes01(k[2 * m + 1]) - c),
+                    as_u32(bytes23(k[2 * m + 1]) - c));
+  } else {
+    // channel order 0, 4, 1, 5, 2, 6, 3, 7
+    const half2_t c = both(1024.0f + 8.0f), d = both(-(64.0f + 8.0f)), f = both(0.0625f);
+    const uint32_t w = k[m], x = w >> 8;
+    return as_half8(as_u32(low_nibbles(w) - c), as_u32(__builtin_elementwise_fma(high_nibbles(w), f, d)),
+                    as_u32(low_nibbles(x) - c), as_u32(__builtin_elementwise_fma(high_nibbles(x), f, d)));
+  }
+}
+
+// A maximum over the four lanes that share a column (head).
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+__device__ __forceinline__ float column_sum(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+struct SplitPlan {
+  int32_t splits, split_len, qtiles;
+};
+
+// One row's 8 channels in a 16-lane DPP row, rotated back and stored.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[8], int64_t seq, int kvh, int head, int c0) {
+  if (D >= 128 && a.signs) {
+    const int jj = threadIdx.x & 15;
+    fwht128_row16_signed(v, jj);
+    const int ch = kvh * D + c0;
+    const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
+    const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= ((sb >> e) & 1u) ? -sc : sc;
+  }
+  *reinterpret_cast<uint4 *>(a.out + seq * a.ldo + (int64_t)head * D + c0) =
+      make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+}
+
+// The positions a sequence attends to, from the last 16-token boundary at
+// or before the first one.
+struct Range {
+  int start, begin, len;
+  __device__ int splits(int split_len) const { return len > begin ? (len - begin + split_len - 1) / split_len : 0; }
+};
+__device__ __forceinline__ Range range_of(const AttnArgs &a, int64_t seq) {
+  Range r;
+  r.len = min(((const_i32)a.lens)[seq], a.max_len);
+  r.start = a.window && r.len > a.window ? r.len - a.window : 0;
+  r.begin = r.start & ~15;
+  return r;
 }
 
 template <int BITS, int D>
-__global__ __launch_bounds__(kAttnThreads) void attn_simple_kernel(AttnArgs a) {
-  constexpr int U = BITS == 4 ? D / 2 : D, P = BITS == 16 ? 32 : (U < 64 ? U : 64);
-  constexpr float kMasked = -INFINITY;
-  __shared__ float qs[D], prob[kAttnThreads], red[kAttnThreads];
-  __shared__ int32_t page_of[kAttnThreads];
-  const int heads = a.kv_heads * a.group;
-  const int head = blockIdx.x % heads, kvh = head / a.group;
-  const int64_t seq = blockIdx.x / heads;
-  const int tid = threadIdx.x;
-  const int len = min(a.lens[seq], a.max_len);
-  const int start = a.window && len > a.window ? len - a.window : 0;
-  // the query, rotated as the cache is, rounded to fp16
-  if (tid < D / 8) {
-    const uint16_t *q = a.q + seq * a.ldq + (int64_t)head * D + 8 * tid;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = half_bits_to_float(q[e]);
+__global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a, SplitPlan plan) {
+  using F = Fmt<BITS, D>;
+  constexpr int kQStride = D + 8, kOStride = D + 4;
+  __shared__ union {
+    _Float16 q[16][kQStride];
+    float o[kWaves][16][kOStride];
+  } sh;
+  __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
+
+  int id = blockIdx.x;
+  const int split = id % plan.splits;
+  id /= plan.splits;
+  const int qt = id % plan.qtiles;
+  id /= plan.qtiles;
+  const int kvh = id % a.kv_heads;
+  const int64_t seq = id / a.kv_heads;
+  const Range rg = range_of(a, seq);
+  const int my_splits = rg.splits(plan.split_len);
+  if (split >= my_splits && split > 0) return;
+  const int begin = rg.begin + split * plan.split_len;
+  const int end = min(begin + plan.split_len, rg.len);   // at or below begin: nothing to attend to
+  const int head0 = kvh * a.group + 16 * qt, heads = min(16, a.group - 16 * qt);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, g = lane >> 4;
+
+  // the queries: rotated as the cache is, rounded to fp16, in the keys' channel order
+  for (int i = tid; i < 16 * (D / 8); i += kAttnThreads) {
+    const int h = i / (D / 8), c0 = 8 * (i % (D / 8));
+    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (h < heads) {
+      const uint4 raw = *reinterpret_cast<const uint4 *>(a.q + seq * a.ldq + (int64_t)(head0 + h) * D + c0);
+      v[0] = half_bits_to_float(raw.x & 0xFFFF); v[1] = half_bits_to_float(raw.x >> 16);
+      v[2] = half_bits_to_float(raw.y & 0xFFFF); v[3] = half_bits_to_float(raw.y >> 16);
+      v[4] = half_bits_to_float(raw.z & 0xFFFF); v[5] = half_bits_to_float(raw.z >> 16);
+      v[6] = half_bits_to_float(raw.w & 0xFFFF); v[7] = half_bits_to_float(raw.w >> 16);
+    }
     if (D >= 128 && a.signs) {
-      const int ch = kvh * D + 8 * tid;
+      const int ch = kvh * D + c0, jj = tid & 15;
       const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = ((sb >> e) & 1u) ? -v[e] : v[e];
-      fwht128_row16_signed(v, tid & 15);
+      fwht128_row16_signed(v, jj);
+      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= fwht_lane_sign(tid & 15) * 0.08838834764831845f;
+      for (int e = 0; e < 8; ++e) v[e] *= sc;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) qs[8 * tid + e] = (float)(_Float16)v[e];
+    uint4 w;
+    if (BITS == 4)
+      w = make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]), pack_half2(v[3], v[7]));
+    else
+      w = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(&sh.q[h][c0]) = w;
   }
-  float m = kMasked, l = 0.0f, acc = 0.0f;
-  const int mask = (1 << a.page_shift) - 1;
-  for (int t0 = start; t0 < len; t0 += kAttnThreads) {
-    __syncthreads();
-    const int t = t0 + tid;
-    float score = kMasked;
-    int32_t page = -1;
-    if (t < len) {
-      page = a.table[seq * a.ld_table + (t >> a.page_shift)];
-      if (page < 0 || page >= a.pages) page = -1;
-    }
-    page_of[tid] = page;
-    const int64_t ph = (int64_t)page * a.kv_heads + kvh;
-    if (page >= 0) {
-      const int at = t & mask;
-      const int64_t base = ph * ((int64_t)U << a.page_shift) + (int64_t)(at >> 4) * 16 * U + (at & 15) * P;
-      float s = 1.0f, z = 0.0f;
-      if (BITS != 16) {
-        const uint32_t par = a.k_params[(ph << a.page_shift) + at];
-        s = half_bits_to_float(par & 0xFFFF);
-        z = half_bits_to_float(par >> 16);
-      }
-      float dot = 0.0f;
-      for (int d = 0; d < D; ++d) {
-        const int u = BITS == 4 ? d / 2 : d;
-        dot += qs[d] * (code_at<BITS, D>(a.k, base + (u / P) * 16 * P + u % P, d) - z);
-      }
-      score = dot * s * a.scale;
-    }
-    red[tid] = score;
-    __syncthreads();
-    for (int o = kAttnThreads / 2; o; o >>= 1) {
-      if (tid < o) red[tid] = fmaxf(red[tid], red[tid + o]);
-      __syncthreads();
-    }
-    const float top = fmaxf(m, red[0]);
-    __syncthreads();
-    const float p = page >= 0 ? __expf(score - top) : 0.0f;
-    prob[tid] = p;
-    red[tid] = p;
-    __syncthreads();
-    for (int o = kAttnThreads / 2; o; o >>= 1) {
-      if (tid < o) red[tid] += red[tid + o];
-      __syncthreads();
-    }
-    const float keep = m == kMasked ? 0.0f : __expf(m - top);
-    l = l * keep + red[0];
-    m = top;
-    acc *= keep;
-    if (tid < D) {
-      const int n = min(kAttnThreads, len - t0);
-      for (int i = 0; i < n; ++i) {
-        if (page_of[i] < 0) continue;
-        const int at = (t0 + i) & mask;
-        const int64_t ph2 = (int64_t)page_of[i] * a.kv_heads + kvh;
-        const int u = BITS == 4 ? tid / 2 : tid;
-        float v = code_at<BITS, D>(a.v, ph2 * ((int64_t)U << a.page_shift) + (int64_t)(at >> 2) * 4 * U + 4 * u + (at & 3), tid);
-        if (BITS != 16) {
-          const uint32_t par = a.v_params[(ph2 << a.page_shift) + at];
-          v = (v - half_bits_to_float(par >> 16)) * half_bits_to_float(par & 0xFFFF);
+  __syncthreads();
+  half8_t q[F::kKeyMfma];
+  float qsum = 0.0f;
+#pragma unroll
+  for (int m = 0; m < F::kKeyMfma; ++m) {
+    q[m] = *reinterpret_cast<const half8_t *>(&sh.q[col][F::key_channel(m, g)]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) qsum += (float)q[m][e];
+  }
+  qsum = column_sum(qsum);
+  __syncthreads();   // sh.q is free for sh.o
+
+  const float to_log2 = a.scale * 1.4426950408889634f;
+  float m = kNone, l = 0.0f;
+  f32x4 o[F::kOutMfma];
+#pragma unroll
+  for (int n = 0; n < F::kOutMfma; ++n) o[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  const_i32 table = (const_i32)(a.table + seq * a.ld_table);
+  const int page_mask = (1 << a.page_shift) - 1;
+  // page of the 16 tokens from t; -1: none of them takes part
+  auto page_at = [&](int t) -> int {
+    if (t >= end) return -1;
+    const int p = table[t >> a.page_shift];
+    return (uint32_t)p < (uint32_t)a.pages ? p : -1;
+  };
+  const char *kbase = static_cast<const char *>(a.k), *vbase = static_cast<const char *>(a.v);
+  const uint32_t k_lane = F::kRow >= 64 ? col * 64 + g * 16 : col * 32 + g * 8;
+  const uint32_t v_lane = g * 4 * F::kRow + col * 4 * F::kPiece;
+  auto load = [&](Step<BITS, D> &s, int t, int p0, int p1) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int p = max(b ? p1 : p0, 0);   // a page that takes no part: page 0, masked
+      const int64_t token = (((int64_t)p * a.kv_heads + kvh) << a.page_shift) + ((t + 16 * b) & page_mask);
+      const char *kb = kbase + token * F::kRow, *vb = vbase + token * F::kRow;
+#pragma unroll
+      for (int i = 0; i < F::kWords / F::kPiece; ++i) {
+        if constexpr (F::kPiece == 4) {
+          const u32x4 kw = *reinterpret_cast<const u32x4 *>(kb + (k_lane + i * 1024));
+          const u32x4 vw = *reinterpret_cast<const u32x4 *>(vb + (v_lane + i * 256));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s.k[b][4 * i + e] = kw[e];
+            s.v[b][4 * i + e] = vw[e];
+          }
+        } else {
+          const u32x2 kw = *reinterpret_cast<const u32x2 *>(kb + k_lane);
+          const u32x2 vw = *reinterpret_cast<const u32x2 *>(vb + v_lane);
+          s.k[b][0] = kw[0]; s.k[b][1] = kw[1];
+          s.v[b][0] = vw[0]; s.v[b][1] = vw[1];
         }
-        acc += prob[i] * v;
+      }
+      if constexpr (BITS != 16) {
+        s.kp[b] = *reinterpret_cast<const u32x4 *>(a.k_params + token + 4 * g);
+        s.vp[b] = *reinterpret_cast<const u32x4 *>(a.v_params + token + 4 * g);
+      }
+    }
+  };
+
+  auto compute = [&](Step<BITS, D> &s, int t, int p0, int p1) {
+    // scores, in units of log2
+    float u[8];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+      if constexpr (BITS != 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = ((float)F::kMid - half_bits_to_float(s.kp[b][i] >> 16)) * qsum;
+      }
+#pragma unroll
+      for (int mm = 0; mm < F::kKeyMfma; ++mm)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(s.k[b], mm), q[mm], acc, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        u[4 * b + i] = acc[i] * (BITS == 16 ? to_log2 : half_bits_to_float(s.kp[b][i] & 0xFFFF) * to_log2);
+    }
+    // the first and the last step of a sequence, pages outside the cache
+    if (t < rg.start || t + kStep > end || p0 < 0 || p1 < 0) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        bool ok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = t + 16 * b + 4 * g + i;
+          ok[i] = at >= rg.start && at < end && (b ? p1 : p0) >= 0;
+          u[4 * b + i] = ok[i] ? u[4 * b + i] : -INFINITY;
+          if (BITS != 16) s.vp[b][i] = ok[i] ? s.vp[b][i] : 0u;   // scale and zero 0
+        }
+        if constexpr (BITS == 16) {
+          const uint32_t lo = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
+          const uint32_t hi = (ok[2] ? 0xFFFFu : 0u) | (ok[3] ? 0xFFFF0000u : 0u);
+#pragma unroll
+          for (int i = 0; i < F::kWords; ++i) s.v[b][i] &= (i & 1) ? hi : lo;
+        }
+      }
+    }
+    float vs[8], p[8], w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      vs[i] = BITS == 16 ? (float)(1 << kGain) : half_bits_to_float(s.vp[i >> 2][i & 3] & 0xFFFF) * (float)(1 << kGain);
+      p[i] = __builtin_amdgcn_exp2f(u[i] - m);
+      w[i] = p[i] * vs[i];
+    }
+    float top = w[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) top = fmaxf(top, w[i]);
+    if (__any(!(top <= (float)(1 << (kGain + kSlack))))) {
+      // move the reference to the largest term so far (2^-24: the smallest
+      // positive scale, so that rows of scale 0 do not leave it unset)
+      float high = m;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        high = fmaxf(high, u[i] + (BITS == 16 ? 0.0f : fmaxf(__builtin_amdgcn_logf(vs[i]) - (float)kGain, -24.0f)));
+      high = column_max(high);
+      const float keep = __builtin_amdgcn_exp2f(m - high);
+      m = high;
+      l *= keep;
+#pragma unroll
+      for (int n = 0; n < F::kOutMfma; ++n) o[n] *= keep;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(u[i] - m);
+        w[i] = p[i] * vs[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l += p[i];
+    // weights as the second operand, in the values' token order: 4-bit
+    // codes of tokens 0, 2 and 1, 3 come out of a word together
+    constexpr int o1 = BITS == 4 ? 2 : 1, o2 = BITS == 4 ? 1 : 2;
+    const half8_t pw = as_half8(pack_half2(w[0], w[o1]), pack_half2(w[o2], w[3]), pack_half2(w[4], w[4 + o1]),
+                                pack_half2(w[4 + o2], w[7]));
+    half2_t z[2][2];
+    if constexpr (BITS != 16) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        z[b][0] = as_half2(__builtin_amdgcn_perm(s.vp[b][o1], s.vp[b][0], 0x07060302u));
+        z[b][1] = as_half2(__builtin_amdgcn_perm(s.vp[b][3], s.vp[b][o2], 0x07060302u));
+      }
+    }
+    if constexpr (BITS == 16) {
+#pragma unroll
+      for (int n = 0; n < F::kOutMfma; ++n)
+        o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            as_half8(s.v[0][2 * n], s.v[0][2 * n + 1], s.v[1][2 * n], s.v[1][2 * n + 1]), pw, o[n], 0, 0, 0);
+    } else if constexpr (BITS == 8) {
+      half2_t c[2][2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i >> 1][i & 1] = z[i >> 1][i & 1] + both(1024.0f);
+#pragma unroll
+      for (int n = 0; n < F::kOutMfma; ++n)
+        o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            as_half8(as_u32(bytes01(s.v[0][n]) - c[0][0]), as_u32(bytes23(s.v[0][n]) - c[0][1]),
+                     as_u32(bytes01(s.v[1][n]) - c[1][0]), as_u32(bytes23(s.v[1][n]) - c[1][1])),
+            pw, o[n], 0, 0, 0);
+    } else {
+      half2_t c[2][2], d[2][2];
+      const half2_t f = both(0.0625f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i >> 1][i & 1] = z[i >> 1][i & 1] + both(1024.0f);
+        d[i >> 1][i & 1] = -(z[i >> 1][i & 1] + both(64.0f));
+      }
+#pragma unroll
+      for (int n = 0; n < F::kOutMfma; n += 2) {
+        const uint32_t a0 = s.v[0][n / 2], a1 = a0 >> 8, b0 = s.v[1][n / 2], b1 = b0 >> 8;
+        o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            as_half8(as_u32(low_nibbles(a0) - c[0][0]), as_u32(low_nibbles(a1) - c[0][1]),
+                     as_u32(low_nibbles(b0) - c[1][0]), as_u32(low_nibbles(b1) - c[1][1])),
+            pw, o[n], 0, 0, 0);
+        o[n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+            as_half8(as_u32(__builtin_elementwise_fma(high_nibbles(a0), f, d[0][0])),
+                     as_u32(__builtin_elementwise_fma(high_nibbles(a1), f, d[0][1])),
+                     as_u32(__builtin_elementwise_fma(high_nibbles(b0), f, d[1][0])),
+                     as_u32(__builtin_elementwise_fma(high_nibbles(b1), f, d[1][1]))),
+            pw, o[n + 1], 0, 0, 0);
+      }
+    }
+  };
+
+  constexpr int kStride = kWaves * kStep;
+  int t = begin + wave * kStep;
+  if (t < end) {
+    Step<BITS, D> s0, s1;
+    int p0 = page_at(t), p1 = page_at(t + 16);
+    load(s0, t, p0, p1);
+    int n0 = page_at(t + kStride), n1 = page_at(t + kStride + 16);
+    for (;;) {
+      const bool more = t + kStride < end;
+      if (more) load(s1, t + kStride, n0, n1);
+      const int f0 = page_at(t + 2 * kStride), f1 = page_at(t + 2 * kStride + 16);
+      compute(s0, t, p0, p1);
+      if (!more) break;
+      t += kStride;
+      const bool more2 = t + kStride < end;
+      if (more2) load(s0, t + kStride, f0, f1);
+      const int h0 = page_at(t + 2 * kStride), h1 = page_at(t + 2 * kStride + 16);
+      compute(s1, t, n0, n1);
+      if (!more2) break;
+      t += kStride;
+      p0 = f0; p1 = f1;
+      n0 = h0; n1 = h1;
+    }
+  }
+
+  // join the four waves
+  l = column_sum(l);
+  if (g == 0) {
+    sh_m[wave][col] = m;
+    sh_l[wave][col] = l;
+  }
+  if (col < heads) {
+#pragma unroll
+    for (int n = 0; n < F::kOutMfma; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sh.o[wave][col][F::out_channel(n, 4 * g + i)] = o[n][i];
+  }
+  __syncthreads();
+  for (int i = tid; i < heads * (D / 8); i += kAttnThreads) {
+    const int h = i / (D / 8), c0 = 8 * (i % (D / 8)), head = head0 + h;
+    float high = sh_m[0][h];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) high = fmaxf(high, sh_m[w][h]);
+    float total = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(sh_m[w][h] - high);
+      total += f * sh_l[w][h];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += f * sh.o[w][h][c0 + e];
+    }
+    if (my_splits <= 1) {
+      const float inv = total > 0.0f || total != total ? (1.0f / (1 << kGain)) / total : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= inv;
+      store_row<D>(a, v, seq, kvh, head, c0);
+    } else {
+      const int64_t at = ((seq * a.kv_heads * a.group + head) * plan.splits + split);
+      float *part = a.partial + at * (D + 4);
+      f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+      *reinterpret_cast<f32x4 *>(part + 4 + c0) = lo;
+      *reinterpret_cast<f32x4 *>(part + 8 + c0) = hi;
+      if (c0 == 0) {
+        part[0] = high;
+        part[1] = total;
       }
     }
   }
-  __syncthreads();
-  if (tid < D) qs[tid] = l > 0.0f ? acc / l : 0.0f;
-  __syncthreads();
-  if (tid < D / 8) {
-    float v[8];
+}
+
+// Joins the splits of one (sequence, head): D / 8 lanes x 8 channels, the
+// other threads share the splits out.
+template <int D>
+__global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, SplitPlan plan) {
+  constexpr int kLanes = D / 8, kParts = kAttnThreads / kLanes;
+  __shared__ float sh[kParts][D + 4], sh_m[kParts], sh_l[kParts];
+  const int all = a.kv_heads * a.group;
+  const int head = blockIdx.x % all;
+  const int64_t seq = blockIdx.x / all;
+  const int n = range_of(a, seq).splits(plan.split_len);
+  if (n <= 1) return;   // written by its one workgroup
+  const int tid = threadIdx.x, part = tid / kLanes, c0 = 8 * (tid % kLanes);
+  const float *in = a.partial + (int64_t)blockIdx.x * plan.splits * (D + 4);
+  float m = kNone, l = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = part; s < n; s += kParts) {
+    const float *p = in + (int64_t)s * (D + 4);
+    const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + 4 + c0), hi = *reinterpret_cast<const f32x4 *>(p + 8 + c0);
+    const float ms = p[0], ls = p[1];
+    const float high = fmaxf(m, ms);
+    const float f = __builtin_amdgcn_exp2f(m - high), fs = __builtin_amdgcn_exp2f(ms - high);
+    m = high;
+    l = l * f + ls * fs;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = qs[8 * tid + e];
-    if (D >= 128 && a.signs) {
-      fwht128_row16_signed(v, tid & 15);
-      const int ch = kvh * D + 8 * tid;
-      const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
-      const float sc = fwht_lane_sign(tid & 15) * 0.08838834764831845f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= ((sb >> e) & 1u) ? -sc : sc;
+    for (int e = 0; e < 4; ++e) {
+      v[e] = v[e] * f + lo[e] * fs;
+      v[e + 4] = v[e + 4] * f + hi[e] * fs;
     }
-    *reinterpret_cast<uint4 *>(a.out + seq * a.ldo + (int64_t)head * D + 8 * tid) = make_uint4(
-        pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
   }
+  if (c0 == 0) {
+    sh_m[part] = m;
+    sh_l[part] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sh[part][c0 + e] = v[e];
+  __syncthreads();
+  if (tid >= kLanes) return;
+  float high = kNone, total = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  const int used = min(n, kParts);
+  for (int i = 0; i < used; ++i) high = fmaxf(high, sh_m[i]);
+  for (int i = 0; i < used; ++i) {
+    const float f = __builtin_amdgcn_exp2f(sh_m[i] - high);
+    total += f * sh_l[i];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += f * sh[i][c0 + e];
+  }
+  const float inv = total > 0.0f || total != total ? (1.0f / (1 << kGain)) / total : 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= inv;
+  store_row<D>(a, v, seq, head / a.group, head, c0);
+}
+
+constexpr int64_t kWorkgroups = 512;   // two a CU
+
+int64_t seen_at_most(int64_t max_len, int64_t window) {
+  return window > 0 && window + 15 < max_len ? window + 15 : max_len;
+}
+
+// How a call is split: enough workgroups to fill the card, runs of at most
+// kMaxSplit tokens so that one long sequence among short ones is shared out.
+SplitPlan plan_for(int64_t seqs, int kv_heads, int group, int64_t max_len, int64_t window) {
+  SplitPlan p;
+  p.qtiles = (group + 15) / 16;
+  const int64_t seen = seen_at_most(max_len, window);
+  const int64_t units = seqs * kv_heads * p.qtiles;
+  const int64_t want = (kWorkgroups + units - 1) / units;
+  int64_t len = (seen + want - 1) / want;
+  len = (len + kMinSplit - 1) / kMinSplit * kMinSplit;
+  if (len < kMinSplit) len = kMinSplit;
+  if (len > kMaxSplit) len = kMaxSplit;
+  p.split_len = (int32_t)len;
+  p.splits = (int32_t)((seen + len - 1) / len);
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+template <int BITS, int D>
+hipError_t launch(const AttnArgs &a, hipStream_t s) {
+  const SplitPlan p = plan_for(a.seqs, a.kv_heads, a.group, a.max_len, a.window);
+  const int64_t wgs = a.seqs * a.kv_heads * p.qtiles * p.splits;
+  if (wgs > INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((attn_split_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+  if (p.splits > 1)
+    hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)(a.seqs * a.kv_heads * a.group)), dim3(kAttnThreads), 0, s, a,
+                       p);
+  return hipGetLastError();
 }
 
 template <int BITS>
 hipError_t launch_bits(int d, const AttnArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.seqs * a.kv_heads * a.group));
   switch (d) {
-    case 64: hipLaunchKernelGGL((attn_simple_kernel<BITS, 64>), grid, dim3(kAttnThreads), 0, s, a); break;
-    case 128: hipLaunchKernelGGL((attn_simple_kernel<BITS, 128>), grid, dim3(kAttnThreads), 0, s, a); break;
-    case 256: hipLaunchKernelGGL((attn_simple_kernel<BITS, 256>), grid, dim3(kAttnThreads), 0, s, a); break;
-    default: return hipErrorInvalidValue;
+    case 64: return launch<BITS, 64>(a, s);
+    case 128: return launch<BITS, 128>(a, s);
+    case 256: return launch<BITS, 256>(a, s);
   }
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t attn_workspace(const wq_kv_cache &, int64_t, int32_t, int64_t, int64_t) { return 0; }
+size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window) {
+  // a bound that grows with seqs and max_len: plan_for gives units * splits
+  // below units + kWorkgroups unless runs are of kMaxSplit tokens, and none
+  // shorter than kMinSplit
+  const int64_t group = q_heads / c.kv_heads, qtiles = (group + 15) / 16, units = seqs * c.kv_heads * qtiles;
+  const int64_t seen = seen_at_most(max_len, window);
+  if (seen <= kMinSplit) return 0;
+  const int64_t few = units * ((seen + kMinSplit - 1) / kMinSplit), many = units * ((seen + kMaxSplit - 1) / kMaxSplit);
+  const int64_t filled = units + kWorkgroups > many ? units + kWorkgroups : many;
+  const int64_t runs = few < filled ? few : filled;
+  return (size_t)((runs * group + qtiles - 1) / qtiles) * (size_t)(c.head_dim + 4) * sizeof(float);
+}
 
 hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, hipStream_t s) {
   switch (bits) {
