@@ -18,10 +18,11 @@
 // never leave their lane.  The cache's layout gives V in that order (quads
 // of tokens side by side) and K as panels, both in whole 16-byte loads.
 //
-// Codes become fp16 by placing them in the significand of 1024 (0x6400 | c)
-// and subtracting: c - 8 or c - 128 for keys, c - zero for values, all
-// exact.  The keys' scale and zero are applied to the score in fp32:
-//   s (dot(q, c - mid) + (mid - z) sum(q)).
+// Codes become fp16 by placing them in the significand of 1024: 0x6400 | c
+// is 1024 + c.  Values have 1024 + zero subtracted (exact).  Keys keep the
+// bias, 1024 + c (8 bits) or 16 (64 + c) (4 bits, the code four places up),
+// and the score takes it out with the zero, in fp32:
+//   s (dot(q, bias + c) - (bias + z) sum(q)).
 // The values' scale goes into the weight, p s, before it is rounded to
 // fp16; the running reference m therefore tracks max(u + log2 s), so that
 // p s of the largest term stays near 2^kGain and weights down to 2^-20 of
@@ -49,13 +50,16 @@ constexpr float kInvSqrt128 = 0.08838834764831845f;
 constexpr float kNone = -1e30f;      // no term seen yet
 constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
 
+// waves per SIMD that the registers are kept for without spilling
+constexpr int occupancy(int bits, int d) { return d <= 128 ? 3 : bits == 16 ? 1 : 2; }
+
 template <int BITS, int D>
 struct Fmt {
   static constexpr int kRow = D * BITS / 8;        // bytes of a row
   static constexpr int kWords = kRow / 16;         // 32-bit words a lane holds of 16 tokens (keys; values)
   static constexpr int kPiece = kWords < 4 ? kWords : 4;   // words per load
   static constexpr int kKeyMfma = D / 32, kOutMfma = D / 16;
-  static constexpr int kMid = BITS == 8 ? 128 : 8;
+  static constexpr float kBias = BITS == 8 ? 1024.0f : 64.0f;   // of a key operand
   // first of the 8 channels of key operand m in lane group g
   __device__ static constexpr int key_channel(int m, int g) {
     if (BITS == 16) return 32 * m + 8 * g;
@@ -70,10 +74,11 @@ struct Fmt {
   }
 };
 
+// What a lane holds of 32 tokens: keys or values, and their (scale, zero) pairs.
 template <int BITS, int D>
-struct Step {
-  uint32_t k[2][Fmt<BITS, D>::kWords], v[2][Fmt<BITS, D>::kWords];
-  u32x4 kp[2], vp[2];
+struct Side {
+  uint32_t w[2][Fmt<BITS, D>::kWords];
+  u32x4 par[2];
 };
 
 __device__ __forceinline__ half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
@@ -98,21 +103,20 @@ __device__ __forceinline__ half2_t bytes23(uint32_t w) {
 __device__ __forceinline__ half2_t low_nibbles(uint32_t w) { return as_half2((w & 0x000F000Fu) | 0x64006400u); }
 __device__ __forceinline__ half2_t high_nibbles(uint32_t w) { return as_half2((w & 0x00F000F0u) | 0x64006400u); }
 
-// key operand m of a block
+// Key operand m of a block, as kBias + code (8 bits) or 16 (kBias + code)
+// (4 bits); the score takes the bias out again.
 template <int BITS, int D>
 __device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>::kWords], int m) {
   if constexpr (BITS == 16) {
     return as_half8(k[4 * m], k[4 * m + 1], k[4 * m + 2], k[4 * m + 3]);
   } else if constexpr (BITS == 8) {
-    const half2_t c = both(1024.0f + 128.0f);
-    return as_half8(as_u32(bytes01(k[2 * m]) - c), as_u32(bytes23(k[2 * m]) - c), as_u32(bytes01(k[2 * m + 1]) - c),
-                    as_u32(bytes23(k[2 * m + 1]) - c));
+    return as_half8(as_u32(bytes01(k[2 * m])), as_u32(bytes23(k[2 * m])), as_u32(bytes01(k[2 * m + 1])),
+                    as_u32(bytes23(k[2 * m + 1])));
   } else {
     // channel order 0, 4, 1, 5, 2, 6, 3, 7
-    const half2_t c = both(1024.0f + 8.0f), d = both(-(64.0f + 8.0f)), f = both(0.0625f);
-    const uint32_t w = k[m], x = w >> 8;
-    return as_half8(as_u32(low_nibbles(w) - c), as_u32(__builtin_elementwise_fma(high_nibbles(w), f, d)),
-                    as_u32(low_nibbles(x) - c), as_u32(__builtin_elementwise_fma(high_nibbles(x), f, d)));
+    const uint32_t w = k[m];
+    return as_half8(as_u32(high_nibbles(w << 4)), as_u32(high_nibbles(w)), as_u32(high_nibbles(w >> 4)),
+                    as_u32(high_nibbles(w >> 8)));
   }
 }
 
@@ -132,12 +136,10 @@ struct SplitPlan {
 
 // One row's 8 channels in a 16-lane DPP row, rotated back and stored.
 template <int D>
-__device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[8], int64_t seq, int kvh, int head, int c0) {
+__device__ __forceinline__ void store_row(const AttnArgs &a, float (&v)[8], int64_t seq, uint32_t sb, int head, int c0) {
   if (D >= 128 && a.signs) {
     const int jj = threadIdx.x & 15;
     fwht128_row16_signed(v, jj);
-    const int ch = kvh * D + c0;
-    const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
     const float sc = fwht_lane_sign(jj) * kInvSqrt128;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= ((sb >> e) & 1u) ? -sc : sc;
@@ -161,7 +163,7 @@ __device__ __forceinline__ Range range_of(const AttnArgs &a, int64_t seq) {
 }
 
 template <int BITS, int D>
-__global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a, SplitPlan plan) {
+__global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_kernel(AttnArgs a, SplitPlan plan) {
   using F = Fmt<BITS, D>;
   constexpr int kQStride = D + 8, kOStride = D + 4;
   __shared__ union {
@@ -171,37 +173,102 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a,
   __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
 
   int id = blockIdx.x;
-  const int split = id % plan.splits;
-  id /= plan.splits;
+  // the sequences' first splits first: the empty ones of short sequences last
+  const int kvh = id % a.kv_heads;
+  id /= a.kv_heads;
   const int qt = id % plan.qtiles;
   id /= plan.qtiles;
-  const int kvh = id % a.kv_heads;
-  const int64_t seq = id / a.kv_heads;
-  const Range rg = range_of(a, seq);
-  const int my_splits = rg.splits(plan.split_len);
-  if (split >= my_splits && split > 0) return;
-  const int begin = rg.begin + split * plan.split_len;
-  const int end = min(begin + plan.split_len, rg.len);   // at or below begin: nothing to attend to
+  const int64_t seq = id % (int)a.seqs;
+  const int split = id / (int)a.seqs;
   const int head0 = kvh * a.group + 16 * qt, heads = min(16, a.group - 16 * qt);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
 
-  // the queries: rotated as the cache is, rounded to fp16, in the keys' channel order
-  for (int i = tid; i < 16 * (D / 8); i += kAttnThreads) {
-    const int h = i / (D / 8), c0 = 8 * (i % (D / 8));
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (h < heads) {
-      const uint4 raw = *reinterpret_cast<const uint4 *>(a.q + seq * a.ldq + (int64_t)(head0 + h) * D + c0);
-      v[0] = half_bits_to_float(raw.x & 0xFFFF); v[1] = half_bits_to_float(raw.x >> 16);
-      v[2] = half_bits_to_float(raw.y & 0xFFFF); v[3] = half_bits_to_float(raw.y >> 16);
-      v[4] = half_bits_to_float(raw.z & 0xFFFF); v[5] = half_bits_to_float(raw.z >> 16);
-      v[6] = half_bits_to_float(raw.w & 0xFFFF); v[7] = half_bits_to_float(raw.w >> 16);
-    }
-    if (D >= 128 && a.signs) {
-      const int ch = kvh * D + c0, jj = tid & 15;
-      const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
+  // The chain to the first scores is: launch arguments, then the length,
+  // the first pages and the queries at once, then the first keys and
+  // values, which travel while the queries are prepared.
+  constexpr int kRows = 16 * (D / 8), kPasses = (kRows + kAttnThreads - 1) / kAttnThreads;
+  uint4 raw[kPasses];
+  const int ch = kvh * D + 8 * (tid % (D / 8));   // this thread's channels in every pass
+  const uint32_t flips = D >= 128 && a.signs ? a.signs[ch >> 5] : 0u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = ((sb >> e) & 1u) ? -v[e] : v[e];
+  for (int i = 0; i < kPasses; ++i) {
+    const int h = (tid + i * kAttnThreads) / (D / 8), c0 = 8 * (tid % (D / 8));
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (h < heads) raw[i] = *reinterpret_cast<const uint4 *>(a.q + seq * a.ldq + (int64_t)(head0 + h) * D + c0);
+  }
+  const_i32 table = (const_i32)(a.table + seq * a.ld_table);
+  const int page_mask = (1 << a.page_shift) - 1;
+  // the table's entry for the 16 tokens from t, not yet looked at (the
+  // scalar load is waited for where it is); past max_len any entry
+  auto entry_at = [&](int t) -> int { return table[max(min(t, a.max_len - 1), 0) >> a.page_shift]; };
+  const Range rg = range_of(a, seq);
+  const int begin = (a.window ? rg.begin : 0) + split * plan.split_len;
+  int t = begin + wave * kStep;
+  int e0 = 0, e1 = 0;
+  if (a.max_len > 0) {
+    e0 = entry_at(t);
+    e1 = entry_at(t + 16);
+  }
+  const int my_splits = rg.splits(plan.split_len);
+  if (split >= my_splits && split > 0) return;
+  const int end = min(begin + plan.split_len, rg.len);   // at or below begin: nothing to attend to
+
+  const char *kbase = static_cast<const char *>(a.k), *vbase = static_cast<const char *>(a.v);
+  const int k_lane = F::kRow >= 64 ? col * 64 + g * 16 : col * 32 + g * 8;
+  const int v_lane = g * 4 * F::kRow + col * 4 * F::kPiece;
+  auto takes_part = [&](int t, int entry) { return t < end && (uint32_t)entry < (uint32_t)a.pages; };
+  // 16 tokens that take no part get empty resources: their loads return
+  // zeros without touching memory, so every load is issued unconditionally
+  auto load = [&](Side<BITS, D> &s, const char *base, const uint32_t *params, int at, int stride, int t, int e0, int e1) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int e = b ? e1 : e0;
+      const bool ok = takes_part(t + 16 * b, e);
+      const int64_t token = (((int64_t)(ok ? e : 0) * a.kv_heads + kvh) << a.page_shift) + ((t + 16 * b) & page_mask);
+      const rsrc_t rs = make_rsrc(base + token * F::kRow, ok ? 16 * F::kRow : 0);
+#pragma unroll
+      for (int i = 0; i < F::kWords / F::kPiece; ++i) {
+        if constexpr (F::kPiece == 4) {
+          const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, at + i * stride, 0, kNT);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s.w[b][4 * i + x] = v[x];
+        } else {
+          const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, kNT);
+          s.w[b][0] = v[0]; s.w[b][1] = v[1];
+        }
+      }
+      if constexpr (BITS != 16)
+        s.par[b] = __builtin_amdgcn_raw_buffer_load_b128(make_rsrc(params + token, ok ? 64 : 0), 16 * g, 0, kNT);
+    }
+  };
+  auto load_k = [&](Side<BITS, D> &s, int t, int e0, int e1) { load(s, kbase, a.k_params, k_lane, 1024, t, e0, e1); };
+  auto load_v = [&](Side<BITS, D> &s, int t, int e0, int e1) { load(s, vbase, a.v_params, v_lane, 256, t, e0, e1); };
+
+  constexpr int kStride = kWaves * kStep;
+  Side<BITS, D> ks, vs;
+  int n0 = 0, n1 = 0;
+  if (t < end) {
+    load_k(ks, t, e0, e1);
+    load_v(vs, t, e0, e1);
+    n0 = entry_at(t + kStride);
+    n1 = entry_at(t + kStride + 16);
+  }
+
+  // the queries: rotated as the cache is, rounded to fp16, in the keys' channel order
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int h = (tid + i * kAttnThreads) / (D / 8), c0 = 8 * (tid % (D / 8));
+    if (kRows < kAttnThreads && h >= 16) break;
+    float v[8];
+    v[0] = half_bits_to_float(raw[i].x & 0xFFFF); v[1] = half_bits_to_float(raw[i].x >> 16);
+    v[2] = half_bits_to_float(raw[i].y & 0xFFFF); v[3] = half_bits_to_float(raw[i].y >> 16);
+    v[4] = half_bits_to_float(raw[i].z & 0xFFFF); v[5] = half_bits_to_float(raw[i].z >> 16);
+    v[6] = half_bits_to_float(raw[i].w & 0xFFFF); v[7] = half_bits_to_float(raw[i].w >> 16);
+    if (D >= 128 && a.signs) {
+      const int jj = tid & 15;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = ((flips >> ((ch + e) & 31)) & 1u) ? -v[e] : v[e];
       fwht128_row16_signed(v, jj);
       const float sc = fwht_lane_sign(jj) * kInvSqrt128;
 #pragma unroll
@@ -226,139 +293,110 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a,
   qsum = column_sum(qsum);
   __syncthreads();   // sh.q is free for sh.o
 
-  const float to_log2 = a.scale * 1.4426950408889634f;
   float m = kNone, l = 0.0f;
   f32x4 o[F::kOutMfma];
 #pragma unroll
   for (int n = 0; n < F::kOutMfma; ++n) o[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const_i32 table = (const_i32)(a.table + seq * a.ld_table);
-  const int page_mask = (1 << a.page_shift) - 1;
-  // page of the 16 tokens from t; -1: none of them takes part
-  auto page_at = [&](int t) -> int {
-    if (t >= end) return -1;
-    const int p = table[t >> a.page_shift];
-    return (uint32_t)p < (uint32_t)a.pages ? p : -1;
-  };
-  const char *kbase = static_cast<const char *>(a.k), *vbase = static_cast<const char *>(a.v);
-  const uint32_t k_lane = F::kRow >= 64 ? col * 64 + g * 16 : col * 32 + g * 8;
-  const uint32_t v_lane = g * 4 * F::kRow + col * 4 * F::kPiece;
-  auto load = [&](Step<BITS, D> &s, int t, int p0, int p1) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int p = max(b ? p1 : p0, 0);   // a page that takes no part: page 0, masked
-      const int64_t token = (((int64_t)p * a.kv_heads + kvh) << a.page_shift) + ((t + 16 * b) & page_mask);
-      const char *kb = kbase + token * F::kRow, *vb = vbase + token * F::kRow;
-#pragma unroll
-      for (int i = 0; i < F::kWords / F::kPiece; ++i) {
-        if constexpr (F::kPiece == 4) {
-          const u32x4 kw = *reinterpret_cast<const u32x4 *>(kb + (k_lane + i * 1024));
-          const u32x4 vw = *reinterpret_cast<const u32x4 *>(vb + (v_lane + i * 256));
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s.k[b][4 * i + e] = kw[e];
-            s.v[b][4 * i + e] = vw[e];
-          }
-        } else {
-          const u32x2 kw = *reinterpret_cast<const u32x2 *>(kb + k_lane);
-          const u32x2 vw = *reinterpret_cast<const u32x2 *>(vb + v_lane);
-          s.k[b][0] = kw[0]; s.k[b][1] = kw[1];
-          s.v[b][0] = vw[0]; s.v[b][1] = vw[1];
-        }
-      }
-      if constexpr (BITS != 16) {
-        s.kp[b] = *reinterpret_cast<const u32x4 *>(a.k_params + token + 4 * g);
-        s.vp[b] = *reinterpret_cast<const u32x4 *>(a.v_params + token + 4 * g);
-      }
-    }
-  };
-
-  auto compute = [&](Step<BITS, D> &s, int t, int p0, int p1) {
-    // scores, in units of log2
-    float u[8];
+  const float to_log2 = a.scale * 1.4426950408889634f * (BITS == 4 ? 0.0625f : 1.0f);
+  const float bias_sum = (BITS == 4 ? -16.0f : -1.0f) * F::kBias * qsum, zero_sum = (BITS == 4 ? -16.0f : -1.0f) * qsum;
+  for (; t < end; t += kStride) {
+    // scores before the keys' scale, in units of log2
+    float x[8];
+    half2_t kp[8];   // the scale is the low half
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (BITS != 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = ((float)F::kMid - half_bits_to_float(s.kp[b][i] >> 16)) * qsum;
+        for (int i = 0; i < 4; ++i) {
+          kp[4 * b + i] = as_half2(ks.par[b][i]);
+          acc[i] = fmaf((float)kp[4 * b + i][1], zero_sum, bias_sum);
+        }
       }
 #pragma unroll
       for (int mm = 0; mm < F::kKeyMfma; ++mm)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(s.k[b], mm), q[mm], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm), q[mm], acc, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        u[4 * b + i] = acc[i] * (BITS == 16 ? to_log2 : half_bits_to_float(s.kp[b][i] & 0xFFFF) * to_log2);
+      for (int i = 0; i < 4; ++i) x[4 * b + i] = acc[i] * to_log2;
     }
+    __builtin_amdgcn_sched_barrier(0);
+    load_k(ks, t + kStride, n0, n1);
+    __builtin_amdgcn_sched_barrier(0);
     // the first and the last step of a sequence, pages outside the cache
-    if (t < rg.start || t + kStep > end || p0 < 0 || p1 < 0) {
+    const bool in0 = takes_part(t, e0), in1 = takes_part(t + 16, e1);
+    if (t < rg.start || t + kStep > end || !in0 || !in1) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         bool ok[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int at = t + 16 * b + 4 * g + i;
-          ok[i] = at >= rg.start && at < end && (b ? p1 : p0) >= 0;
-          u[4 * b + i] = ok[i] ? u[4 * b + i] : -INFINITY;
-          if (BITS != 16) s.vp[b][i] = ok[i] ? s.vp[b][i] : 0u;   // scale and zero 0
+          ok[i] = at >= rg.start && at < end && (b ? in1 : in0);
+          x[4 * b + i] = ok[i] ? x[4 * b + i] : -INFINITY;
+          if (BITS != 16) {
+            kp[4 * b + i][0] = ok[i] ? kp[4 * b + i][0] : (_Float16)1.0f;
+            vs.par[b][i] = ok[i] ? vs.par[b][i] : 0u;   // scale and zero 0
+          }
         }
         if constexpr (BITS == 16) {
           const uint32_t lo = (ok[0] ? 0xFFFFu : 0u) | (ok[1] ? 0xFFFF0000u : 0u);
           const uint32_t hi = (ok[2] ? 0xFFFFu : 0u) | (ok[3] ? 0xFFFF0000u : 0u);
 #pragma unroll
-          for (int i = 0; i < F::kWords; ++i) s.v[b][i] &= (i & 1) ? hi : lo;
+          for (int i = 0; i < F::kWords; ++i) vs.w[b][i] &= (i & 1) ? hi : lo;
         }
       }
     }
-    float vs[8], p[8], w[8];
+    // p = 2^(u - m), w = fp16(p s); both from one fused step each
+    float p[8];
+    _Float16 w[8];
+    auto weigh = [&]() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      vs[i] = BITS == 16 ? (float)(1 << kGain) : half_bits_to_float(s.vp[i >> 2][i & 3] & 0xFFFF) * (float)(1 << kGain);
-      p[i] = __builtin_amdgcn_exp2f(u[i] - m);
-      w[i] = p[i] * vs[i];
-    }
-    float top = w[0];
+      for (int i = 0; i < 8; ++i) {
+        p[i] = __builtin_amdgcn_exp2f(BITS == 16 ? x[i] - m : fmaf((float)kp[i][0], x[i], -m));
+        w[i] = BITS == 16 ? (_Float16)p[i] : (_Float16)fmaf(p[i], (float)as_half2(vs.par[i >> 2][i & 3])[0], 0.0f);
+      }
+    };
+    weigh();
+    _Float16 top = w[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, w[i]);
-    if (__any(!(top <= (float)(1 << (kGain + kSlack))))) {
-      // move the reference to the largest term so far (2^-24: the smallest
-      // positive scale, so that rows of scale 0 do not leave it unset)
-      float high = m;
+    for (int i = 1; i < 8; ++i) top = __builtin_fmaxf16(top, w[i]);
+    if (__any(!(top <= (_Float16)(1 << (kGain + kSlack))))) {
+      // move the reference: the largest term so far becomes 2^kGain (2^-24:
+      // the smallest positive scale, so that rows of scale 0 do not leave
+      // it unset)
+      float high = m + (float)kGain;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        high = fmaxf(high, u[i] + (BITS == 16 ? 0.0f : fmaxf(__builtin_amdgcn_logf(vs[i]) - (float)kGain, -24.0f)));
-      high = column_max(high);
+        high = fmaxf(high, BITS == 16 ? x[i]
+                                      : (float)kp[i][0] * x[i] +
+                                            fmaxf(__builtin_amdgcn_logf((float)as_half2(vs.par[i >> 2][i & 3])[0]), -24.0f));
+      high = column_max(high) - (float)kGain;
       const float keep = __builtin_amdgcn_exp2f(m - high);
       m = high;
       l *= keep;
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n) o[n] *= keep;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(u[i] - m);
-        w[i] = p[i] * vs[i];
-      }
+      weigh();
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) l += p[i];
+    l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     // weights as the second operand, in the values' token order: 4-bit
     // codes of tokens 0, 2 and 1, 3 come out of a word together
     constexpr int o1 = BITS == 4 ? 2 : 1, o2 = BITS == 4 ? 1 : 2;
-    const half8_t pw = as_half8(pack_half2(w[0], w[o1]), pack_half2(w[o2], w[3]), pack_half2(w[4], w[4 + o1]),
-                                pack_half2(w[4 + o2], w[7]));
+    const half8_t pw = {w[0], w[o1], w[o2], w[3], w[4], w[4 + o1], w[4 + o2], w[7]};
     half2_t z[2][2];
     if constexpr (BITS != 16) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        z[b][0] = as_half2(__builtin_amdgcn_perm(s.vp[b][o1], s.vp[b][0], 0x07060302u));
-        z[b][1] = as_half2(__builtin_amdgcn_perm(s.vp[b][3], s.vp[b][o2], 0x07060302u));
+        z[b][0] = as_half2(__builtin_amdgcn_perm(vs.par[b][o1], vs.par[b][0], 0x07060302u));
+        z[b][1] = as_half2(__builtin_amdgcn_perm(vs.par[b][3], vs.par[b][o2], 0x07060302u));
       }
     }
     if constexpr (BITS == 16) {
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n)
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(s.v[0][2 * n], s.v[0][2 * n + 1], s.v[1][2 * n], s.v[1][2 * n + 1]), pw, o[n], 0, 0, 0);
+            as_half8(vs.w[0][2 * n], vs.w[0][2 * n + 1], vs.w[1][2 * n], vs.w[1][2 * n + 1]), pw, o[n], 0, 0, 0);
     } else if constexpr (BITS == 8) {
       half2_t c[2][2];
 #pragma unroll
@@ -366,8 +404,8 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a,
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n)
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(as_u32(bytes01(s.v[0][n]) - c[0][0]), as_u32(bytes23(s.v[0][n]) - c[0][1]),
-                     as_u32(bytes01(s.v[1][n]) - c[1][0]), as_u32(bytes23(s.v[1][n]) - c[1][1])),
+            as_half8(as_u32(bytes01(vs.w[0][n]) - c[0][0]), as_u32(bytes23(vs.w[0][n]) - c[0][1]),
+                     as_u32(bytes01(vs.w[1][n]) - c[1][0]), as_u32(bytes23(vs.w[1][n]) - c[1][1])),
             pw, o[n], 0, 0, 0);
     } else {
       half2_t c[2][2], d[2][2];
@@ -379,7 +417,7 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a,
       }
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; n += 2) {
-        const uint32_t a0 = s.v[0][n / 2], a1 = a0 >> 8, b0 = s.v[1][n / 2], b1 = b0 >> 8;
+        const uint32_t a0 = vs.w[0][n / 2], a1 = a0 >> 8, b0 = vs.w[1][n / 2], b1 = b0 >> 8;
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
             as_half8(as_u32(low_nibbles(a0) - c[0][0]), as_u32(low_nibbles(a1) - c[0][1]),
                      as_u32(low_nibbles(b0) - c[1][0]), as_u32(low_nibbles(b1) - c[1][1])),
@@ -392,31 +430,11 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a,
             pw, o[n + 1], 0, 0, 0);
       }
     }
-  };
-
-  constexpr int kStride = kWaves * kStep;
-  int t = begin + wave * kStep;
-  if (t < end) {
-    Step<BITS, D> s0, s1;
-    int p0 = page_at(t), p1 = page_at(t + 16);
-    load(s0, t, p0, p1);
-    int n0 = page_at(t + kStride), n1 = page_at(t + kStride + 16);
-    for (;;) {
-      const bool more = t + kStride < end;
-      if (more) load(s1, t + kStride, n0, n1);
-      const int f0 = page_at(t + 2 * kStride), f1 = page_at(t + 2 * kStride + 16);
-      compute(s0, t, p0, p1);
-      if (!more) break;
-      t += kStride;
-      const bool more2 = t + kStride < end;
-      if (more2) load(s0, t + kStride, f0, f1);
-      const int h0 = page_at(t + 2 * kStride), h1 = page_at(t + 2 * kStride + 16);
-      compute(s1, t, n0, n1);
-      if (!more2) break;
-      t += kStride;
-      p0 = f0; p1 = f1;
-      n0 = h0; n1 = h1;
-    }
+    __builtin_amdgcn_sched_barrier(0);
+    load_v(vs, t + kStride, n0, n1);
+    e0 = n0; e1 = n1;
+    n0 = entry_at(t + 2 * kStride);
+    n1 = entry_at(t + 2 * kStride + 16);
   }
 
   // join the four waves
@@ -446,10 +464,10 @@ __global__ __launch_bounds__(kAttnThreads, 1) void attn_split_kernel(AttnArgs a,
       for (int e = 0; e < 8; ++e) v[e] += f * sh.o[w][h][c0 + e];
     }
     if (my_splits <= 1) {
-      const float inv = total > 0.0f || total != total ? (1.0f / (1 << kGain)) / total : 0.0f;
+      const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= inv;
-      store_row<D>(a, v, seq, kvh, head, c0);
+      store_row<D>(a, v, seq, flips >> (ch & 31), head, c0);
     } else {
       const int64_t at = ((seq * a.kv_heads * a.group + head) * plan.splits + split);
       float *part = a.partial + at * (D + 4);
@@ -476,6 +494,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Spl
   const int n = range_of(a, seq).splits(plan.split_len);
   if (n <= 1) return;   // written by its one workgroup
   const int tid = threadIdx.x, part = tid / kLanes, c0 = 8 * (tid % kLanes);
+  const int ch = head / a.group * D + c0;
+  const uint32_t flips = D >= 128 && a.signs ? a.signs[ch >> 5] : 0u;
   const float *in = a.partial + (int64_t)blockIdx.x * plan.splits * (D + 4);
   float m = kNone, l = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   for (int s = part; s < n; s += kParts) {
@@ -511,10 +531,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Spl
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += f * sh[i][c0 + e];
   }
-  const float inv = total > 0.0f || total != total ? (1.0f / (1 << kGain)) / total : 0.0f;
+  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] *= inv;
-  store_row<D>(a, v, seq, head / a.group, head, c0);
+  store_row<D>(a, v, seq, flips >> (ch & 31), head, c0);
 }
 
 constexpr int64_t kWorkgroups = 512;   // two a CU
