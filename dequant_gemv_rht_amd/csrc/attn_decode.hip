@@ -99,14 +99,20 @@ __device__ __forceinline__ half2_t bytes01(uint32_t w) {
 __device__ __forceinline__ half2_t bytes23(uint32_t w) {
   return as_half2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u));
 }
-// 4-bit codes at bits 0 and 16 -> 1024 + code; at bits 4 and 20 -> 1024 + 16 code
-__device__ __forceinline__ half2_t low_nibbles(uint32_t w) { return as_half2((w & 0x000F000Fu) | 0x64006400u); }
-__device__ __forceinline__ half2_t high_nibbles(uint32_t w) { return as_half2((w & 0x00F000F0u) | 0x64006400u); }
+// 4-bit codes at bits 0 and 16 -> 1024 + code; at bits 4 and 20 -> 1024 +
+// 16 code.  One and-or each: the constants are kept in registers, as two
+// literals would make it two instructions.
+struct Nibbles {
+  uint32_t low = 0x000F000Fu, high = 0x00F000F0u, one = 0x64006400u;
+  __device__ __forceinline__ Nibbles() { asm volatile("" : "+s"(low), "+s"(high), "+v"(one)); }
+  __device__ __forceinline__ half2_t lo(uint32_t w) const { return as_half2((w & low) | one); }
+  __device__ __forceinline__ half2_t hi(uint32_t w) const { return as_half2((w & high) | one); }
+};
 
 // Key operand m of a block, as kBias + code (8 bits) or 16 (kBias + code)
 // (4 bits); the score takes the bias out again.
 template <int BITS, int D>
-__device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>::kWords], int m) {
+__device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>::kWords], int m, const Nibbles &nib) {
   if constexpr (BITS == 16) {
     return as_half8(k[4 * m], k[4 * m + 1], k[4 * m + 2], k[4 * m + 3]);
   } else if constexpr (BITS == 8) {
@@ -115,8 +121,7 @@ __device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>:
   } else {
     // channel order 0, 4, 1, 5, 2, 6, 3, 7
     const uint32_t w = k[m];
-    return as_half8(as_u32(high_nibbles(w << 4)), as_u32(high_nibbles(w)), as_u32(high_nibbles(w >> 4)),
-                    as_u32(high_nibbles(w >> 8)));
+    return as_half8(as_u32(nib.hi(w << 4)), as_u32(nib.hi(w)), as_u32(nib.hi(w >> 4)), as_u32(nib.hi(w >> 8)));
   }
 }
 
@@ -300,28 +305,33 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
 
   const float to_log2 = a.scale * 1.4426950408889634f * (BITS == 4 ? 0.0625f : 1.0f);
   const float bias_sum = (BITS == 4 ? -16.0f : -1.0f) * F::kBias * qsum, zero_sum = (BITS == 4 ? -16.0f : -1.0f) * qsum;
+  const Nibbles nib;
   for (; t < end; t += kStride) {
     // scores before the keys' scale, in units of log2
     float x[8];
-    half2_t kp[8];   // the scale is the low half
+    uint32_t kp[4];   // the keys' scales, two to a word
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
       if constexpr (BITS != 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          kp[4 * b + i] = as_half2(ks.par[b][i]);
-          acc[i] = fmaf((float)kp[4 * b + i][1], zero_sum, bias_sum);
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf((float)as_half2(ks.par[b][i])[1], zero_sum, bias_sum);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          kp[2 * b + i] = __builtin_amdgcn_perm(ks.par[b][2 * i + 1], ks.par[b][2 * i], 0x05040100u);
+          // here, and not where it is used: the pairs' registers are about to be loaded again
+          asm volatile("" : "+v"(kp[2 * b + i]));
         }
       }
 #pragma unroll
       for (int mm = 0; mm < F::kKeyMfma; ++mm)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm), q[mm], acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm, nib), q[mm], acc, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[4 * b + i] = acc[i] * to_log2;
     }
     __builtin_amdgcn_sched_barrier(0);
     load_k(ks, t + kStride, n0, n1);
+    const int f0 = entry_at(t + 2 * kStride), f1 = entry_at(t + 2 * kStride + 16);
     __builtin_amdgcn_sched_barrier(0);
     // the first and the last step of a sequence, pages outside the cache
     const bool in0 = takes_part(t, e0), in1 = takes_part(t + 16, e1);
@@ -335,8 +345,10 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
           ok[i] = at >= rg.start && at < end && (b ? in1 : in0);
           x[4 * b + i] = ok[i] ? x[4 * b + i] : -INFINITY;
           if (BITS != 16) {
-            kp[4 * b + i][0] = ok[i] ? kp[4 * b + i][0] : (_Float16)1.0f;
-            vs.par[b][i] = ok[i] ? vs.par[b][i] : 0u;   // scale and zero 0
+            // keys: scale 1 (a NaN there must not undo the mask); values: scale and zero 0
+            const uint32_t half = 0xFFFFu << (16 * (i & 1));
+            kp[2 * b + (i >> 1)] = ok[i] ? kp[2 * b + (i >> 1)] : (kp[2 * b + (i >> 1)] & ~half) | (0x3C003C00u & half);
+            vs.par[b][i] = ok[i] ? vs.par[b][i] : 0u;
           }
         }
         if constexpr (BITS == 16) {
@@ -353,7 +365,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
     auto weigh = [&]() {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(BITS == 16 ? x[i] - m : fmaf((float)kp[i][0], x[i], -m));
+        p[i] = __builtin_amdgcn_exp2f(BITS == 16 ? x[i] - m : fmaf((float)as_half2(kp[i >> 1])[i & 1], x[i], -m));
         w[i] = BITS == 16 ? (_Float16)p[i] : (_Float16)fmaf(p[i], (float)as_half2(vs.par[i >> 2][i & 3])[0], 0.0f);
       }
     };
@@ -369,7 +381,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         high = fmaxf(high, BITS == 16 ? x[i]
-                                      : (float)kp[i][0] * x[i] +
+                                      : (float)as_half2(kp[i >> 1])[i & 1] * x[i] +
                                             fmaxf(__builtin_amdgcn_logf((float)as_half2(vs.par[i >> 2][i & 3])[0]), -24.0f));
       high = column_max(high) - (float)kGain;
       const float keep = __builtin_amdgcn_exp2f(m - high);
@@ -419,22 +431,21 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
       for (int n = 0; n < F::kOutMfma; n += 2) {
         const uint32_t a0 = vs.w[0][n / 2], a1 = a0 >> 8, b0 = vs.w[1][n / 2], b1 = b0 >> 8;
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(as_u32(low_nibbles(a0) - c[0][0]), as_u32(low_nibbles(a1) - c[0][1]),
-                     as_u32(low_nibbles(b0) - c[1][0]), as_u32(low_nibbles(b1) - c[1][1])),
+            as_half8(as_u32(nib.lo(a0) - c[0][0]), as_u32(nib.lo(a1) - c[0][1]),
+                     as_u32(nib.lo(b0) - c[1][0]), as_u32(nib.lo(b1) - c[1][1])),
             pw, o[n], 0, 0, 0);
         o[n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(as_u32(__builtin_elementwise_fma(high_nibbles(a0), f, d[0][0])),
-                     as_u32(__builtin_elementwise_fma(high_nibbles(a1), f, d[0][1])),
-                     as_u32(__builtin_elementwise_fma(high_nibbles(b0), f, d[1][0])),
-                     as_u32(__builtin_elementwise_fma(high_nibbles(b1), f, d[1][1]))),
+            as_half8(as_u32(__builtin_elementwise_fma(nib.hi(a0), f, d[0][0])),
+                     as_u32(__builtin_elementwise_fma(nib.hi(a1), f, d[0][1])),
+                     as_u32(__builtin_elementwise_fma(nib.hi(b0), f, d[1][0])),
+                     as_u32(__builtin_elementwise_fma(nib.hi(b1), f, d[1][1]))),
             pw, o[n + 1], 0, 0, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
     load_v(vs, t + kStride, n0, n1);
     e0 = n0; e1 = n1;
-    n0 = entry_at(t + 2 * kStride);
-    n1 = entry_at(t + 2 * kStride + 16);
+    n0 = f0; n1 = f1;
   }
 
   // join the four waves

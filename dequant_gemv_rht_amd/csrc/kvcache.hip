@@ -1,11 +1,19 @@
 // The paged key-value cache: new rows coded as they are written, and read
 // back (gfx950).  Layouts and rules: include/wq.h.
 //
-// A row of D = 64, 128 or 256 values is D / 8 lanes with 8 channels each, so
-// a 128-block is the 16 lanes of a DPP row and its rotation is
+// A wave takes four tokens of one head (two heads of 64 channels), keys or
+// values: lane 16 t + c holds 8 channels of token t (two sets of 8 for 256),
+// so a 128-block is the 16 lanes of a DPP row and its rotation is
 // fwht128_row16_signed.  Everything is fp32, in the order the definition
 // gives it; no product feeds a sum, so no fused multiply-add can change a
 // code.
+//
+// Values lie in quads, the four tokens of a channel side by side.  Where the
+// four tokens fill a quad, the wave transposes it in registers (the two
+// lane swaps of gfx950) and moves it in whole 4- to 16-byte pieces;
+// otherwise, as in a decode step, each token's units go one by one.  The
+// tokens' slots may start anywhere in a quad, so waves look for quads among
+// the slots rather than at multiples of four.
 #include "wq_internal.h"
 
 namespace wq {
@@ -22,23 +30,111 @@ struct Layout {
   static constexpr int kUnits = BITS == 4 ? D / 2 : D;          // units of a row
   static constexpr int kUnitBytes = BITS == 16 ? 2 : 1;
   static constexpr int kPanel = kUnits * kUnitBytes < 64 ? kUnits : 64 / kUnitBytes;   // units
+  static constexpr int kSets = D == 256 ? 2 : 1;                // sets of 8 channels in a lane
+  static constexpr int kHeads = D == 64 ? 2 : 1;                // heads in a wave
+  static constexpr int kWords = 8 * BITS / 32;                  // 32-bit words of 8 channels
   __device__ static int64_t key_unit(int t, int u) {
     return (int64_t)(t >> 4) * 16 * kUnits + (u / kPanel) * 16 * kPanel + (t & 15) * kPanel + u % kPanel;
   }
   __device__ static int64_t value_unit(int t, int u) { return (int64_t)(t >> 2) * 4 * kUnits + 4 * u + (t & 3); }
 };
 
+// Reductions over the 16 lanes of a DPP row, or (D = 64) each 8 of them.
 template <int D>
 __device__ __forceinline__ float row_min(float v) {
-#pragma unroll
-  for (int o = 1; o < D / 8; o <<= 1) v = fminf(v, __shfl_xor(v, o));
-  return v;
+  v = fminf(v, dpp<kQuadXor1>(v));
+  v = fminf(v, dpp<kQuadXor2>(v));
+  v = fminf(v, dpp<kRowHalfMirror>(v));
+  return D == 64 ? v : fminf(v, dpp<kRowMirror>(v));
 }
 
 template <int D>
 __device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-  for (int o = 1; o < D / 8; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+  v = fmaxf(v, dpp<kQuadXor1>(v));
+  v = fmaxf(v, dpp<kQuadXor2>(v));
+  v = fmaxf(v, dpp<kRowHalfMirror>(v));
+  return D == 64 ? v : fmaxf(v, dpp<kRowMirror>(v));
+}
+
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {   // a's upper 32 lanes with b's lower 32
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {   // a's odd rows of 16 with b's even rows
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ uint32_t bytes(uint32_t hi, uint32_t lo, uint32_t sel) {
+  return __builtin_amdgcn_perm(hi, lo, sel);
+}
+
+// Lane 16 t + c: 8 channels of token t as packed codes  <->  a quarter of the
+// quad, units 2 t' .. (8 bits, fp16) or t' (4 bits) of lane c's 8 channels,
+// the four tokens of each side by side.  Both directions are the transpose
+// of a 4 x 4 matrix whose rows are the four DPP rows of the wave.
+template <int BITS>
+__device__ __forceinline__ void rows_to_quad(uint32_t (&w)[8 * BITS / 32]) {
+  if constexpr (BITS == 16) {
+    swap32(w[0], w[2]);
+    swap32(w[1], w[3]);
+    swap16(w[0], w[1]);
+    swap16(w[2], w[3]);
+    // w[t]: channels 2 t', 2 t' + 1 of token t
+    const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+    w[0] = bytes(b, a, 0x05040100u);
+    w[1] = bytes(d, c, 0x05040100u);
+    w[2] = bytes(b, a, 0x07060302u);
+    w[3] = bytes(d, c, 0x07060302u);
+  } else if constexpr (BITS == 8) {
+    swap32(w[0], w[1]);
+    // 16-bit units: even ones of both words, odd ones of both
+    uint32_t a = bytes(w[1], w[0], 0x05040100u), b = bytes(w[1], w[0], 0x07060302u);
+    swap16(a, b);
+    // a: tokens 0, 2 (one unit each); b: tokens 1, 3
+    w[0] = bytes(b, a, 0x06020400u);
+    w[1] = bytes(b, a, 0x07030501u);
+  } else {
+    uint32_t x = w[0] & 0xFFFFu, y = w[0] >> 16;
+    swap32(x, y);
+    uint32_t a = bytes(y, x, 0x0C040C00u), b = bytes(y, x, 0x0C050C01u);   // even and odd bytes, spread
+    swap16(a, b);
+    w[0] = a | (b << 8);   // a: tokens 0, 2; b: tokens 1, 3
+  }
+}
+
+template <int BITS>
+__device__ __forceinline__ void quad_to_rows(uint32_t (&w)[8 * BITS / 32]) {
+  if constexpr (BITS == 16) {
+    const uint32_t a = w[0], b = w[1], c = w[2], d = w[3];
+    w[0] = bytes(c, a, 0x05040100u);
+    w[1] = bytes(c, a, 0x07060302u);
+    w[2] = bytes(d, b, 0x05040100u);
+    w[3] = bytes(d, b, 0x07060302u);
+    swap16(w[0], w[1]);
+    swap16(w[2], w[3]);
+    swap32(w[0], w[2]);
+    swap32(w[1], w[3]);
+  } else if constexpr (BITS == 8) {
+    uint32_t a = bytes(w[1], w[0], 0x06020400u), b = bytes(w[1], w[0], 0x07030501u);
+    swap16(a, b);
+    w[0] = bytes(b, a, 0x05040100u);
+    w[1] = bytes(b, a, 0x07060302u);
+    swap32(w[0], w[1]);
+  } else {
+    uint32_t a = w[0] & 0x00FF00FFu, b = (w[0] >> 8) & 0x00FF00FFu;
+    swap16(a, b);
+    uint32_t x = bytes(b, a, 0x0C0C0400u), y = bytes(b, a, 0x0C0C0602u);
+    swap32(x, y);
+    w[0] = x | (y << 16);
+  }
+}
+
+// A product rounded to fp32 where it stands: without this the compiler may
+// fold it into a following conversion to fp16, which then rounds once.
+__device__ __forceinline__ float rounded(float v) {
+  asm("" : "+v"(v));
   return v;
 }
 
@@ -60,49 +156,98 @@ struct RowArgs {
   int32_t kv_heads, page_shift, capacity;   // capacity: pages * page_size
 };
 
-// One row (token, head, key or value) per D / 8 lanes.
+// The four tokens 4 j .. 4 j + 3 are the wave's window.  `quad` >= 0: the
+// token of the call that starts the full quad of slots beginning in the
+// window; `rest`: bit t set where token 4 j + t has a slot in the cache and
+// lies in no full quad of the call; `outside`: where its slot is not one of
+// the cache's.
+struct Window {
+  int64_t quad;
+  uint32_t rest, outside;
+};
+__device__ __forceinline__ Window find_window(const RowArgs &a, int64_t j) {
+  // lane i of a row of 16 looks at token 4 j - 3 + i
+  const int i = threadIdx.x & 15;
+  const int64_t token = 4 * j - 3 + i;
+  const int32_t slot = token >= 0 && token < a.tokens && i < 10 ? a.slots[token] : -1;
+  const bool in = slot >= 0 && slot < a.capacity;
+  // every lane takes part in the shuffles
+  const int32_t s1 = __shfl_down(slot, 1, 16), s2 = __shfl_down(slot, 2, 16), s3 = __shfl_down(slot, 3, 16);
+  const bool start = in && (slot & 3) == 0 && s1 == slot + 1 && s2 == slot + 2 && s3 == slot + 3;
+  const uint32_t starts = (uint32_t)__ballot(start) & 0x7Fu;
+  const uint32_t covered = starts | (starts << 1) | (starts << 2) | (starts << 3);
+  Window w;
+  w.quad = starts >> 3 ? 4 * j + __builtin_ctz(starts >> 3) : -1;
+  w.rest = (((uint32_t)__ballot(in) & ~covered) >> 3) & 0xFu;
+  w.outside = ((uint32_t)__ballot(!in && token >= 0 && token < a.tokens) >> 3) & 0xFu;
+  return w;
+}
+
+// A wave's work: window, head (of the first of its heads), keys or values.
 template <int BITS, int D>
-__global__ __launch_bounds__(kRowThreads) void kv_write_kernel(RowArgs a) {
+struct Item {
+  int64_t window;
+  int head, c0;
+  bool is_v, live;
+  __device__ explicit Item(const RowArgs &a) {
+    using L = Layout<BITS, D>;
+    const int64_t id = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
+    const int groups = (a.kv_heads + L::kHeads - 1) / L::kHeads;
+    is_v = id & 1;
+    window = (id >> 1) / groups;
+    head = (int)((id >> 1) % groups) * L::kHeads;
+    const int lane = threadIdx.x & 15;
+    c0 = 8 * lane;
+    if (L::kHeads == 2) {
+      head += lane >> 3;
+      c0 = 8 * (lane & 7);
+    }
+    live = head < a.kv_heads;
+  }
+};
+
+template <int BITS, int D>
+__device__ __forceinline__ void write_rows(const RowArgs &a, const Item<BITS, D> &it, int64_t token, bool live, bool quad) {
   using L = Layout<BITS, D>;
-  const int64_t gid = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  const int c0 = 8 * (int)(gid % (D / 8));
-  const int64_t row = gid / (D / 8);
-  const bool is_v = row & 1;
-  const int64_t token = (row >> 1) / a.kv_heads;
-  const int head = (int)((row >> 1) % a.kv_heads);
-  if (token >= a.tokens) return;   // whole rows of lanes leave together
-  const int32_t slot = a.slots[token];
-  if (slot < 0 || slot >= a.capacity) return;
-  const uint16_t *x = (is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)head * D + c0;
-  float v[8];
-  unpack8(*reinterpret_cast<const uint4 *>(x), v);
-  if (D >= 128 && a.signs) {
-    const int ch = head * D + c0;
-    const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
+  live = live && it.live;
+  const int32_t slot = live ? a.slots[token] : 0;
+  const uint16_t *x =
+      (it.is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)it.head * D + it.c0;
+  float v[L::kSets][8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = ((sb >> e) & 1u) ? -v[e] : v[e];
-    const int jj = threadIdx.x & 15;
-    fwht128_row16_signed(v, jj);
-    const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+  for (int b = 0; b < L::kSets; ++b) {
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (live) raw = *reinterpret_cast<const uint4 *>(x + 128 * b);
+    unpack8(raw, v[b]);
+    if (D >= 128 && a.signs) {
+      const int ch = it.head * D + it.c0 + 128 * b, jj = threadIdx.x & 15;
+      const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= sc;
+      for (int e = 0; e < 8; ++e) v[b][e] = ((sb >> e) & 1u) ? -v[b][e] : v[b][e];
+      fwht128_row16_signed(v[b], jj);
+      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[b][e] = rounded(v[b][e] * sc);
+    }
   }
   const int t = slot & ((1 << a.page_shift) - 1);
-  const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + head;
-  const int64_t base = ph * ((int64_t)L::kUnits << a.page_shift);
+  const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + (live ? it.head : 0);
+  char *base = static_cast<char *>(it.is_v ? a.v : a.k) + ph * (((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift);
+  uint32_t w[L::kSets][L::kWords];
   if constexpr (BITS == 16) {
-    uint16_t *out = static_cast<uint16_t *>(is_v ? a.v : a.k) + base;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      out[is_v ? L::value_unit(t, c0 + e) : L::key_unit(t, c0 + e)] =
-          __builtin_bit_cast(uint16_t, (_Float16)v[e]);
+    for (int b = 0; b < L::kSets; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[b][e] = pack_half2(v[b][2 * e], v[b][2 * e + 1]);
   } else {
     float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, v[e]);
-      hi = fmaxf(hi, v[e]);
-    }
+    for (int b = 0; b < L::kSets; ++b)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo = fminf(lo, v[b][e]);
+        hi = fmaxf(hi, v[b][e]);
+      }
     lo = row_min<D>(lo);
     hi = row_max<D>(hi);
     const float qmax = (float)((1 << BITS) - 1);
@@ -110,73 +255,148 @@ __global__ __launch_bounds__(kRowThreads) void kv_write_kernel(RowArgs a) {
     if (s16 == (_Float16)0.0f) s16 = (_Float16)1.0f;
     const float s = (float)s16;
     const float z = fminf(fmaxf(rintf((0.0f - lo) / s), 0.0f), qmax);
-    uint32_t code[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) code[e] = (uint32_t)fminf(fmaxf(rintf(v[e] / s + z), 0.0f), qmax);
-    uint8_t *out = static_cast<uint8_t *>(is_v ? a.v : a.k) + base;
-    constexpr int kStep = BITS == 4 ? 2 : 1;
+    for (int b = 0; b < L::kSets; ++b) {
 #pragma unroll
-    for (int e = 0; e < 8; e += kStep) {
-      const uint32_t b = BITS == 4 ? code[e] | (code[e + 1] << 4) : code[e];
-      const int u = (c0 + e) / kStep;
-      out[is_v ? L::value_unit(t, u) : L::key_unit(t, u)] = (uint8_t)b;
+      for (int e = 0; e < L::kWords; ++e) w[b][e] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t code = (uint32_t)fminf(fmaxf(rintf(v[b][e] / s + z), 0.0f), qmax);
+        w[b][e * BITS / 32] |= code << (e * BITS % 32);
+      }
     }
-    if (c0 == 0) (is_v ? a.v_params : a.k_params)[(ph << a.page_shift) + t] = pack_half2(s, z);
+    if (live && it.c0 == 0) (it.is_v ? a.v_params : a.k_params)[(ph << a.page_shift) + t] = pack_half2(s, z);
+  }
+  constexpr int kStep = BITS == 4 ? 2 : 1;   // channels of a unit
+  if (!it.is_v) {   // keys: the lane's channels are neighbours
+    if (!live) return;
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      char *out = base + L::kUnitBytes * L::key_unit(t, (it.c0 + 128 * b) / kStep);
+      if constexpr (BITS == 16) *reinterpret_cast<uint4 *>(out) = make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]);
+      if constexpr (BITS == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(w[b][0], w[b][1]);
+      if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(out) = w[b][0];
+    }
+  } else if (quad) {   // all four tokens: unit pairs of the quad
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      rows_to_quad<BITS>(w[b]);
+      const int u = (it.c0 + 128 * b) / kStep + (BITS == 4 ? 1 : 2) * (int)((threadIdx.x >> 4) & 3);
+      char *out = base + L::kUnitBytes * L::value_unit(t & ~3, u);
+      if (!live) continue;
+      if constexpr (BITS == 16) *reinterpret_cast<uint4 *>(out) = make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]);
+      if constexpr (BITS == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(w[b][0], w[b][1]);
+      if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(out) = w[b][0];
+    }
+  } else if (live) {
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b)
+#pragma unroll
+      for (int e = 0; e < 8 / kStep; ++e) {
+        char *out = base + L::kUnitBytes * L::value_unit(t, (it.c0 + 128 * b) / kStep + e);
+        if constexpr (BITS == 16)
+          *reinterpret_cast<uint16_t *>(out) = (uint16_t)(w[b][e / 2] >> (16 * (e & 1)));
+        else
+          *out = (char)(w[b][e / 4] >> (8 * (e & 3)));
+      }
   }
 }
 
 template <int BITS, int D>
-__global__ __launch_bounds__(kRowThreads) void kv_read_kernel(RowArgs a) {
+__device__ __forceinline__ void read_rows(const RowArgs &a, const Item<BITS, D> &it, int64_t token, bool live, bool in,
+                                          bool quad) {
   using L = Layout<BITS, D>;
-  const int64_t gid = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-  const int c0 = 8 * (int)(gid % (D / 8));
-  const int64_t row = gid / (D / 8);
-  const bool is_v = row & 1;
-  const int64_t token = (row >> 1) / a.kv_heads;
-  const int head = (int)((row >> 1) % a.kv_heads);
-  if (token >= a.tokens) return;
-  const int32_t slot = a.slots[token];
-  float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (slot >= 0 && slot < a.capacity) {
-    const int t = slot & ((1 << a.page_shift) - 1);
-    const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + head;
-    const int64_t base = ph * ((int64_t)L::kUnits << a.page_shift);
-    if constexpr (BITS == 16) {
-      const uint16_t *in = static_cast<const uint16_t *>(is_v ? a.v : a.k) + base;
+  live = live && it.live;
+  in = in && it.live;
+  const int32_t slot = in ? a.slots[token] : 0;
+  const int t = slot & ((1 << a.page_shift) - 1);
+  const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + (in ? it.head : 0);
+  const char *base = static_cast<const char *>(it.is_v ? a.v : a.k) + ph * (((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift);
+  constexpr int kStep = BITS == 4 ? 2 : 1;
+  uint32_t par = 0;
+  if (BITS != 16 && in) par = (it.is_v ? a.v_params : a.k_params)[(ph << a.page_shift) + t];
+  uint32_t w[L::kSets][L::kWords];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = half_bits_to_float(in[is_v ? L::value_unit(t, c0 + e) : L::key_unit(t, c0 + e)]);
+  for (int b = 0; b < L::kSets; ++b) {
+#pragma unroll
+    for (int e = 0; e < L::kWords; ++e) w[b][e] = 0;
+    const int u0 = (it.c0 + 128 * b) / kStep;
+    if (!in) continue;
+    if (!it.is_v || quad) {
+      const int64_t at = it.is_v ? L::value_unit(t & ~3, u0 + (BITS == 4 ? 1 : 2) * (int)((threadIdx.x >> 4) & 3))
+                                 : L::key_unit(t, u0);
+      const char *p = base + L::kUnitBytes * at;
+      if constexpr (BITS == 16) {
+        const uint4 r = *reinterpret_cast<const uint4 *>(p);
+        w[b][0] = r.x; w[b][1] = r.y; w[b][2] = r.z; w[b][3] = r.w;
+      }
+      if constexpr (BITS == 8) {
+        const uint2 r = *reinterpret_cast<const uint2 *>(p);
+        w[b][0] = r.x; w[b][1] = r.y;
+      }
+      if constexpr (BITS == 4) w[b][0] = *reinterpret_cast<const uint32_t *>(p);
     } else {
-      const uint8_t *in = static_cast<const uint8_t *>(is_v ? a.v : a.k) + base;
-      const uint32_t par = (is_v ? a.v_params : a.k_params)[(ph << a.page_shift) + t];
-      const float s = half_bits_to_float(par & 0xFFFF), z = half_bits_to_float(par >> 16);
-      constexpr int kStep = BITS == 4 ? 2 : 1;
 #pragma unroll
-      for (int e = 0; e < 8; e += kStep) {
-        const int u = (c0 + e) / kStep;
-        const uint32_t b = in[is_v ? L::value_unit(t, u) : L::key_unit(t, u)];
-        if (BITS == 4) {
-          v[e] = ((float)(b & 15u) - z) * s;
-          v[e + 1] = ((float)(b >> 4) - z) * s;
-        } else {
-          v[e] = ((float)b - z) * s;
-        }
+      for (int e = 0; e < 8 / kStep; ++e) {
+        const char *p = base + L::kUnitBytes * L::value_unit(t, u0 + e);
+        if constexpr (BITS == 16)
+          w[b][e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p) << (16 * (e & 1));
+        else
+          w[b][e / 4] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p) << (8 * (e & 3));
       }
     }
   }
-  // rotated back: x = D H x' / sqrt(128) (H is symmetric)
-  if (D >= 128 && a.signs) {
-    const int jj = threadIdx.x & 15;
-    fwht128_row16_signed(v, jj);
-    const float sc = fwht_lane_sign(jj) * kInvSqrt128;
-    const int ch = head * D + c0;
-    const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
+  uint16_t *x = (it.is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)it.head * D + it.c0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= ((sb >> e) & 1u) ? -sc : sc;
+  for (int b = 0; b < L::kSets; ++b) {
+    if (it.is_v && quad) quad_to_rows<BITS>(w[b]);
+    float v[8];
+    if constexpr (BITS == 16) {
+      unpack8(make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]), v);
+    } else {
+      const float s = half_bits_to_float(par & 0xFFFF), z = half_bits_to_float(par >> 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = ((float)((w[b][e * BITS / 32] >> (e * BITS % 32)) & ((1u << BITS) - 1u)) - z) * s;
+    }
+    // rotated back: x = D H x' / sqrt(128) (H is symmetric)
+    if (D >= 128 && a.signs) {
+      const int jj = threadIdx.x & 15;
+      fwht128_row16_signed(v, jj);
+      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+      const int ch = it.head * D + it.c0 + 128 * b;
+      const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * (((sb >> e) & 1u) ? -sc : sc));
+    }
+    if (live)
+      *reinterpret_cast<uint4 *>(x + 128 * b) =
+          make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
   }
-  uint16_t *x = (is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)head * D + c0;
-  *reinterpret_cast<uint4 *>(x) = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]),
-                                             pack_half2(v[6], v[7]));
+}
+
+template <int BITS, int D>
+__global__ __launch_bounds__(kRowThreads) void kv_write_kernel(RowArgs a) {
+  const Item<BITS, D> it(a);
+  if (4 * it.window >= a.tokens) return;   // whole waves leave together
+  const Window w = find_window(a, it.window);
+  const int t = (threadIdx.x >> 4) & 3;
+  if (w.quad >= 0) write_rows<BITS, D>(a, it, w.quad + t, true, true);
+  if (w.rest) write_rows<BITS, D>(a, it, 4 * it.window + t, (w.rest >> t) & 1u, false);
+}
+
+template <int BITS, int D>
+__global__ __launch_bounds__(kRowThreads) void kv_read_kernel(RowArgs a) {
+  const Item<BITS, D> it(a);
+  if (4 * it.window >= a.tokens) return;
+  const Window w = find_window(a, it.window);
+  const int t = (threadIdx.x >> 4) & 3;
+  if (w.quad >= 0) read_rows<BITS, D>(a, it, w.quad + t, true, true, true);
+  // tokens in no quad, those outside the cache (zeros) among them
+  if (w.rest | w.outside) {
+    const bool in = (w.rest >> t) & 1u;
+    read_rows<BITS, D>(a, it, 4 * it.window + t, in || ((w.outside >> t) & 1u), in, false);
+  }
 }
 
 RowArgs row_args(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, const uint16_t *k, int64_t ldk,
@@ -202,8 +422,9 @@ RowArgs row_args(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, con
 
 template <int BITS, int D>
 hipError_t launch_rows(const RowArgs &a, bool write, hipStream_t s) {
-  const int64_t threads = a.tokens * a.kv_heads * 2 * (D / 8);
-  const int64_t wgs = (threads + kRowThreads - 1) / kRowThreads;
+  constexpr int kHeads = Layout<BITS, D>::kHeads;
+  const int64_t waves = (a.tokens + 3) / 4 * ((a.kv_heads + kHeads - 1) / kHeads) * 2;
+  const int64_t wgs = (waves + kRowThreads / 64 - 1) / (kRowThreads / 64);
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
   if (write)
     hipLaunchKernelGGL((kv_write_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
