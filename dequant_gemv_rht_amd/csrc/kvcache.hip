@@ -22,6 +22,7 @@ using namespace dev;
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int64_t kManyWaves = 2048;
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 
 // unit u of token t of a block of 16 (keys) / a quad of 4 (values)
@@ -183,219 +184,279 @@ __device__ __forceinline__ Window find_window(const RowArgs &a, int64_t j) {
   return w;
 }
 
-// A wave's work: window, head (of the first of its heads), keys or values.
-template <int BITS, int D>
+// A wave's work: a window of four tokens, keys or values, and NH heads (pairs
+// of heads of 64 channels), one after the other from `head` on.
+template <int BITS, int D, int NH>
 struct Item {
   int64_t window;
   int head, c0;
-  bool is_v, live;
+  bool is_v;
   __device__ explicit Item(const RowArgs &a) {
     using L = Layout<BITS, D>;
     const int64_t id = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
-    const int groups = (a.kv_heads + L::kHeads - 1) / L::kHeads;
+    const int groups = (a.kv_heads + L::kHeads * NH - 1) / (L::kHeads * NH);
     is_v = id & 1;
     window = (id >> 1) / groups;
-    head = (int)((id >> 1) % groups) * L::kHeads;
+    head = (int)((id >> 1) % groups) * L::kHeads * NH;
     const int lane = threadIdx.x & 15;
     c0 = 8 * lane;
     if (L::kHeads == 2) {
       head += lane >> 3;
       c0 = 8 * (lane & 7);
     }
-    live = head < a.kv_heads;
   }
 };
 
+// Where the lane's row of each head is: its codes (keys, or one token's
+// units of a quad), its scale and zero, and the caller's row.
 template <int BITS, int D>
-__device__ __forceinline__ void write_rows(const RowArgs &a, const Item<BITS, D> &it, int64_t token, bool live, bool quad) {
-  using L = Layout<BITS, D>;
-  live = live && it.live;
-  const int32_t slot = live ? a.slots[token] : 0;
-  const uint16_t *x =
-      (it.is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)it.head * D + it.c0;
-  float v[L::kSets][8];
-#pragma unroll
-  for (int b = 0; b < L::kSets; ++b) {
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (live) raw = *reinterpret_cast<const uint4 *>(x + 128 * b);
-    unpack8(raw, v[b]);
-    if (D >= 128 && a.signs) {
-      const int ch = it.head * D + it.c0 + 128 * b, jj = threadIdx.x & 15;
-      const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[b][e] = ((sb >> e) & 1u) ? -v[b][e] : v[b][e];
-      fwht128_row16_signed(v[b], jj);
-      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[b][e] = rounded(v[b][e] * sc);
-    }
+struct Place {
+  char *codes;
+  uint32_t *par;
+  uint16_t *x;
+  int64_t head_codes, head_par;   // from one head to the next
+  int t;
+  template <int NH>
+  __device__ Place(const RowArgs &a, const Item<BITS, D, NH> &it, int64_t token, int32_t slot) {
+    using L = Layout<BITS, D>;
+    t = slot & ((1 << a.page_shift) - 1);
+    head_codes = ((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift;
+    head_par = (int64_t)1 << a.page_shift;
+    const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + it.head;
+    codes = static_cast<char *>(it.is_v ? a.v : a.k) + ph * head_codes;
+    par = (it.is_v ? a.v_params : a.k_params) + ph * head_par + t;
+    x = (it.is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)it.head * D + it.c0;
   }
-  const int t = slot & ((1 << a.page_shift) - 1);
-  const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + (live ? it.head : 0);
-  char *base = static_cast<char *>(it.is_v ? a.v : a.k) + ph * (((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift);
-  uint32_t w[L::kSets][L::kWords];
+  // byte offset of the lane's channels of set b
+  __device__ int64_t at(bool is_v, bool quad, int c0, int b) const {
+    using L = Layout<BITS, D>;
+    const int u = (c0 + 128 * b) / (BITS == 4 ? 2 : 1);
+    if (!is_v) return L::kUnitBytes * L::key_unit(t, u);
+    if (quad) return L::kUnitBytes * L::value_unit(t & ~3, u + (BITS == 4 ? 1 : 2) * (int)((threadIdx.x >> 4) & 3));
+    return L::kUnitBytes * L::value_unit(t, u);
+  }
+};
+
+template <int BITS>
+__device__ __forceinline__ void store_piece(char *out, const uint32_t (&w)[8 * BITS / 32]) {
+  if constexpr (BITS == 16) *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+  if constexpr (BITS == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[1]);
+  if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(out) = w[0];
+}
+template <int BITS>
+__device__ __forceinline__ void load_piece(const char *in, uint32_t (&w)[8 * BITS / 32]) {
   if constexpr (BITS == 16) {
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[b][e] = pack_half2(v[b][2 * e], v[b][2 * e + 1]);
-  } else {
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo = fminf(lo, v[b][e]);
-        hi = fmaxf(hi, v[b][e]);
-      }
-    lo = row_min<D>(lo);
-    hi = row_max<D>(hi);
-    const float qmax = (float)((1 << BITS) - 1);
-    _Float16 s16 = (_Float16)fminf((hi - lo) / qmax, 65504.0f);
-    if (s16 == (_Float16)0.0f) s16 = (_Float16)1.0f;
-    const float s = (float)s16;
-    const float z = fminf(fmaxf(rintf((0.0f - lo) / s), 0.0f), qmax);
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b) {
-#pragma unroll
-      for (int e = 0; e < L::kWords; ++e) w[b][e] = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t code = (uint32_t)fminf(fmaxf(rintf(v[b][e] / s + z), 0.0f), qmax);
-        w[b][e * BITS / 32] |= code << (e * BITS % 32);
-      }
-    }
-    if (live && it.c0 == 0) (it.is_v ? a.v_params : a.k_params)[(ph << a.page_shift) + t] = pack_half2(s, z);
+    const uint4 r = *reinterpret_cast<const uint4 *>(in);
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
   }
-  constexpr int kStep = BITS == 4 ? 2 : 1;   // channels of a unit
-  if (!it.is_v) {   // keys: the lane's channels are neighbours
-    if (!live) return;
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b) {
-      char *out = base + L::kUnitBytes * L::key_unit(t, (it.c0 + 128 * b) / kStep);
-      if constexpr (BITS == 16) *reinterpret_cast<uint4 *>(out) = make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]);
-      if constexpr (BITS == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(w[b][0], w[b][1]);
-      if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(out) = w[b][0];
-    }
-  } else if (quad) {   // all four tokens: unit pairs of the quad
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b) {
-      rows_to_quad<BITS>(w[b]);
-      const int u = (it.c0 + 128 * b) / kStep + (BITS == 4 ? 1 : 2) * (int)((threadIdx.x >> 4) & 3);
-      char *out = base + L::kUnitBytes * L::value_unit(t & ~3, u);
-      if (!live) continue;
-      if constexpr (BITS == 16) *reinterpret_cast<uint4 *>(out) = make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]);
-      if constexpr (BITS == 8) *reinterpret_cast<uint2 *>(out) = make_uint2(w[b][0], w[b][1]);
-      if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(out) = w[b][0];
-    }
-  } else if (live) {
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b)
-#pragma unroll
-      for (int e = 0; e < 8 / kStep; ++e) {
-        char *out = base + L::kUnitBytes * L::value_unit(t, (it.c0 + 128 * b) / kStep + e);
-        if constexpr (BITS == 16)
-          *reinterpret_cast<uint16_t *>(out) = (uint16_t)(w[b][e / 2] >> (16 * (e & 1)));
-        else
-          *out = (char)(w[b][e / 4] >> (8 * (e & 3)));
-      }
+  if constexpr (BITS == 8) {
+    const uint2 r = *reinterpret_cast<const uint2 *>(in);
+    w[0] = r.x; w[1] = r.y;
   }
+  if constexpr (BITS == 4) w[0] = *reinterpret_cast<const uint32_t *>(in);
 }
 
-template <int BITS, int D>
-__device__ __forceinline__ void read_rows(const RowArgs &a, const Item<BITS, D> &it, int64_t token, bool live, bool in,
-                                          bool quad) {
+// Codes of a lane's channels, the row's scale and zero: the rule of
+// wq_kv_write.  The quotients x / scale come from the scale's correctly
+// rounded reciprocal with one correction by the remainder (Markstein's
+// division), three operations each instead of a dozen.
+template <int BITS, int D, int SETS>
+__device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t (&w)[SETS][8 * BITS / 32]) {
+  float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+  for (int b = 0; b < SETS; ++b)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      lo = fminf(lo, v[b][e]);
+      hi = fmaxf(hi, v[b][e]);
+    }
+  lo = row_min<D>(lo);
+  hi = row_max<D>(hi);
+  const float qmax = (float)((1 << BITS) - 1);
+  _Float16 s16 = (_Float16)fminf((hi - lo) / qmax, 65504.0f);
+  if (s16 == (_Float16)0.0f) s16 = (_Float16)1.0f;
+  const float s = (float)s16, r = 1.0f / s;
+  const float z = fminf(fmaxf(rintf((0.0f - lo) / s), 0.0f), qmax);
+#pragma unroll
+  for (int b = 0; b < SETS; ++b) {
+    float c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = v[b][e] * r;
+      c[e] = rintf(fmaf(fmaf(-q, s, v[b][e]), r, q) + z);
+    }
+    // whole numbers now; the conversion to a byte clamps to 0 .. 255
+#pragma unroll
+    for (int e = 0; e < 8 * BITS / 32; ++e) w[b][e] = 0;
+    if constexpr (BITS == 8) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[b][e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c[e], e & 3, w[b][e / 4]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = __builtin_amdgcn_fmed3f(c[e], 0.0f, 15.0f);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) w[b][0] = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(c[e + 1], 16.0f, c[e]), e / 2, w[b][0]);
+    }
+  }
+  return pack_half2(s, z);
+}
+
+template <int BITS, int D, int NH>
+__device__ __forceinline__ void write_rows(const RowArgs &a, const Item<BITS, D, NH> &it, int64_t token, bool live,
+                                           bool quad) {
   using L = Layout<BITS, D>;
-  live = live && it.live;
-  in = in && it.live;
-  const int32_t slot = in ? a.slots[token] : 0;
-  const int t = slot & ((1 << a.page_shift) - 1);
-  const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + (in ? it.head : 0);
-  const char *base = static_cast<const char *>(it.is_v ? a.v : a.k) + ph * (((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift);
-  constexpr int kStep = BITS == 4 ? 2 : 1;
-  uint32_t par = 0;
-  if (BITS != 16 && in) par = (it.is_v ? a.v_params : a.k_params)[(ph << a.page_shift) + t];
-  uint32_t w[L::kSets][L::kWords];
+  const Place<BITS, D> pl(a, it, token, live ? a.slots[token] : 0);
+  uint4 raw[NH][L::kSets];
+  uint32_t flips[NH][L::kSets];
 #pragma unroll
-  for (int b = 0; b < L::kSets; ++b) {
+  for (int n = 0; n < NH; ++n) {
+    const int head = it.head + L::kHeads * n;
 #pragma unroll
-    for (int e = 0; e < L::kWords; ++e) w[b][e] = 0;
-    const int u0 = (it.c0 + 128 * b) / kStep;
-    if (!in) continue;
-    if (!it.is_v || quad) {
-      const int64_t at = it.is_v ? L::value_unit(t & ~3, u0 + (BITS == 4 ? 1 : 2) * (int)((threadIdx.x >> 4) & 3))
-                                 : L::key_unit(t, u0);
-      const char *p = base + L::kUnitBytes * at;
-      if constexpr (BITS == 16) {
-        const uint4 r = *reinterpret_cast<const uint4 *>(p);
-        w[b][0] = r.x; w[b][1] = r.y; w[b][2] = r.z; w[b][3] = r.w;
-      }
-      if constexpr (BITS == 8) {
-        const uint2 r = *reinterpret_cast<const uint2 *>(p);
-        w[b][0] = r.x; w[b][1] = r.y;
-      }
-      if constexpr (BITS == 4) w[b][0] = *reinterpret_cast<const uint32_t *>(p);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8 / kStep; ++e) {
-        const char *p = base + L::kUnitBytes * L::value_unit(t, u0 + e);
-        if constexpr (BITS == 16)
-          w[b][e / 2] |= (uint32_t)*reinterpret_cast<const uint16_t *>(p) << (16 * (e & 1));
-        else
-          w[b][e / 4] |= (uint32_t)*reinterpret_cast<const uint8_t *>(p) << (8 * (e & 3));
+    for (int b = 0; b < L::kSets; ++b) {
+      raw[n][b] = make_uint4(0, 0, 0, 0);
+      flips[n][b] = 0;
+      if (live && head < a.kv_heads) {
+        raw[n][b] = *reinterpret_cast<const uint4 *>(pl.x + L::kHeads * n * D + 128 * b);
+        if (D >= 128 && a.signs) flips[n][b] = a.signs[(head * D + it.c0 + 128 * b) >> 5];
       }
     }
   }
-  uint16_t *x = (it.is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)it.head * D + it.c0;
 #pragma unroll
-  for (int b = 0; b < L::kSets; ++b) {
-    if (it.is_v && quad) quad_to_rows<BITS>(w[b]);
-    float v[8];
+  for (int n = 0; n < NH; ++n) {
+    const bool mine = live && it.head + L::kHeads * n < a.kv_heads;
+    float v[L::kSets][8];
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      unpack8(raw[n][b], v[b]);
+      if (D >= 128 && a.signs) {
+        const uint32_t sb = flips[n][b] >> (it.c0 & 31);
+        const int jj = threadIdx.x & 15;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[b][e] = ((sb >> e) & 1u) ? -v[b][e] : v[b][e];
+        fwht128_row16_signed(v[b], jj);
+        const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[b][e] = rounded(v[b][e] * sc);
+      }
+    }
+    uint32_t w[L::kSets][L::kWords];
     if constexpr (BITS == 16) {
-      unpack8(make_uint4(w[b][0], w[b][1], w[b][2], w[b][3]), v);
+#pragma unroll
+      for (int b = 0; b < L::kSets; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[b][e] = pack_half2(v[b][2 * e], v[b][2 * e + 1]);
     } else {
-      const float s = half_bits_to_float(par & 0xFFFF), z = half_bits_to_float(par >> 16);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = ((float)((w[b][e * BITS / 32] >> (e * BITS % 32)) & ((1u << BITS) - 1u)) - z) * s;
+      const uint32_t par = code_row<BITS, D, L::kSets>(v, w);
+      if (mine && it.c0 == 0) pl.par[L::kHeads * n * pl.head_par] = par;
     }
-    // rotated back: x = D H x' / sqrt(128) (H is symmetric)
-    if (D >= 128 && a.signs) {
-      const int jj = threadIdx.x & 15;
-      fwht128_row16_signed(v, jj);
-      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
-      const int ch = it.head * D + it.c0 + 128 * b;
-      const uint32_t sb = a.signs[ch >> 5] >> (ch & 31);
+    char *out = pl.codes + L::kHeads * n * pl.head_codes;
+    constexpr int kStep = BITS == 4 ? 2 : 1;   // channels of a unit
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * (((sb >> e) & 1u) ? -sc : sc));
+    for (int b = 0; b < L::kSets; ++b) {
+      if (it.is_v && quad) rows_to_quad<BITS>(w[b]);
+      char *to = out + pl.at(it.is_v, quad, it.c0, b);
+      if (!mine) continue;
+      if (!it.is_v || quad) {
+        store_piece<BITS>(to, w[b]);
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 8 / kStep; ++e) {   // one token of a quad
+        if constexpr (BITS == 16)
+          reinterpret_cast<uint16_t *>(to)[4 * e] = (uint16_t)(w[b][e / 2] >> (16 * (e & 1)));
+        else
+          to[4 * e] = (char)(w[b][e / 4] >> (8 * (e & 3)));
+      }
     }
-    if (live)
-      *reinterpret_cast<uint4 *>(x + 128 * b) =
-          make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
   }
 }
 
-template <int BITS, int D>
+template <int BITS, int D, int NH>
+__device__ __forceinline__ void read_rows(const RowArgs &a, const Item<BITS, D, NH> &it, int64_t token, bool live,
+                                          bool in, bool quad) {
+  using L = Layout<BITS, D>;
+  const Place<BITS, D> pl(a, it, token, in ? a.slots[token] : 0);
+  constexpr int kStep = BITS == 4 ? 2 : 1;
+  uint32_t w[NH][L::kSets][L::kWords], par[NH], flips[NH][L::kSets];
+#pragma unroll
+  for (int n = 0; n < NH; ++n) {
+    const int head = it.head + L::kHeads * n;
+    const bool mine = in && head < a.kv_heads;
+    const char *from = pl.codes + L::kHeads * n * pl.head_codes;
+    par[n] = 0;
+    if (BITS != 16 && mine) par[n] = pl.par[L::kHeads * n * pl.head_par];
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+#pragma unroll
+      for (int e = 0; e < L::kWords; ++e) w[n][b][e] = 0;
+      flips[n][b] = 0;
+      if (!mine) continue;
+      if (D >= 128 && a.signs) flips[n][b] = a.signs[(head * D + it.c0 + 128 * b) >> 5];
+      const char *p = from + pl.at(it.is_v, quad, it.c0, b);
+      if (!it.is_v || quad) {
+        load_piece<BITS>(p, w[n][b]);
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 8 / kStep; ++e) {
+        if constexpr (BITS == 16)
+          w[n][b][e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[4 * e] << (16 * (e & 1));
+        else
+          w[n][b][e / 4] |= (uint32_t)(uint8_t)p[4 * e] << (8 * (e & 3));
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NH; ++n) {
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      if (it.is_v && quad) quad_to_rows<BITS>(w[n][b]);
+      float v[8];
+      if constexpr (BITS == 16) {
+        unpack8(make_uint4(w[n][b][0], w[n][b][1], w[n][b][2], w[n][b][3]), v);
+      } else {
+        const float s = half_bits_to_float(par[n] & 0xFFFF), z = half_bits_to_float(par[n] >> 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = ((float)((w[n][b][e * BITS / 32] >> (e * BITS % 32)) & ((1u << BITS) - 1u)) - z) * s;
+      }
+      // rotated back: x = D H x' / sqrt(128) (H is symmetric)
+      if (D >= 128 && a.signs) {
+        const int jj = threadIdx.x & 15;
+        fwht128_row16_signed(v, jj);
+        const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+        const uint32_t sb = flips[n][b] >> (it.c0 & 31);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * (((sb >> e) & 1u) ? -sc : sc));
+      }
+      if (live && it.head + L::kHeads * n < a.kv_heads)
+        *reinterpret_cast<uint4 *>(pl.x + L::kHeads * n * D + 128 * b) =
+            make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+    }
+  }
+}
+
+template <int BITS, int D, int NH>
 __global__ __launch_bounds__(kRowThreads) void kv_write_kernel(RowArgs a) {
-  const Item<BITS, D> it(a);
+  const Item<BITS, D, NH> it(a);
   if (4 * it.window >= a.tokens) return;   // whole waves leave together
   const Window w = find_window(a, it.window);
   const int t = (threadIdx.x >> 4) & 3;
-  if (w.quad >= 0) write_rows<BITS, D>(a, it, w.quad + t, true, true);
-  if (w.rest) write_rows<BITS, D>(a, it, 4 * it.window + t, (w.rest >> t) & 1u, false);
+  if (w.quad >= 0) write_rows<BITS, D, NH>(a, it, w.quad + t, true, true);
+  if (w.rest) write_rows<BITS, D, NH>(a, it, 4 * it.window + t, (w.rest >> t) & 1u, false);
 }
 
-template <int BITS, int D>
+template <int BITS, int D, int NH>
 __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(RowArgs a) {
-  const Item<BITS, D> it(a);
+  const Item<BITS, D, NH> it(a);
   if (4 * it.window >= a.tokens) return;
   const Window w = find_window(a, it.window);
   const int t = (threadIdx.x >> 4) & 3;
-  if (w.quad >= 0) read_rows<BITS, D>(a, it, w.quad + t, true, true, true);
+  if (w.quad >= 0) read_rows<BITS, D, NH>(a, it, w.quad + t, true, true, true);
   // tokens in no quad, those outside the cache (zeros) among them
   if (w.rest | w.outside) {
     const bool in = (w.rest >> t) & 1u;
-    read_rows<BITS, D>(a, it, 4 * it.window + t, in || ((w.outside >> t) & 1u), in, false);
+    read_rows<BITS, D, NH>(a, it, 4 * it.window + t, in || ((w.outside >> t) & 1u), in, false);
   }
 }
 
@@ -420,25 +481,31 @@ RowArgs row_args(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, con
   return a;
 }
 
-template <int BITS, int D>
+template <int BITS, int D, int NH>
 hipError_t launch_rows(const RowArgs &a, bool write, hipStream_t s) {
-  constexpr int kHeads = Layout<BITS, D>::kHeads;
+  constexpr int kHeads = Layout<BITS, D>::kHeads * NH;
   const int64_t waves = (a.tokens + 3) / 4 * ((a.kv_heads + kHeads - 1) / kHeads) * 2;
+  // several heads a wave once that still gives every SIMD two waves
+  if constexpr (NH == 1) {
+    constexpr int kMore = D == 256 ? 2 : 4;
+    if (waves >= kManyWaves * kMore && a.kv_heads > Layout<BITS, D>::kHeads)
+      return launch_rows<BITS, D, kMore>(a, write, s);
+  }
   const int64_t wgs = (waves + kRowThreads / 64 - 1) / (kRowThreads / 64);
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
   if (write)
-    hipLaunchKernelGGL((kv_write_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_write_kernel<BITS, D, NH>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((kv_read_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_read_kernel<BITS, D, NH>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
   return hipGetLastError();
 }
 
 template <int BITS>
 hipError_t launch_rows_bits(int d, const RowArgs &a, bool write, hipStream_t s) {
   switch (d) {
-    case 64: return launch_rows<BITS, 64>(a, write, s);
-    case 128: return launch_rows<BITS, 128>(a, write, s);
-    case 256: return launch_rows<BITS, 256>(a, write, s);
+    case 64: return launch_rows<BITS, 64, 1>(a, write, s);
+    case 128: return launch_rows<BITS, 128, 1>(a, write, s);
+    case 256: return launch_rows<BITS, 256, 1>(a, write, s);
   }
   return hipErrorInvalidValue;
 }
