@@ -84,9 +84,8 @@ SIGNATURES = {
     "wq_attn_decode_workspace": (_sz, [ctypes.POINTER(WqKvCache), _i64, _i32, _i64, _i64]),
     "wq_attn_decode": (_i32, [ctypes.POINTER(WqKvCache), _vp, _i64, _i32, _i64, _vp, _i64, _vp, _i64, _i64,
                               ctypes.c_float, _vp, _i64, _vp, _sz, _vp]),
-    "wq_rope": (_i32, [_i32, ctypes.POINTER(_vp), ctypes.POINTER(_i64), ctypes.POINTER(_vp),
-                       ctypes.POINTER(_i64), ctypes.POINTER(_i32), _i64, _i32, _i32, _vp, _vp, _i64, _vp,
-                       _i64, _i32, _vp, _u32, _vp]),
+    "wq_rope": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _vp,
+                       _u32, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 64 << 20   # WQ_NOALLOC_SCRATCH_BYTES
 
@@ -124,8 +123,15 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current stream's handle (without building a Stream object where
+    torch can give the handle itself: 0.2 us instead of 2.6)."""
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dev(t: torch.Tensor, dtype, name: str):
@@ -466,14 +472,21 @@ def wq_attn_decode(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: t
         max_len = held
     elif max_len > held:
         raise ValueError(f"max_len={max_len}: {table.shape[1]} pages of {cache.page_size} tokens hold {held}")
-    y = torch.empty((seqs, cols), dtype=torch.float16, device=q.device) if out is None else _rows(out, cols, "out")
-    if y.shape[0] != seqs:
-        raise ValueError(f"out: {y.shape[0]} rows for {seqs} sequences")
+    if out is None:
+        y = torch.empty_like(q) if q.is_contiguous() else torch.empty((seqs, cols), dtype=torch.float16, device=q.device)
+    else:
+        y = _rows(out, cols, "out")
+        if y.shape[0] != seqs:
+            raise ValueError(f"out: {y.shape[0]} rows for {seqs} sequences")
     heads = cols // cache.head_dim
+    wp, wn = None, 0
     if workspace is None:
-        need = wq_attn_decode_workspace(cache, seqs, heads, max_len, window)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        wn = wq_attn_decode_workspace(cache, seqs, heads, max_len, window)
+        if wn:
+            workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
+            wp = workspace.data_ptr()
+    else:
+        wp, wn = workspace.data_ptr(), workspace.numel()
     _check("wq_attn_decode", lib().wq_attn_decode(
         cache._ref, q.data_ptr(), _ld(q), heads, seqs, table.data_ptr(), table.stride(0) if seqs > 1 else table.shape[1],
         lens.data_ptr(), max_len, window, cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), _ld(y),
@@ -497,22 +510,34 @@ def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, po
     axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
     if pair_axis is not None and len(pair_axis) != half:
         raise ValueError(f"pair_axis: {len(pair_axis)} entries for {half} pairs")
-    ys = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs] if out is None else list(out)
-    if len(ys) != len(xs):
-        raise ValueError(f"out: {len(ys)} arrays for {len(xs)}")
-    for t in [*xs, *ys]:
-        _rows(t, t.shape[-1], "xs and out")
-        if t.shape[0] != tokens or t.shape[1] % head_dim:
-            raise ValueError(f"an array of {tuple(t.shape)} is not [{tokens}][heads * {head_dim}]")
-    if any(x.shape != y.shape for x, y in zip(xs, ys)):
-        raise ValueError("out must have the shapes of xs")
+    for x in xs:
+        cols = x.shape[-1]
+        _rows(x, cols, "xs")
+        if x.shape[0] != tokens or cols % head_dim:
+            raise ValueError(f"an array of {tuple(x.shape)} is not [{tokens}][heads * {head_dim}]")
+    if out is None:
+        ys = [torch.empty_like(x) if x.is_contiguous() else
+              torch.empty(x.shape, dtype=torch.float16, device=x.device) for x in xs]
+    else:
+        ys = list(out)
+        if len(ys) != len(xs):
+            raise ValueError(f"out: {len(ys)} arrays for {len(xs)}")
+        for x, y in zip(xs, ys):
+            _rows(y, x.shape[1], "out")
+            if y.shape[0] != tokens:
+                raise ValueError(f"out: {y.shape[0]} rows for {tokens} tokens")
     c = len(ys)
+    # x, ldx, y, ldy and heads as the call's five arrays, in one block
+    ptrs = (_i64 * (4 * c))(*[x.data_ptr() for x in xs], *[_ld(x) for x in xs],
+                            *[y.data_ptr() for y in ys], *[_ld(y) for y in ys])
+    heads = (_i32 * c)(*[x.shape[1] // head_dim for x in xs])
+    at = ctypes.addressof(ptrs)
+    if pair_axis is not None and not isinstance(pair_axis, bytes):
+        pair_axis = bytes(pair_axis)
     _check("wq_rope", lib().wq_rope(
-        c, (_vp * c)(*[x.data_ptr() for x in xs]), (_i64 * c)(*[_ld(x) for x in xs]),
-        (_vp * c)(*[y.data_ptr() for y in ys]), (_i64 * c)(*[_ld(y) for y in ys]),
-        (_i32 * c)(*[x.shape[1] // head_dim for x in xs]), tokens, head_dim, 2 * half, cos.data_ptr(),
-        sin.data_ptr(), rows, positions.data_ptr(), tokens, axes,
-        None if pair_axis is None else bytes(pair_axis), WQ_ROPE_ADJACENT if adjacent else 0, _stream()))
+        c, at, at + 8 * c, at + 16 * c, at + 24 * c, heads, tokens, head_dim, 2 * half, cos.data_ptr(),
+        sin.data_ptr(), rows, positions.data_ptr(), tokens, axes, pair_axis,
+        WQ_ROPE_ADJACENT if adjacent else 0, _stream()))
     return ys
 
 
