@@ -197,7 +197,9 @@ wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, u
       a.pair_axis[i] = pair_axis[i];
     }
   int64_t all = 0;
+  int32_t most = 0;
   for (int i = 0; i < count; ++i) {
+    if (heads[i] > most) most = heads[i];
     if (heads[i] <= 0) return set_error(WQ_E_ARG, "%s: heads[%d]=%d must be positive", who, i, heads[i]);
     all += heads[i];
     const int64_t row = (int64_t)heads[i] * head_dim;
@@ -214,7 +216,7 @@ wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, u
       return set_error(WQ_E_ARG, "%s: in place needs ldx == ldy", who);
     a.arr[i] = {x[i], y[i], ldx[i], ldy[i], heads[i]};
   }
-  if (tokens > INT32_MAX / 64 || all * (head_dim / 8) > INT32_MAX || (tokens && all * (head_dim / 8) > ((int64_t)1 << 38) / tokens))
+  if (tokens > INT32_MAX / 64 || most > 65535)
     return set_error(WQ_E_UNSUPPORTED, "%s: tokens=%lld, heads=%lld too many for one call", who, (long long)tokens,
                      (long long)all);
   if (tokens == 0) return WQ_OK;

@@ -424,7 +424,7 @@ wq_status wq_attn_decode(const wq_kv_cache *cache, const uint16_t *q, int64_t ld
  *   pair_axis  HOST uint8 [rot / 2], each below axes, read during the call
  *              only; NULL: every pair on axis 0
  * head_dim a multiple of 8 up to 256, rot a multiple of 16 up to head_dim,
- * axes 1 to 4.  Errors as above. */
+ * axes 1 to 4, heads up to 65535.  Errors as above. */
 #define WQ_ROPE_ADJACENT 1u
 #define WQ_ROPE_MAX_AXES 4
 wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, uint16_t *const *y,
