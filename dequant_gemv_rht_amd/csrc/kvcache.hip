@@ -132,6 +132,11 @@ __device__ __forceinline__ void quad_to_rows(uint32_t (&w)[8 * BITS / 32]) {
   }
 }
 
+// v with its sign turned where the top bit of t is set
+__device__ __forceinline__ float flip(float v, uint32_t t) {
+  return __uint_as_float(__float_as_uint(v) ^ (t & 0x80000000u));
+}
+
 // A product rounded to fp32 where it stands: without this the compiler may
 // fold it into a following conversion to fp16, which then rounds once.
 __device__ __forceinline__ float rounded(float v) {
@@ -256,10 +261,18 @@ __device__ __forceinline__ void load_piece(const char *in, uint32_t (&w)[8 * BIT
   if constexpr (BITS == 4) w[0] = *reinterpret_cast<const uint32_t *>(in);
 }
 
+// a / b from r, the reciprocal of b, rounded as a division rounds it: one
+// correction by the remainder (Markstein's division), three operations
+// instead of a dozen.  b here is an fp16 value or a small whole number, so
+// neither the product nor the remainder leaves the normal range where the
+// quotient matters (below 2^-20 it rounds to the zero code either way).
+__device__ __forceinline__ float divide(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
 // Codes of a lane's channels, the row's scale and zero: the rule of
-// wq_kv_write.  The quotients x / scale come from the scale's correctly
-// rounded reciprocal with one correction by the remainder (Markstein's
-// division), three operations each instead of a dozen.
+// wq_kv_write.
 template <int BITS, int D, int SETS>
 __device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t (&w)[SETS][8 * BITS / 32]) {
   float lo = 0.0f, hi = 0.0f;
@@ -273,18 +286,17 @@ __device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t
   lo = row_min<D>(lo);
   hi = row_max<D>(hi);
   const float qmax = (float)((1 << BITS) - 1);
-  _Float16 s16 = (_Float16)fminf((hi - lo) / qmax, 65504.0f);
+  _Float16 s16 = (_Float16)fminf(divide(hi - lo, qmax, 1.0f / qmax), 65504.0f);
   if (s16 == (_Float16)0.0f) s16 = (_Float16)1.0f;
-  const float s = (float)s16, r = 1.0f / s;
-  const float z = fminf(fmaxf(rintf((0.0f - lo) / s), 0.0f), qmax);
+  const float s = (float)s16;
+  float r = __builtin_amdgcn_rcpf(s);
+  r = fmaf(fmaf(-s, r, 1.0f), r, r);
+  const float z = __builtin_amdgcn_fmed3f(rintf(divide(0.0f - lo, s, r)), 0.0f, qmax);
 #pragma unroll
   for (int b = 0; b < SETS; ++b) {
     float c[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q = v[b][e] * r;
-      c[e] = rintf(fmaf(fmaf(-q, s, v[b][e]), r, q) + z);
-    }
+    for (int e = 0; e < 8; ++e) c[e] = rintf(divide(v[b][e], s, r) + z);
     // whole numbers now; the conversion to a byte clamps to 0 .. 255
 #pragma unroll
     for (int e = 0; e < 8 * BITS / 32; ++e) w[b][e] = 0;
@@ -332,11 +344,11 @@ __device__ __forceinline__ void write_rows(const RowArgs &a, const Item<BITS, D,
         const uint32_t sb = flips[n][b] >> (it.c0 & 31);
         const int jj = threadIdx.x & 15;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[b][e] = ((sb >> e) & 1u) ? -v[b][e] : v[b][e];
+        for (int e = 0; e < 8; ++e) v[b][e] = flip(v[b][e], sb << (31 - e));
         fwht128_row16_signed(v[b], jj);
         const float sc = fwht_lane_sign(jj) * kInvSqrt128;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[b][e] = rounded(v[b][e] * sc);
+        for (int e = 0; e < 8; ++e) v[b][e] = BITS == 16 ? rounded(v[b][e] * sc) : v[b][e] * sc;
       }
     }
     uint32_t w[L::kSets][L::kWords];
@@ -427,7 +439,7 @@ __device__ __forceinline__ void read_rows(const RowArgs &a, const Item<BITS, D, 
         const float sc = fwht_lane_sign(jj) * kInvSqrt128;
         const uint32_t sb = flips[n][b] >> (it.c0 & 31);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * (((sb >> e) & 1u) ? -sc : sc));
+        for (int e = 0; e < 8; ++e) v[e] = rounded(flip(v[e] * sc, sb << (31 - e)));
       }
       if (live && it.head + L::kHeads * n < a.kv_heads)
         *reinterpret_cast<uint4 *>(pl.x + L::kHeads * n * D + 128 * b) =
