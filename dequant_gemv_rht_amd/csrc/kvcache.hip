@@ -71,6 +71,102 @@ __device__ __forceinline__ uint32_t bytes(uint32_t hi, uint32_t lo, uint32_t sel
   return __builtin_amdgcn_perm(hi, lo, sel);
 }
 
+__device__ __forceinline__ half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
+
+// 8 codes less their zero, as pairs (2 i, 2 i + 1) of fp16: whole numbers,
+// exact (0x6400 | c is 1024 + c).
+template <int BITS>
+__device__ __forceinline__ void codes_to_pairs(const uint32_t (&w)[8 * BITS / 32], _Float16 z, half2_t (&p)[4]) {
+  const half2_t bias = half2_t{(_Float16)1024.0f, (_Float16)1024.0f} + half2_t{z, z};
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = as_half2(bytes(0x64646464u, w[i / 2], i & 1 ? 0x04030402u : 0x04010400u)) - bias;
+  } else {
+    const uint32_t even = w[0] & 0x0F0F0F0Fu, odd = (w[0] >> 4) & 0x0F0F0F0Fu;   // channels 0, 2, 4, 6 and 1, 3, 5, 7
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = as_half2(bytes(odd, even, 0x0C000C00u + 0x00040000u + 0x00010001u * i) | 0x64006400u) - bias;
+  }
+}
+
+template <int BITS>
+__device__ __forceinline__ void codes_to_float(const uint32_t (&w)[8 * BITS / 32], _Float16 z, float (&v)[8]) {
+  half2_t p[4];
+  if constexpr (BITS == 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = as_half2(w[i]);
+  } else {
+    codes_to_pairs<BITS>(w, z, p);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = (float)p[e / 2][e & 1];
+}
+
+// One butterfly stage between lanes on pairs of fp16: partner + beta * mine
+template <int CTRL>
+__device__ __forceinline__ void pair_stage(half2_t (&p)[4], half2_t beta) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t mine = __builtin_bit_cast(uint32_t, p[i]);
+    uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)mine, CTRL, 0xF, 0xF, true);
+    if (CTRL == kRowHalfMirror) other = (uint32_t)__builtin_amdgcn_mov_dpp((int)other, kQuadRev, 0xF, 0xF, true);   // lane ^ 4
+    p[i] = __builtin_elementwise_fma(p[i], beta, as_half2(other));
+  }
+}
+
+// The 128-point transform of code - zero (fp16 values for 16 bits) times
+// (-1)^popcount(lane), as fwht128_row16_signed gives it.  Sums of whole
+// numbers stay whole: up to 2048 they are exact in fp16 pairs, half the
+// instructions of fp32.  That holds for all 128 codes of 4 bits (1920 at
+// most), and for 8 bits through the three stages inside a lane (2040).
+template <int BITS>
+__device__ __forceinline__ void hadamard_codes(const uint32_t (&w)[8 * BITS / 32], _Float16 z, int jj, float (&v)[8]) {
+  if constexpr (BITS == 16) {
+    codes_to_float<16>(w, z, v);
+    fwht128_row16_signed(v, jj);
+  } else {
+    half2_t p[4];
+    codes_to_pairs<BITS>(w, z, p);
+    const half2_t one_minus = {(_Float16)1.0f, (_Float16)-1.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = __builtin_elementwise_fma(half2_t{p[i][1], p[i][1]}, one_minus, half2_t{p[i][0], p[i][0]});
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const half2_t a = p[i], b = p[i + 1];
+      p[i] = a + b;
+      p[i + 1] = a - b;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const half2_t a = p[i], b = p[i + 2];
+      p[i] = a + b;
+      p[i + 2] = a - b;
+    }
+    if constexpr (BITS == 4) {
+      // stored = partner + beta mine, beta = -1 on the lane of the pair's
+      // second element: the transform itself; the sign that the fp32 form
+      // leaves is put on at the end
+      const half2_t b1 = half2_t{(_Float16)1.0f, (_Float16)1.0f};
+      pair_stage<kQuadXor1>(p, jj & 1 ? -b1 : b1);
+      pair_stage<kQuadXor2>(p, jj & 2 ? -b1 : b1);
+      pair_stage<kRowHalfMirror>(p, jj & 4 ? -b1 : b1);
+      pair_stage<kRowRor8>(p, jj & 8 ? -b1 : b1);
+      const float sign = fwht_lane_sign(jj);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)p[e / 2][e & 1] * sign;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)p[e / 2][e & 1];
+#if defined(__HIP_DEVICE_COMPILE__)
+      fwht_xstages_dpp(v, (jj & 1) ? -1.0f : 1.0f, (jj & 2) ? -1.0f : 1.0f, (jj & 4) ? -1.0f : 1.0f,
+                       (jj & 8) ? -1.0f : 1.0f);
+#endif
+    }
+  }
+}
+
 // Lane 16 t + c: 8 channels of token t as packed codes  <->  a quarter of the
 // quad, units 2 t' .. (8 bits, fp16) or t' (4 bits) of lane c's 8 channels,
 // the four tokens of each side by side.  Both directions are the transpose
@@ -420,26 +516,24 @@ __device__ __forceinline__ void read_rows(const RowArgs &a, const Item<BITS, D, 
   }
 #pragma unroll
   for (int n = 0; n < NH; ++n) {
+    const float s = half_bits_to_float(par[n] & 0xFFFF);
 #pragma unroll
     for (int b = 0; b < L::kSets; ++b) {
       if (it.is_v && quad) quad_to_rows<BITS>(w[n][b]);
       float v[8];
-      if constexpr (BITS == 16) {
-        unpack8(make_uint4(w[n][b][0], w[n][b][1], w[n][b][2], w[n][b][3]), v);
-      } else {
-        const float s = half_bits_to_float(par[n] & 0xFFFF), z = half_bits_to_float(par[n] >> 16);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = ((float)((w[n][b][e * BITS / 32] >> (e * BITS % 32)) & ((1u << BITS) - 1u)) - z) * s;
-      }
-      // rotated back: x = D H x' / sqrt(128) (H is symmetric)
       if (D >= 128 && a.signs) {
+        // x = D H (code - zero) (scale / sqrt(128)); H is symmetric
         const int jj = threadIdx.x & 15;
-        fwht128_row16_signed(v, jj);
-        const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+        hadamard_codes<BITS>(w[n][b], as_half2(par[n])[1], jj, v);
+        const float sc = fwht_lane_sign(jj) * (BITS == 16 ? kInvSqrt128 : rounded(s * kInvSqrt128));
         const uint32_t sb = flips[n][b] >> (it.c0 & 31);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = rounded(flip(v[e] * sc, sb << (31 - e)));
+      } else {
+        codes_to_float<BITS>(w[n][b], as_half2(par[n])[1], v);
+        if (BITS != 16)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * s);
       }
       if (live && it.head + L::kHeads * n < a.kv_heads)
         *reinterpret_cast<uint4 *>(pl.x + L::kHeads * n * D + 128 * b) =

@@ -95,10 +95,17 @@ def rotate_rows_f32(x, signs):
     return _hadamard_f32(x.astype(np.float32) * sg)
 
 
-def unrotate_rows_f32(x, signs):
+def unrotate_rows_f32(x, signs, scale=None):
+    """R^T x in single precision.  Coded rows: x is code - zero, whose
+    transform is a whole number (exact), and scale [tokens][heads] their
+    scales, each times 1/sqrt(128) and rounded before the one product."""
     _, heads, d = x.shape
     sg = signs_from_bits(signs, heads * d).astype(np.float32).reshape(heads, d)
-    return _hadamard_f32(x) * sg
+    if scale is None:
+        return _hadamard_f32(x) * sg
+    h = hadamard(128).astype(np.float64)
+    y = (x.astype(np.float64).reshape(-1, d // 128, 128) @ h).reshape(x.shape).astype(np.float32)
+    return y * (scale.astype(np.float32) * np.float32(0.08838834764831845))[..., None] * sg
 
 
 def code_rows(x, bits):

@@ -49,13 +49,19 @@ def _expect_read(host, slots, page, heads, d, bits):
     capacity = host["k"].shape[0] * page
     out = {}
     for which in "kv":
-        vals = OK.dequant_pages(which, host[which], host[which + "_params"], bits, d, page).astype(np.float32)
-        y = np.zeros((len(slots), heads, d), np.float32)
+        codes = OK.unpack_pages(which, host[which], bits, d, page).astype(np.float32)
+        scale = np.ones(codes.shape[:-1], np.float32)
+        if bits != 16:
+            scale = host[which + "_params"][..., 0].astype(np.float32)
+            codes = codes - host[which + "_params"][..., 1:].astype(np.float32)
+        y, sc = np.zeros((len(slots), heads, d), np.float32), np.zeros((len(slots), heads), np.float32)
         for i, slot in enumerate(slots):
             if 0 <= slot < capacity:
-                y[i] = vals[slot // page, :, slot % page]
+                y[i], sc[i] = codes[slot // page, :, slot % page], scale[slot // page, :, slot % page]
         if host["signs"] is not None:
-            y = OK.unrotate_rows_f32(y, host["signs"])
+            y = OK.unrotate_rows_f32(y, host["signs"], None if bits == 16 else sc)
+        elif bits != 16:
+            y = y * sc[..., None]
         out[which] = y.astype(np.float16).reshape(len(slots), -1)
     return out
 

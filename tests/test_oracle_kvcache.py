@@ -66,6 +66,10 @@ def test_rotation_is_the_hadamard_oracles():
     assert np.allclose(OK.rotate_rows_f32(x, signs), want, atol=1e-5)
     back = rht_inverse(want.reshape(3, 512), signs).reshape(3, 2, 256)
     assert np.allclose(OK.unrotate_rows_f32(want.astype(np.float32), signs), back, atol=1e-5)
+    codes, scale = rng.integers(-15, 16, (3, 2, 256)).astype(np.float32), rng.uniform(0.1, 1, (3, 2)).astype(np.float16)
+    vals = codes.astype(np.float64) * scale[..., None]
+    assert np.allclose(OK.unrotate_rows_f32(codes, signs, scale),
+                       rht_inverse(vals.reshape(3, 512), signs).reshape(3, 2, 256), atol=1e-5)
 
 
 def test_attend_direct():
