@@ -493,50 +493,81 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
   }
 }
 
-// Joins the splits of one (sequence, head): D / 8 lanes x 8 channels, the
-// other threads share the splits out.
+// Joins the splits of one (sequence, head).  16 lanes x 8 channels (D = 64:
+// 8 lanes) hold a split's sum, a workgroup 16 (32) splits at a time, and each
+// lane asks for kAhead of them before it looks at the first: the kernel is
+// one round trip to the partial sums long.
 template <int D>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, SplitPlan plan) {
-  constexpr int kLanes = D / 8, kParts = kAttnThreads / kLanes;
-  __shared__ float sh[kParts][D + 4], sh_m[kParts], sh_l[kParts];
+  constexpr int kLanes = D / 8, kParts = kAttnThreads / kLanes, kAhead = 4;
+  __shared__ float sh[kWaves][D + 4], sh_m[kWaves], sh_l[kWaves];
   const int all = a.kv_heads * a.group;
   const int head = blockIdx.x % all;
   const int64_t seq = blockIdx.x / all;
-  const int n = range_of(a, seq).splits(plan.split_len);
-  if (n <= 1) return;   // written by its one workgroup
   const int tid = threadIdx.x, part = tid / kLanes, c0 = 8 * (tid % kLanes);
   const int ch = head / a.group * D + c0;
   const uint32_t flips = D >= 128 && a.signs ? a.signs[ch >> 5] : 0u;
   const float *in = a.partial + (int64_t)blockIdx.x * plan.splits * (D + 4);
+  const int n = range_of(a, seq).splits(plan.split_len);
   float m = kNone, l = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = part; s < n; s += kParts) {
-    const float *p = in + (int64_t)s * (D + 4);
-    const f32x4 lo = *reinterpret_cast<const f32x4 *>(p + 4 + c0), hi = *reinterpret_cast<const f32x4 *>(p + 8 + c0);
-    const float ms = p[0], ls = p[1];
-    const float high = fmaxf(m, ms);
-    const float f = __builtin_amdgcn_exp2f(m - high), fs = __builtin_amdgcn_exp2f(ms - high);
-    m = high;
-    l = l * f + ls * fs;
+  f32x4 lo[kAhead], hi[kAhead];
+  float ms[kAhead], ls[kAhead];
+  for (int s0 = part; s0 < plan.splits; s0 += kParts * kAhead) {
+    // up to the plan's splits: inside the workspace, whatever n turns out to be
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] = v[e] * f + lo[e] * fs;
-      v[e + 4] = v[e + 4] * f + hi[e] * fs;
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = min(s0 + i * kParts, plan.splits - 1);
+      const float *p = in + (int64_t)s * (D + 4);
+      ms[i] = p[0];
+      ls[i] = p[1];
+      lo[i] = *reinterpret_cast<const f32x4 *>(p + 4 + c0);
+      hi[i] = *reinterpret_cast<const f32x4 *>(p + 8 + c0);
     }
-  }
-  if (c0 == 0) {
-    sh_m[part] = m;
-    sh_l[part] = l;
-  }
+    if (n <= 1) return;   // written by its one workgroup
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sh[part][c0 + e] = v[e];
+    for (int i = 0; i < kAhead; ++i) {
+      if (s0 + i * kParts >= n) continue;
+      const float high = fmaxf(m, ms[i]);
+      const float f = __builtin_amdgcn_exp2f(m - high), fs = __builtin_amdgcn_exp2f(ms[i] - high);
+      m = high;
+      l = l * f + ls[i] * fs;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = v[e] * f + lo[i][e] * fs;
+        v[e + 4] = v[e + 4] * f + hi[i][e] * fs;
+      }
+    }
+    if (s0 - part + kParts * kAhead >= n) break;
+  }
+  if (n <= 1) return;
+  // the parts of a wave, then the waves
+#pragma unroll
+  for (int o = kLanes; o < 64; o <<= 1) {
+    const float mo = __shfl_xor(m, o), lo2 = __shfl_xor(l, o), high = fmaxf(m, mo);
+    const float f = __builtin_amdgcn_exp2f(m - high), fo = __builtin_amdgcn_exp2f(mo - high);
+    m = high;
+    l = l * f + lo2 * fo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * f + __shfl_xor(v[e], o) * fo;
+  }
+  const int wave = tid >> 6;
+  if ((tid & 63) < kLanes) {
+    if (c0 == 0) {
+      sh_m[wave] = m;
+      sh_l[wave] = l;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sh[wave][c0 + e] = v[e];
+  }
   __syncthreads();
   if (tid >= kLanes) return;
   float high = kNone, total = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-  const int used = min(n, kParts);
-  for (int i = 0; i < used; ++i) high = fmaxf(high, sh_m[i]);
-  for (int i = 0; i < used; ++i) {
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) high = fmaxf(high, sh_m[i]);
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
     const float f = __builtin_amdgcn_exp2f(sh_m[i] - high);
     total += f * sh_l[i];
 #pragma unroll
