@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -124,6 +125,7 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream() -> int:
@@ -131,7 +133,7 @@ def _stream() -> int:
     torch can give the handle itself: 0.2 us instead of 2.6)."""
     if _raw_stream is None:
         return torch.cuda.current_stream().cuda_stream
-    return _raw_stream(torch.cuda.current_device())
+    return _raw_stream(_device())
 
 
 def _dev(t: torch.Tensor, dtype, name: str):
@@ -342,18 +344,34 @@ def wq_embed(table: QWeight, ids: torch.Tensor, out_dtype=torch.float16, out: Op
     return y
 
 
-def _rows(t: torch.Tensor, cols: int, name: str) -> torch.Tensor:
-    """fp16 GPU rows [n][cols], any row stride."""
-    if not t.is_cuda or t.dtype != torch.float16:
+# A decode step issues these calls every few microseconds, so the checks
+# below ask each tensor for as little as they can.
+_F16, _INT32 = torch.float16, torch.int32
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, row stride) of fp16 GPU rows with any row stride."""
+    if t.dtype is not _F16 or not t.is_cuda:
         raise ValueError(f"{name} must be a float16 GPU tensor")
-    if t.dim() != 2 or t.shape[1] != cols or (t.stride(1) != 1 and cols > 1):
-        raise ValueError(f"{name} must be [rows][{cols}] with contiguous rows, got {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be [rows][columns], got {tuple(shape)}")
+    rows, cols = shape
+    if t.is_contiguous():
+        return rows, cols, cols
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+    return rows, cols, t.stride(0) if rows > 1 else cols   # torch leaves a single row's stride arbitrary
+
+
+def _ints(t: torch.Tensor, name: str) -> torch.Tensor:
+    if t.dtype is not _INT32 or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 GPU tensor")
     return t
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride; torch leaves that of a single row arbitrary."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _new(rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(rows, cols, dtype=_F16, device=like.device)
 
 
 @dataclass
@@ -398,6 +416,8 @@ class KVCache:
                             _ptr(self.v), _ptr(self.k_params), _ptr(self.v_params), _ptr(self.signs),
                             128 if self.signs is not None else 0)
         self._ref = ctypes.byref(self._c)
+        self._cols = self.kv_heads * self.head_dim
+        self._workspace = {}     # wq_attn_decode_workspace by shape
 
     @classmethod
     def new(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int,
@@ -415,37 +435,42 @@ class KVCache:
 def wq_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
     """Code the rows of ``k`` and ``v`` (fp16 [tokens][kv_heads * head_dim]) into
     the cache at ``slots`` (int32 [tokens]; outside the cache: skipped)."""
-    cols = cache.kv_heads * cache.head_dim
-    _rows(k, cols, "k")
-    _rows(v, cols, "v")
-    _dev(slots, torch.int32, "slots")
-    n = slots.numel()
-    if k.shape[0] != n or v.shape[0] != n:
-        raise ValueError(f"{k.shape[0]} key and {v.shape[0]} value rows for {n} slots")
-    _check("wq_kv_write", lib().wq_kv_write(cache._ref, k.data_ptr(), _ld(k), v.data_ptr(), _ld(v),
-                                            slots.data_ptr(), n, _stream()))
+    rows_k, cols_k, ldk = _rows(k, "k")
+    rows_v, cols_v, ldv = _rows(v, "v")
+    n = _ints(slots, "slots").numel()
+    if cols_k != cache._cols or cols_v != cache._cols or rows_k != n or rows_v != n:
+        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} are not [{n} slots][{cache._cols} channels]")
+    _check("wq_kv_write", lib().wq_kv_write(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, slots.data_ptr(), n,
+                                            _stream()))
 
 
 def wq_kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None):
     """The cached rows at ``slots`` as fp16: (k, v), each [tokens][kv_heads * head_dim]."""
-    _dev(slots, torch.int32, "slots")
-    n, cols = slots.numel(), cache.kv_heads * cache.head_dim
+    n, cols = _ints(slots, "slots").numel(), cache._cols
     if out is None:
-        k = torch.empty((n, cols), dtype=torch.float16, device=slots.device)
-        v = torch.empty_like(k)
+        k, v = _new(n, cols, slots), _new(n, cols, slots)
+        ldk = ldv = cols
     else:
-        k, v = _rows(out[0], cols, "out[0]"), _rows(out[1], cols, "out[1]")
-        if k.shape[0] != n or v.shape[0] != n:
-            raise ValueError(f"out: {k.shape[0]} and {v.shape[0]} rows for {n} slots")
-    _check("wq_kv_read", lib().wq_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), _ld(k), v.data_ptr(),
-                                          _ld(v), _stream()))
+        k, v = out
+        rows_k, cols_k, ldk = _rows(k, "out[0]")
+        rows_v, cols_v, ldv = _rows(v, "out[1]")
+        if cols_k != cols or cols_v != cols or rows_k != n or rows_v != n:
+            raise ValueError(f"out {tuple(k.shape)} and {tuple(v.shape)} are not [{n} slots][{cols} channels]")
+    _check("wq_kv_read", lib().wq_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                                          _stream()))
     return k, v
 
 
 def wq_attn_decode_workspace(cache: KVCache, seqs: int, q_heads: int, max_len: int, window: int = 0) -> int:
-    size = lib().wq_attn_decode_workspace(cache._ref, seqs, q_heads, max_len, window)
-    if size == ctypes.c_size_t(-1).value:
-        raise WqError("wq_attn_decode_workspace", WQ_E_ARG, lib().wq_last_error().decode())
+    key = (seqs, q_heads, max_len, window)
+    size = cache._workspace.get(key)
+    if size is None:
+        size = lib().wq_attn_decode_workspace(cache._ref, seqs, q_heads, max_len, window)
+        if size == ctypes.c_size_t(-1).value:
+            raise WqError("wq_attn_decode_workspace", WQ_E_ARG, lib().wq_last_error().decode())
+        if len(cache._workspace) >= 4096:
+            cache._workspace.clear()
+        cache._workspace[key] = size
     return size
 
 
@@ -457,41 +482,49 @@ def wq_attn_decode(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: t
     ``lens`` (int32 [seqs]) name.  ``max_len``: an upper bound of the lengths
     (default: what the table's pages hold); ``scale``: default
     head_dim ** -0.5."""
-    seqs, cols = q.shape
-    _rows(q, cols, "q")
-    if cols % cache.head_dim:
-        raise ValueError(f"q: {cols} columns are not heads of {cache.head_dim}")
-    if not (table.is_cuda and lens.is_cuda) or table.dtype != torch.int32 or lens.dtype != torch.int32:
-        raise ValueError("table and lens must be int32 GPU tensors")
-    if table.dim() != 2 or table.shape[0] != seqs or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError(f"table must be [{seqs}][pages] with contiguous rows, got {tuple(table.shape)}")
-    if lens.shape != (seqs,) or (seqs > 1 and lens.stride(0) != 1):
-        raise ValueError(f"lens must be [{seqs}], got {tuple(lens.shape)}")
-    held = table.shape[1] * cache.page_size
-    if max_len is None:
-        max_len = held
-    elif max_len > held:
-        raise ValueError(f"max_len={max_len}: {table.shape[1]} pages of {cache.page_size} tokens hold {held}")
-    if out is None:
-        y = torch.empty_like(q) if q.is_contiguous() else torch.empty((seqs, cols), dtype=torch.float16, device=q.device)
-    else:
-        y = _rows(out, cols, "out")
-        if y.shape[0] != seqs:
-            raise ValueError(f"out: {y.shape[0]} rows for {seqs} sequences")
+    seqs, cols, ldq = _rows(q, "q")
     heads = cols // cache.head_dim
-    wp, wn = None, 0
+    if heads * cache.head_dim != cols:
+        raise ValueError(f"q: {cols} columns are not heads of {cache.head_dim}")
+    if table.dtype is not _INT32 or not table.is_cuda:
+        raise ValueError("table must be an int32 GPU tensor")
+    shape = table.shape
+    if len(shape) != 2 or shape[0] != seqs:
+        raise ValueError(f"table must be [{seqs}][pages], got {tuple(shape)}")
+    pages = ld_table = shape[1]
+    if not table.is_contiguous():
+        if pages > 1 and table.stride(1) != 1:
+            raise ValueError(f"table must have contiguous rows, got strides {table.stride()}")
+        if seqs > 1:
+            ld_table = table.stride(0)
+    if _ints(lens, "lens").shape != (seqs,):
+        raise ValueError(f"lens must be [{seqs}], got {tuple(lens.shape)}")
+    if max_len is None:
+        max_len = pages * cache.page_size
+    elif max_len > pages * cache.page_size:
+        raise ValueError(f"max_len={max_len}: {pages} pages of {cache.page_size} tokens hold {pages * cache.page_size}")
+    if out is None:
+        y, ldo = _new(seqs, cols, q), cols
+    else:
+        y = out
+        rows_y, cols_y, ldo = _rows(y, "out")
+        if rows_y != seqs or cols_y != cols:
+            raise ValueError(f"out must be [{seqs}][{cols}], got {tuple(y.shape)}")
     if workspace is None:
-        wn = wq_attn_decode_workspace(cache, seqs, heads, max_len, window)
+        wp, wn = None, wq_attn_decode_workspace(cache, seqs, heads, max_len, window)
         if wn:
             workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
             wp = workspace.data_ptr()
     else:
-        wp, wn = workspace.data_ptr(), workspace.numel()
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check("wq_attn_decode", lib().wq_attn_decode(
-        cache._ref, q.data_ptr(), _ld(q), heads, seqs, table.data_ptr(), table.stride(0) if seqs > 1 else table.shape[1],
-        lens.data_ptr(), max_len, window, cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), _ld(y),
-        wp, wn, _stream()))
+        cache._ref, q.data_ptr(), ldq, heads, seqs, table.data_ptr(), ld_table, lens.data_ptr(), max_len, window,
+        cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), ldo, wp, wn, _stream()))
     return y
+
+
+_PACK64 = [struct.Struct(f"{c}q") for c in range(WQ_MAX_BATCH + 1)]
+_PACK32 = [struct.Struct(f"{c}i") for c in range(WQ_MAX_BATCH + 1)]
 
 
 def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
@@ -503,40 +536,45 @@ def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, po
     of each pair.  ``out`` may be ``xs`` itself (in place)."""
     _dev(cos, torch.float32, "cos")
     _dev(sin, torch.float32, "sin")
-    _dev(positions, torch.int32, "positions")
-    if cos.dim() != 2 or cos.shape != sin.shape:
-        raise ValueError(f"cos and sin must be [rows][rot / 2], got {tuple(cos.shape)} and {tuple(sin.shape)}")
-    rows, half = cos.shape
-    axes, tokens = (1, positions.shape[0]) if positions.dim() == 1 else positions.shape
-    if pair_axis is not None and len(pair_axis) != half:
-        raise ValueError(f"pair_axis: {len(pair_axis)} entries for {half} pairs")
-    for x in xs:
-        cols = x.shape[-1]
-        _rows(x, cols, "xs")
-        if x.shape[0] != tokens or cols % head_dim:
-            raise ValueError(f"an array of {tuple(x.shape)} is not [{tokens}][heads * {head_dim}]")
-    if out is None:
-        ys = [torch.empty_like(x) if x.is_contiguous() else
-              torch.empty(x.shape, dtype=torch.float16, device=x.device) for x in xs]
-    else:
-        ys = list(out)
-        if len(ys) != len(xs):
-            raise ValueError(f"out: {len(ys)} arrays for {len(xs)}")
-        for x, y in zip(xs, ys):
-            _rows(y, x.shape[1], "out")
-            if y.shape[0] != tokens:
-                raise ValueError(f"out: {y.shape[0]} rows for {tokens} tokens")
-    c = len(ys)
-    # x, ldx, y, ldy and heads as the call's five arrays, in one block
-    ptrs = (_i64 * (4 * c))(*[x.data_ptr() for x in xs], *[_ld(x) for x in xs],
-                            *[y.data_ptr() for y in ys], *[_ld(y) for y in ys])
-    heads = (_i32 * c)(*[x.shape[1] // head_dim for x in xs])
-    at = ctypes.addressof(ptrs)
-    if pair_axis is not None and not isinstance(pair_axis, bytes):
+    shape = _ints(positions, "positions").shape
+    axes, tokens = shape if len(shape) == 2 else (1, positions.numel())
+    shape = cos.shape
+    if len(shape) != 2 or shape != sin.shape:
+        raise ValueError(f"cos and sin must be [rows][rot / 2], got {tuple(shape)} and {tuple(sin.shape)}")
+    rows, half = shape
+    if pair_axis is not None:
+        if len(pair_axis) != half:
+            raise ValueError(f"pair_axis: {len(pair_axis)} entries for {half} pairs")
         pair_axis = bytes(pair_axis)
+    if head_dim <= 0:
+        raise ValueError(f"head_dim={head_dim} must be positive")
+    count = len(xs)
+    if not 0 < count <= WQ_MAX_BATCH or (out is not None and len(out) != count):
+        raise ValueError(f"xs: {count} arrays (1 to {WQ_MAX_BATCH}), and as many in out")
+    ys, px, ldx, py, ldy, heads = [], [], [], [], [], []
+    for i, x in enumerate(xs):
+        n, cols, ld = _rows(x, "xs")
+        h = cols // head_dim
+        if n != tokens or h * head_dim != cols:
+            raise ValueError(f"an array of {tuple(x.shape)} is not [{tokens}][heads * {head_dim}]")
+        px.append(x.data_ptr())
+        ldx.append(ld)
+        heads.append(h)
+        if out is None:
+            y = _new(n, cols, x)
+            ld = cols
+        else:
+            y = out[i]
+            rows_y, cols_y, ld = _rows(y, "out")
+            if rows_y != n or cols_y != cols:
+                raise ValueError(f"out must be [{n}][{cols}], got {tuple(y.shape)}")
+        ys.append(y)
+        py.append(y.data_ptr())
+        ldy.append(ld)
+    p64 = _PACK64[count].pack
     _check("wq_rope", lib().wq_rope(
-        c, at, at + 8 * c, at + 16 * c, at + 24 * c, heads, tokens, head_dim, 2 * half, cos.data_ptr(),
-        sin.data_ptr(), rows, positions.data_ptr(), tokens, axes, pair_axis,
+        count, p64(*px), p64(*ldx), p64(*py), p64(*ldy), _PACK32[count].pack(*heads), tokens, head_dim, 2 * half,
+        cos.data_ptr(), sin.data_ptr(), rows, positions.data_ptr(), tokens, axes, pair_axis,
         WQ_ROPE_ADJACENT if adjacent else 0, _stream()))
     return ys
 

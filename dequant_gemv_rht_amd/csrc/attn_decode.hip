@@ -493,26 +493,31 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
   }
 }
 
-// Joins the splits of one (sequence, head).  16 lanes x 8 channels (D = 64:
-// 8 lanes) hold a split's sum, a workgroup 16 (32) splits at a time, and each
-// lane asks for kAhead of them before it looks at the first: the kernel is
-// one round trip to the partial sums long.
-template <int D>
+// Joins the splits of a (sequence, head).  D / 8 lanes x 8 channels hold a
+// split's sum, so a wave takes 64 / (D / 8) splits at a time, and each lane
+// asks for kAhead of them before it looks at the first: the kernel is one
+// round trip to the partial sums long.  HW waves share a head: one where it
+// holds all the plan's splits that way, else four that meet in LDS.
+constexpr int kAhead = 4;
+template <int D, int HW>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, SplitPlan plan) {
-  constexpr int kLanes = D / 8, kParts = kAttnThreads / kLanes, kAhead = 4;
+  constexpr int kLanes = D / 8, kParts = 64 * HW / kLanes;
   __shared__ float sh[kWaves][D + 4], sh_m[kWaves], sh_l[kWaves];
   const int all = a.kv_heads * a.group;
-  const int head = blockIdx.x % all;
-  const int64_t seq = blockIdx.x / all;
-  const int tid = threadIdx.x, part = tid / kLanes, c0 = 8 * (tid % kLanes);
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int64_t id = HW == 1 ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x;
+  if (id >= a.seqs * all) return;
+  const int head = (int)(id % all);
+  const int64_t seq = id / all;
+  const int part = (tid & (64 * HW - 1)) / kLanes, c0 = 8 * (tid % kLanes);
   const int ch = head / a.group * D + c0;
   const uint32_t flips = D >= 128 && a.signs ? a.signs[ch >> 5] : 0u;
-  const float *in = a.partial + (int64_t)blockIdx.x * plan.splits * (D + 4);
+  const float *in = a.partial + id * plan.splits * (D + 4);
   const int n = range_of(a, seq).splits(plan.split_len);
   float m = kNone, l = 0.0f, v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  f32x4 lo[kAhead], hi[kAhead];
-  float ms[kAhead], ls[kAhead];
   for (int s0 = part; s0 < plan.splits; s0 += kParts * kAhead) {
+    f32x4 lo[kAhead], hi[kAhead];
+    float ms[kAhead], ls[kAhead];
     // up to the plan's splits: inside the workspace, whatever n turns out to be
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -540,40 +545,41 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Spl
     if (s0 - part + kParts * kAhead >= n) break;
   }
   if (n <= 1) return;
-  // the parts of a wave, then the waves
 #pragma unroll
   for (int o = kLanes; o < 64; o <<= 1) {
-    const float mo = __shfl_xor(m, o), lo2 = __shfl_xor(l, o), high = fmaxf(m, mo);
+    const float mo = __shfl_xor(m, o), lx = __shfl_xor(l, o), high = fmaxf(m, mo);
     const float f = __builtin_amdgcn_exp2f(m - high), fo = __builtin_amdgcn_exp2f(mo - high);
     m = high;
-    l = l * f + lo2 * fo;
+    l = l * f + lx * fo;
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] * f + __shfl_xor(v[e], o) * fo;
   }
-  const int wave = tid >> 6;
-  if ((tid & 63) < kLanes) {
-    if (c0 == 0) {
-      sh_m[wave] = m;
-      sh_l[wave] = l;
+  if (HW > 1) {
+    if ((tid & 63) < kLanes) {
+      if (c0 == 0) {
+        sh_m[wave] = m;
+        sh_l[wave] = l;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sh[wave][c0 + e] = v[e];
     }
+    __syncthreads();
+    m = kNone;
+    l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sh[wave][c0 + e] = v[e];
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) m = fmaxf(m, sh_m[i]);
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      const float f = __builtin_amdgcn_exp2f(sh_m[i] - m);
+      l += f * sh_l[i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += f * sh[i][c0 + e];
+    }
   }
-  __syncthreads();
-  if (tid >= kLanes) return;
-  float high = kNone, total = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) high = fmaxf(high, sh_m[i]);
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    const float f = __builtin_amdgcn_exp2f(sh_m[i] - high);
-    total += f * sh_l[i];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += f * sh[i][c0 + e];
-  }
-  const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+  if ((tid & (64 * HW - 1)) >= kLanes) return;
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] *= inv;
   store_row<D>(a, v, seq, flips >> (ch & 31), head, c0);
@@ -609,9 +615,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
   const int64_t wgs = a.seqs * a.kv_heads * p.qtiles * p.splits;
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL((attn_split_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
-  if (p.splits > 1)
-    hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)(a.seqs * a.kv_heads * a.group)), dim3(kAttnThreads), 0, s, a,
-                       p);
+  if (p.splits > 1) {
+    const int64_t rows = a.seqs * a.kv_heads * a.group;
+    if (p.splits <= 64 / (D / 8) * kAhead)
+      hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kAttnThreads), 0, s,
+                         a, p);
+    else
+      hipLaunchKernelGGL((attn_join_kernel<D, kWaves>), dim3((unsigned)rows), dim3(kAttnThreads), 0, s, a, p);
+  }
   return hipGetLastError();
 }
 
