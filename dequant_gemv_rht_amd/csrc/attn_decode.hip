@@ -45,7 +45,7 @@ typedef const __attribute__((address_space(4))) int32_t *const_i32;   // scalar 
 constexpr int kAttnThreads = 256, kWaves = 4;
 constexpr int kStep = 32;            // tokens per wave and step
 constexpr int kMinSplit = kWaves * kStep;
-constexpr int kMaxSplit = 2048;
+constexpr int kMaxSplit = 5120;
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 constexpr float kNone = -1e30f;      // no term seen yet
 constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
@@ -585,24 +585,36 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Spl
   store_row<D>(a, v, seq, flips >> (ch & 31), head, c0);
 }
 
-constexpr int64_t kWorkgroups = 512;   // two a CU
+// Workgroups that a call is split into where its sequences and heads alone
+// make fewer: one a CU where a row is 256 bytes or more (such a workgroup
+// keeps enough bytes on the way: 42 MB of 8-bit heads of 256 take 16.8 us
+// with 256 workgroups, 18.5 with 512), two a CU below that (33 MB of 4-bit
+// heads of 128: 16.5 and 15.2 us; four a CU 18.6).
+int64_t workgroups(int bits, int d) { return d * bits / 8 >= 256 ? 256 : 512; }
 
 int64_t seen_at_most(int64_t max_len, int64_t window) {
   return window > 0 && window + 15 < max_len ? window + 15 : max_len;
 }
 
-// How a call is split: enough workgroups to fill the card, runs of at most
-// kMaxSplit tokens so that one long sequence among short ones is shared out.
-SplitPlan plan_for(int64_t seqs, int kv_heads, int group, int64_t max_len, int64_t window) {
+// How a call is split: enough workgroups to fill the card, in runs of one
+// length, at most kMaxSplit tokens each.  A workgroup costs about 0.8 us of
+// its CU beside its tokens (64 x 8 heads of 16381 int8 tokens: 353 us in
+// runs of 4096, 365 of 2048, 379 of 1024), so runs are long where there are
+// workgroups enough, and bounded so that one long sequence among many short
+// ones is still shared out.
+SplitPlan plan_for(int bits, int d, int64_t seqs, int kv_heads, int group, int64_t max_len, int64_t window) {
   SplitPlan p;
   p.qtiles = (group + 15) / 16;
   const int64_t seen = seen_at_most(max_len, window);
   const int64_t units = seqs * kv_heads * p.qtiles;
-  const int64_t want = (kWorkgroups + units - 1) / units;
-  int64_t len = (seen + want - 1) / want;
+  const int64_t want = (workgroups(bits, d) + units - 1) / units;
+  int64_t splits = (seen + kMinSplit - 1) / kMinSplit;
+  if (splits > want) splits = want;
+  if (splits < (seen + kMaxSplit - 1) / kMaxSplit) splits = (seen + kMaxSplit - 1) / kMaxSplit;
+  if (splits < 1) splits = 1;
+  int64_t len = (seen + splits - 1) / splits;   // runs of one length
   len = (len + kMinSplit - 1) / kMinSplit * kMinSplit;
   if (len < kMinSplit) len = kMinSplit;
-  if (len > kMaxSplit) len = kMaxSplit;
   p.split_len = (int32_t)len;
   p.splits = (int32_t)((seen + len - 1) / len);
   if (p.splits < 1) p.splits = 1;
@@ -611,7 +623,7 @@ SplitPlan plan_for(int64_t seqs, int kv_heads, int group, int64_t max_len, int64
 
 template <int BITS, int D>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  const SplitPlan p = plan_for(a.seqs, a.kv_heads, a.group, a.max_len, a.window);
+  const SplitPlan p = plan_for(BITS, D, a.seqs, a.kv_heads, a.group, a.max_len, a.window);
   const int64_t wgs = a.seqs * a.kv_heads * p.qtiles * p.splits;
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL((attn_split_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
@@ -640,13 +652,13 @@ hipError_t launch_bits(int d, const AttnArgs &a, hipStream_t s) {
 
 size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window) {
   // a bound that grows with seqs and max_len: plan_for gives units * splits
-  // below units + kWorkgroups unless runs are of kMaxSplit tokens, and none
+  // below units + workgroups() unless runs are of kMaxSplit tokens, and none
   // shorter than kMinSplit
   const int64_t group = q_heads / c.kv_heads, qtiles = (group + 15) / 16, units = seqs * c.kv_heads * qtiles;
   const int64_t seen = seen_at_most(max_len, window);
   if (seen <= kMinSplit) return 0;
   const int64_t few = units * ((seen + kMinSplit - 1) / kMinSplit), many = units * ((seen + kMaxSplit - 1) / kMaxSplit);
-  const int64_t filled = units + kWorkgroups > many ? units + kWorkgroups : many;
+  const int64_t fill = units + workgroups(c.bits, c.head_dim), filled = fill > many ? fill : many;
   const int64_t runs = few < filled ? few : filled;
   return (size_t)((runs * group + qtiles - 1) / qtiles) * (size_t)(c.head_dim + 4) * sizeof(float);
 }
