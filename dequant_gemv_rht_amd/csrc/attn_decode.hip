@@ -135,6 +135,15 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+constexpr float kLowScale = 2048.0f;   // of a query's low part
+
+template <int BITS>
+__device__ __forceinline__ uint4 pack_query(const float (&v)[8]) {
+  if (BITS == 4)
+    return make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]), pack_half2(v[3], v[7]));
+  return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+}
+
 struct SplitPlan {
   int32_t splits, split_len, qtiles;
 };
@@ -260,7 +269,11 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
     n1 = entry_at(t + kStride + 16);
   }
 
-  // the queries: rotated as the cache is, rounded to fp16, in the keys' channel order
+  // The queries, rotated as the cache is, rounded to fp16, in the keys'
+  // channel order.  A rotated query is no longer an fp16 value: with at most
+  // 8 heads, what the rounding leaves (times 2^11) goes to columns 8 to 15,
+  // and its scores are added to the heads' own.
+  const bool split_q = D >= 128 && a.signs && heads <= 8;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int h = (tid + i * kAttnThreads) / (D / 8), c0 = 8 * (tid % (D / 8));
@@ -279,12 +292,14 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= sc;
     }
-    uint4 w;
-    if (BITS == 4)
-      w = make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]), pack_half2(v[3], v[7]));
-    else
-      w = make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
+    const uint4 w = pack_query<BITS>(v);
+    if (split_q && h >= 8) continue;
     *reinterpret_cast<uint4 *>(&sh.q[h][c0]) = w;
+    if (split_q) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] - (float)(_Float16)v[e]) * kLowScale;
+      *reinterpret_cast<uint4 *>(&sh.q[h + 8][c0]) = pack_query<BITS>(v);
+    }
   }
   __syncthreads();
   half8_t q[F::kKeyMfma];
@@ -326,6 +341,10 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
 #pragma unroll
       for (int mm = 0; mm < F::kKeyMfma; ++mm)
         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm, nib), q[mm], acc, 0, 0, 0);
+      if (split_q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(dpp<kRowRor8>(acc[i]), 1.0f / kLowScale, acc[i]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[4 * b + i] = acc[i] * to_log2;
     }
