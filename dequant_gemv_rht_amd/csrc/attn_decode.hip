@@ -51,7 +51,9 @@ constexpr float kNone = -1e30f;      // no term seen yet
 constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
 
 // waves per SIMD that the registers are kept for without spilling
-constexpr int occupancy(int bits, int d) { return d <= 128 ? 3 : bits == 16 ? 1 : 2; }
+constexpr int occupancy(int bits, int d, bool low) {
+  return d <= 128 ? (low ? 2 : 3) : bits == 16 || low ? 1 : 2;
+}
 
 template <int BITS, int D>
 struct Fmt {
@@ -176,12 +178,14 @@ __device__ __forceinline__ Range range_of(const AttnArgs &a, int64_t seq) {
   return r;
 }
 
-template <int BITS, int D>
-__global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_kernel(AttnArgs a, SplitPlan plan) {
+// LOW: the low parts of rotated queries are operands of their own (more than
+// 8 heads, no columns left for them).
+template <int BITS, int D, bool LOW>
+__global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_split_kernel(AttnArgs a, SplitPlan plan) {
   using F = Fmt<BITS, D>;
   constexpr int kQStride = D + 8, kOStride = D + 4;
   __shared__ union {
-    _Float16 q[16][kQStride];
+    _Float16 q[LOW ? 32 : 16][kQStride];
     float o[kWaves][16][kOStride];
   } sh;
   __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
@@ -270,10 +274,11 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
   }
 
   // The queries, rotated as the cache is, rounded to fp16, in the keys'
-  // channel order.  A rotated query is no longer an fp16 value: with at most
-  // 8 heads, what the rounding leaves (times 2^11) goes to columns 8 to 15,
-  // and its scores are added to the heads' own.
-  const bool split_q = D >= 128 && a.signs && heads <= 8;
+  // channel order.  A rotated query is no longer an fp16 value: what the
+  // rounding leaves (times 2^11) goes to columns 8 to 15 where there are at
+  // most 8 heads, else to operands of its own, and its scores are added to
+  // the heads' own.
+  const bool split_q = !LOW && D >= 128 && a.signs && heads <= 8;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const int h = (tid + i * kAttnThreads) / (D / 8), c0 = 8 * (tid % (D / 8));
@@ -295,22 +300,28 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
     const uint4 w = pack_query<BITS>(v);
     if (split_q && h >= 8) continue;
     *reinterpret_cast<uint4 *>(&sh.q[h][c0]) = w;
-    if (split_q) {
+    if (split_q || LOW) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = (v[e] - (float)(_Float16)v[e]) * kLowScale;
-      *reinterpret_cast<uint4 *>(&sh.q[h + 8][c0]) = pack_query<BITS>(v);
+      *reinterpret_cast<uint4 *>(&sh.q[h + (LOW ? 16 : 8)][c0]) = pack_query<BITS>(v);
     }
   }
   __syncthreads();
-  half8_t q[F::kKeyMfma];
-  float qsum = 0.0f;
+  half8_t q[F::kKeyMfma], ql[LOW ? F::kKeyMfma : 1];
+  float qsum = 0.0f, lsum = 0.0f;
 #pragma unroll
   for (int m = 0; m < F::kKeyMfma; ++m) {
     q[m] = *reinterpret_cast<const half8_t *>(&sh.q[col][F::key_channel(m, g)]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) qsum += (float)q[m][e];
+    if constexpr (LOW) {
+      ql[m] = *reinterpret_cast<const half8_t *>(&sh.q[16 + col][F::key_channel(m, g)]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lsum += (float)ql[m][e];
+    }
   }
   qsum = column_sum(qsum);
+  if (LOW) lsum = column_sum(lsum);
   __syncthreads();   // sh.q is free for sh.o
 
   float m = kNone, l = 0.0f;
@@ -341,6 +352,18 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D)) void attn_split_k
 #pragma unroll
       for (int mm = 0; mm < F::kKeyMfma; ++mm)
         acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm, nib), q[mm], acc, 0, 0, 0);
+      if constexpr (LOW) {
+        f32x4 low = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (BITS != 16)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            low[i] = (F::kBias + (float)as_half2(ks.par[b][i])[1]) * ((BITS == 4 ? -16.0f : -1.0f) * lsum);
+#pragma unroll
+        for (int mm = 0; mm < F::kKeyMfma; ++mm)
+          low = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm, nib), ql[mm], low, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(low[i], 1.0f / kLowScale, acc[i]);
+      }
       if (split_q) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = fmaf(dpp<kRowRor8>(acc[i]), 1.0f / kLowScale, acc[i]);
@@ -645,7 +668,14 @@ hipError_t launch(const AttnArgs &a, hipStream_t s) {
   const SplitPlan p = plan_for(BITS, D, a.seqs, a.kv_heads, a.group, a.max_len, a.window);
   const int64_t wgs = a.seqs * a.kv_heads * p.qtiles * p.splits;
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((attn_split_kernel<BITS, D>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+  if constexpr (D >= 128) {
+    if (a.signs && a.group > 8)
+      hipLaunchKernelGGL((attn_split_kernel<BITS, D, true>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+    else
+      hipLaunchKernelGGL((attn_split_kernel<BITS, D, false>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+  } else {
+    hipLaunchKernelGGL((attn_split_kernel<BITS, D, false>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+  }
   if (p.splits > 1) {
     const int64_t rows = a.seqs * a.kv_heads * a.group;
     if (p.splits <= 64 / (D / 8) * kAhead)

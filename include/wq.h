@@ -379,8 +379,7 @@ wq_status wq_kv_read(const wq_kv_cache *cache, const int32_t *slots, int64_t tok
  * table[b][t / page_size].  The new token's own key and value are expected
  * in the cache already (wq_kv_write first, lens counting it).  Scores,
  * softmax and sums are fp32; the queries and the softmax weights enter the
- * products as fp16.  A rotated query enters as two fp16 parts (22 bits)
- * where up to 8 query heads share a key-value head, else rounded to one.
+ * products as fp16, a rotated query as two fp16 parts (22 bits).
  *   q        fp16 [seqs][ldq]: q_heads rows of head_dim; q_heads a multiple
  *            of kv_heads
  *   table    device int32 [seqs][ld_table] page numbers; only entries of
