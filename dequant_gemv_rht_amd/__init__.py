@@ -370,8 +370,12 @@ def _ints(t: torch.Tensor, name: str) -> torch.Tensor:
     return t
 
 
-def _new(rows: int, cols: int, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(rows, cols, dtype=_F16, device=like.device)
+def _new(rows: int, cols: int, device) -> torch.Tensor:
+    return torch.empty(rows, cols, dtype=_F16, device=device)
+
+
+def _new_like(x: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
+    return torch.empty_like(x) if x.is_contiguous() else _new(rows, cols, x.device)
 
 
 @dataclass
@@ -448,7 +452,8 @@ def wq_kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Sequence[torch
     """The cached rows at ``slots`` as fp16: (k, v), each [tokens][kv_heads * head_dim]."""
     n, cols = _ints(slots, "slots").numel(), cache._cols
     if out is None:
-        k, v = _new(n, cols, slots), _new(n, cols, slots)
+        k = _new(n, cols, slots.device)
+        v = torch.empty_like(k)
         ldk = ldv = cols
     else:
         k, v = out
@@ -504,7 +509,7 @@ def wq_attn_decode(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: t
     elif max_len > pages * cache.page_size:
         raise ValueError(f"max_len={max_len}: {pages} pages of {cache.page_size} tokens hold {pages * cache.page_size}")
     if out is None:
-        y, ldo = _new(seqs, cols, q), cols
+        y, ldo = _new_like(q, seqs, cols), cols
     else:
         y = out
         rows_y, cols_y, ldo = _rows(y, "out")
@@ -561,7 +566,7 @@ def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, po
         ldx.append(ld)
         heads.append(h)
         if out is None:
-            y = _new(n, cols, x)
+            y = _new_like(x, n, cols)
             ld = cols
         else:
             y = out[i]
