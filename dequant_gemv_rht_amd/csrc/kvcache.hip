@@ -14,6 +14,11 @@
 // otherwise, as in a decode step, each token's units go one by one.  The
 // tokens' slots may start anywhere in a quad, so waves look for quads among
 // the slots rather than at multiples of four.
+//
+// What bounds it: vector instructions (about 200 to code 8 channels of a
+// lane, 130 to read them back; traffic alone would allow two thirds of the
+// time), so whatever does not depend on the token is kept out of the loop
+// over a wave's quads: the signs, the lane's offsets, the head.
 #include "wq_internal.h"
 
 namespace wq {
@@ -115,8 +120,9 @@ __device__ __forceinline__ void pair_stage(half2_t (&p)[4], half2_t beta) {
   }
 }
 
-// The 128-point transform of code - zero (fp16 values for 16 bits) times
-// (-1)^popcount(lane), as fwht128_row16_signed gives it.  Sums of whole
+// The 128-point transform of code - zero (fp16 values for 16 bits); 8 and 16
+// bits times (-1)^popcount(lane), which fwht128_row16_signed leaves to the
+// caller's scale (lane_sign below).  Sums of whole
 // numbers stay whole: up to 2048 they are exact in fp16 pairs, half the
 // instructions of fp32.  That holds for all 128 codes of 4 bits (1920 at
 // most), and for 8 bits through the three stages inside a lane (2040).
@@ -146,16 +152,14 @@ __device__ __forceinline__ void hadamard_codes(const uint32_t (&w)[8 * BITS / 32
     }
     if constexpr (BITS == 4) {
       // stored = partner + beta mine, beta = -1 on the lane of the pair's
-      // second element: the transform itself; the sign that the fp32 form
-      // leaves is put on at the end
+      // second element: the transform itself
       const half2_t b1 = half2_t{(_Float16)1.0f, (_Float16)1.0f};
       pair_stage<kQuadXor1>(p, jj & 1 ? -b1 : b1);
       pair_stage<kQuadXor2>(p, jj & 2 ? -b1 : b1);
       pair_stage<kRowHalfMirror>(p, jj & 4 ? -b1 : b1);
       pair_stage<kRowRor8>(p, jj & 8 ? -b1 : b1);
-      const float sign = fwht_lane_sign(jj);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (float)p[e / 2][e & 1] * sign;
+      for (int e = 0; e < 8; ++e) v[e] = (float)p[e / 2][e & 1];
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = (float)p[e / 2][e & 1];
@@ -228,9 +232,12 @@ __device__ __forceinline__ void quad_to_rows(uint32_t (&w)[8 * BITS / 32]) {
   }
 }
 
-// v with its sign turned where the top bit of t is set
-__device__ __forceinline__ float flip(float v, uint32_t t) {
-  return __uint_as_float(__float_as_uint(v) ^ (t & 0x80000000u));
+// The rotation's signs of a lane's 8 channels as sign bits of packed fp16
+// pairs (an exclusive or turns them).
+__device__ __forceinline__ void sign_masks(uint32_t bits8, uint32_t (&m)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    m[i] = (((bits8 >> (2 * i)) & 1u) << 15) | (((bits8 >> (2 * i + 1)) & 1u) << 31);
 }
 
 // A product rounded to fp32 where it stands: without this the compiler may
@@ -258,83 +265,87 @@ struct RowArgs {
   int32_t kv_heads, page_shift, capacity;   // capacity: pages * page_size
 };
 
-// The four tokens 4 j .. 4 j + 3 are the wave's window.  `quad` >= 0: the
-// token of the call that starts the full quad of slots beginning in the
-// window; `rest`: bit t set where token 4 j + t has a slot in the cache and
-// lies in no full quad of the call; `outside`: where its slot is not one of
-// the cache's.
-struct Window {
-  int64_t quad;
-  uint32_t rest, outside;
+// A wave's span: 4 NW tokens of the call from `first`.  Bit t stands for
+// token first + t: `quads`, a full quad of slots starts there; `rest`, its
+// slot is one of the cache's and in no full quad of the call; `outside`, its
+// slot is not one of the cache's.
+template <int NW>
+struct Span {
+  static constexpr int kLanes = NW == 1 ? 16 : 32;
+  int64_t first;
+  int32_t slot;                 // lane i: the slot of token first - 3 + i
+  uint32_t quads, rest, outside;
+  __device__ Span(const RowArgs &a, int64_t span) {
+    static_assert(4 * NW + 6 <= kLanes, "three tokens on either side of the span");
+    first = 4 * NW * span;
+    const int i = threadIdx.x & (kLanes - 1);
+    const int64_t token = first - 3 + i;
+    const bool real = token >= 0 && token < a.tokens && i < 4 * NW + 6;
+    slot = real ? a.slots[token] : -1;
+    const bool in = slot >= 0 && slot < a.capacity;
+    // every lane takes part in the shuffles
+    const int32_t s1 = __shfl_down(slot, 1, kLanes), s2 = __shfl_down(slot, 2, kLanes), s3 = __shfl_down(slot, 3, kLanes);
+    const bool start = in && (slot & 3) == 0 && s1 == slot + 1 && s2 == slot + 2 && s3 == slot + 3;
+    constexpr uint32_t kMine = (1u << (4 * NW)) - 1u;
+    const uint32_t starts = (uint32_t)__ballot(start) & ((kMine << 3) | 7u);
+    const uint32_t covered = starts | (starts << 1) | (starts << 2) | (starts << 3);
+    quads = (starts >> 3) & kMine;
+    rest = (((uint32_t)__ballot(in) & ~covered) >> 3) & kMine;
+    outside = ((uint32_t)__ballot(!in && real) >> 3) & kMine;
+  }
+  __device__ int32_t slot_of(int t) const { return __builtin_amdgcn_readlane(slot, t + 3); }
 };
-__device__ __forceinline__ Window find_window(const RowArgs &a, int64_t j) {
-  // lane i of a row of 16 looks at token 4 j - 3 + i
-  const int i = threadIdx.x & 15;
-  const int64_t token = 4 * j - 3 + i;
-  const int32_t slot = token >= 0 && token < a.tokens && i < 10 ? a.slots[token] : -1;
-  const bool in = slot >= 0 && slot < a.capacity;
-  // every lane takes part in the shuffles
-  const int32_t s1 = __shfl_down(slot, 1, 16), s2 = __shfl_down(slot, 2, 16), s3 = __shfl_down(slot, 3, 16);
-  const bool start = in && (slot & 3) == 0 && s1 == slot + 1 && s2 == slot + 2 && s3 == slot + 3;
-  const uint32_t starts = (uint32_t)__ballot(start) & 0x7Fu;
-  const uint32_t covered = starts | (starts << 1) | (starts << 2) | (starts << 3);
-  Window w;
-  w.quad = starts >> 3 ? 4 * j + __builtin_ctz(starts >> 3) : -1;
-  w.rest = (((uint32_t)__ballot(in) & ~covered) >> 3) & 0xFu;
-  w.outside = ((uint32_t)__ballot(!in && token >= 0 && token < a.tokens) >> 3) & 0xFu;
-  return w;
-}
 
-// A wave's work: a window of four tokens, keys or values, and NH heads (pairs
-// of heads of 64 channels), one after the other from `head` on.
-template <int BITS, int D, int NH>
+// A wave's work: a span of tokens, keys or values, one head (a pair of heads
+// of 64 channels), and what a lane keeps over the span.
+template <int BITS, int D, int NW>
 struct Item {
-  int64_t window;
-  int head, c0;
-  bool is_v;
+  using L = Layout<BITS, D>;
+  int64_t span;
+  int head, c0, t;              // t: the lane's token of four
+  bool is_v, live;
+  char *codes;                  // the head's first page
+  uint32_t *par;
+  uint16_t *x;                  // the caller's row of token 0
+  int64_t ld, page_codes, page_par;
+  uint32_t signs[L::kSets][4];
+  bool rotated;
   __device__ explicit Item(const RowArgs &a) {
-    using L = Layout<BITS, D>;
-    const int64_t id = (int64_t)blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
-    const int groups = (a.kv_heads + L::kHeads * NH - 1) / (L::kHeads * NH);
+    const int64_t id = (int64_t)blockIdx.x * (kRowThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int groups = (a.kv_heads + L::kHeads - 1) / L::kHeads;
     is_v = id & 1;
-    window = (id >> 1) / groups;
-    head = (int)((id >> 1) % groups) * L::kHeads * NH;
+    span = (id >> 1) / groups;
+    head = (int)((id >> 1) % groups) * L::kHeads;
     const int lane = threadIdx.x & 15;
+    t = (threadIdx.x >> 4) & 3;
     c0 = 8 * lane;
     if (L::kHeads == 2) {
       head += lane >> 3;
       c0 = 8 * (lane & 7);
     }
+    live = head < a.kv_heads;
+    const int h = live ? head : 0;
+    const int64_t head_codes = ((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift, head_par = (int64_t)1 << a.page_shift;
+    codes = static_cast<char *>(is_v ? a.v : a.k) + h * head_codes;
+    par = (is_v ? a.v_params : a.k_params) + h * head_par;
+    page_codes = head_codes * a.kv_heads;
+    page_par = head_par * a.kv_heads;
+    x = (is_v ? a.xv : a.xk) + (int64_t)h * D + c0;
+    ld = is_v ? a.ldv : a.ldk;
+    rotated = D >= 128 && a.signs;
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      const int ch = h * D + c0 + 128 * b;
+      sign_masks(rotated ? a.signs[ch >> 5] >> (ch & 31) : 0u, signs[b]);
+    }
   }
-};
-
-// Where the lane's row of each head is: its codes (keys, or one token's
-// units of a quad), its scale and zero, and the caller's row.
-template <int BITS, int D>
-struct Place {
-  char *codes;
-  uint32_t *par;
-  uint16_t *x;
-  int64_t head_codes, head_par;   // from one head to the next
-  int t;
-  template <int NH>
-  __device__ Place(const RowArgs &a, const Item<BITS, D, NH> &it, int64_t token, int32_t slot) {
-    using L = Layout<BITS, D>;
-    t = slot & ((1 << a.page_shift) - 1);
-    head_codes = ((int64_t)L::kUnits * L::kUnitBytes) << a.page_shift;
-    head_par = (int64_t)1 << a.page_shift;
-    const int64_t ph = (int64_t)(slot >> a.page_shift) * a.kv_heads + it.head;
-    codes = static_cast<char *>(it.is_v ? a.v : a.k) + ph * head_codes;
-    par = (it.is_v ? a.v_params : a.k_params) + ph * head_par + t;
-    x = (it.is_v ? a.xv + token * a.ldv : a.xk + token * a.ldk) + (int64_t)it.head * D + it.c0;
-  }
-  // byte offset of the lane's channels of set b
-  __device__ int64_t at(bool is_v, bool quad, int c0, int b) const {
-    using L = Layout<BITS, D>;
+  // byte offset, in the lane's head and page, of its channels of set b of
+  // token `at`, or of its quarter of the quad that starts there
+  __device__ int64_t piece(int at, bool quad, int b) const {
     const int u = (c0 + 128 * b) / (BITS == 4 ? 2 : 1);
-    if (!is_v) return L::kUnitBytes * L::key_unit(t, u);
-    if (quad) return L::kUnitBytes * L::value_unit(t & ~3, u + (BITS == 4 ? 1 : 2) * (int)((threadIdx.x >> 4) & 3));
-    return L::kUnitBytes * L::value_unit(t, u);
+    if (!is_v) return L::kUnitBytes * L::key_unit(at, u);
+    if (quad) return L::kUnitBytes * L::value_unit(at, u + (BITS == 4 ? 1 : 2) * t);
+    return L::kUnitBytes * L::value_unit(at, u);
   }
 };
 
@@ -406,70 +417,133 @@ __device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t
       for (int e = 0; e < 8; e += 2) w[b][0] = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(c[e + 1], 16.0f, c[e]), e / 2, w[b][0]);
     }
   }
-  return pack_half2(s, z);
+  return cvt_pk_half2(s, z);
 }
 
-template <int BITS, int D, int NH>
-__device__ __forceinline__ void write_rows(const RowArgs &a, const Item<BITS, D, NH> &it, int64_t token, bool live,
-                                           bool quad) {
+// The lane's 8 channels (or two sets of them): given fp16 -> codes and the
+// row's scale and zero.
+template <int BITS, int D, int NW>
+__device__ __forceinline__ uint32_t code_lane(const Item<BITS, D, NW> &it, const uint4 (&raw)[Layout<BITS, D>::kSets],
+                                              uint32_t (&w)[Layout<BITS, D>::kSets][Layout<BITS, D>::kWords]) {
   using L = Layout<BITS, D>;
-  const Place<BITS, D> pl(a, it, token, live ? a.slots[token] : 0);
-  uint4 raw[NH][L::kSets];
-  uint32_t flips[NH][L::kSets];
+  float v[L::kSets][8];
 #pragma unroll
-  for (int n = 0; n < NH; ++n) {
-    const int head = it.head + L::kHeads * n;
+  for (int b = 0; b < L::kSets; ++b) {
+    const uint32_t(&m)[4] = it.signs[b];
+    unpack8(make_uint4(raw[b].x ^ m[0], raw[b].y ^ m[1], raw[b].z ^ m[2], raw[b].w ^ m[3]), v[b]);
+    if (it.rotated) {
+      const int jj = threadIdx.x & 15;
+      fwht128_row16_signed(v[b], jj);
+      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
 #pragma unroll
-    for (int b = 0; b < L::kSets; ++b) {
-      raw[n][b] = make_uint4(0, 0, 0, 0);
-      flips[n][b] = 0;
-      if (live && head < a.kv_heads) {
-        raw[n][b] = *reinterpret_cast<const uint4 *>(pl.x + L::kHeads * n * D + 128 * b);
-        if (D >= 128 && a.signs) flips[n][b] = a.signs[(head * D + it.c0 + 128 * b) >> 5];
-      }
+      for (int e = 0; e < 8; ++e) v[b][e] = BITS == 16 ? rounded(v[b][e] * sc) : v[b][e] * sc;
+    }
+  }
+  if constexpr (BITS == 16) {
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[b][e] = cvt_pk_half2(v[b][2 * e], v[b][2 * e + 1]);
+    return 0;
+  } else {
+    return code_row<BITS, D, L::kSets>(v, w);
+  }
+}
+
+// codes -> fp16 rows
+template <int BITS, int D, int NW>
+__device__ __forceinline__ u32x4 decode_lane(const Item<BITS, D, NW> &it, const uint32_t (&w)[Layout<BITS, D>::kWords],
+                                             uint32_t par, int b) {
+  float v[8];
+  const float s = half_bits_to_float(par & 0xFFFF);
+  float sc = s;
+  if (it.rotated) {
+    // x = D H (code - zero) (scale / sqrt(128)); H is symmetric
+    const int jj = threadIdx.x & 15;
+    hadamard_codes<BITS>(w, as_half2(par)[1], jj, v);
+    sc = BITS == 16 ? kInvSqrt128 : rounded(s * kInvSqrt128);
+    if (BITS != 4) sc *= fwht_lane_sign(jj);
+  } else {
+    codes_to_float<BITS>(w, as_half2(par)[1], v);
+  }
+  if (BITS != 16 || it.rotated)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * sc);
+  u32x4 y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = cvt_pk_half2(v[2 * e], v[2 * e + 1]) ^ it.signs[b][e];
+  return y;
+}
+
+template <int BITS, int D, int NW>
+__global__ __launch_bounds__(kRowThreads) void kv_write_kernel(RowArgs a) {
+  using L = Layout<BITS, D>;
+  const Item<BITS, D, NW> it(a);
+  if (4 * NW * it.span >= a.tokens) return;   // whole waves leave together
+  const Span<NW> sp(a, it.span);
+  const int mask = (1 << a.page_shift) - 1;
+
+  // the quads: all rows asked for before the first is coded
+  int at[NW];
+  uint4 raw[NW][L::kSets];
+  const int count = __builtin_popcount(sp.quads);
+  uint32_t left = sp.quads;
+  if (count) {
+#pragma unroll
+    for (int n = 0; n < NW; ++n) {
+      at[n] = left ? __builtin_ctz(left) : at[n ? n - 1 : 0];   // past the last: the last again
+      left &= left - 1;
+#pragma unroll
+      for (int b = 0; b < L::kSets; ++b)
+        raw[n][b] = *reinterpret_cast<const uint4 *>(it.x + (sp.first + at[n] + it.t) * it.ld + 128 * b);
     }
   }
 #pragma unroll
-  for (int n = 0; n < NH; ++n) {
-    const bool mine = live && it.head + L::kHeads * n < a.kv_heads;
-    float v[L::kSets][8];
+  for (int n = 0; n < NW; ++n) {
+    if (n >= count) break;
+    const int32_t slot = sp.slot_of(at[n]);
+    const int64_t page = slot >> a.page_shift;
+    const int t0 = slot & mask;
+    uint32_t w[L::kSets][L::kWords];
+    const uint32_t par = code_lane<BITS, D, NW>(it, raw[n], w);
+    if (BITS != 16 && it.live && it.c0 == 0) it.par[page * it.page_par + t0 + it.t] = par;
+    char *to = it.codes + page * it.page_codes;
 #pragma unroll
     for (int b = 0; b < L::kSets; ++b) {
-      unpack8(raw[n][b], v[b]);
-      if (D >= 128 && a.signs) {
-        const uint32_t sb = flips[n][b] >> (it.c0 & 31);
-        const int jj = threadIdx.x & 15;
+      if (it.is_v) rows_to_quad<BITS>(w[b]);
+      if (it.live) store_piece<BITS>(to + it.piece(it.is_v ? t0 : t0 + it.t, true, b), w[b]);
+    }
+  }
+
+  // tokens in no quad, four at a time
+#pragma unroll 1
+  for (int n = 0; n < NW; ++n) {
+    const uint32_t four = (sp.rest >> (4 * n)) & 0xFu;
+    if (!four) continue;
+    const bool mine = ((four >> it.t) & 1u) && it.live;
+    const int64_t token = sp.first + 4 * n + it.t;
+    const int32_t slot = mine ? a.slots[token] : 0;
+    uint4 one[L::kSets];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[b][e] = flip(v[b][e], sb << (31 - e));
-        fwht128_row16_signed(v[b], jj);
-        const float sc = fwht_lane_sign(jj) * kInvSqrt128;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[b][e] = BITS == 16 ? rounded(v[b][e] * sc) : v[b][e] * sc;
-      }
+    for (int b = 0; b < L::kSets; ++b) {
+      one[b] = make_uint4(0, 0, 0, 0);
+      if (mine) one[b] = *reinterpret_cast<const uint4 *>(it.x + token * it.ld + 128 * b);
     }
     uint32_t w[L::kSets][L::kWords];
-    if constexpr (BITS == 16) {
-#pragma unroll
-      for (int b = 0; b < L::kSets; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[b][e] = pack_half2(v[b][2 * e], v[b][2 * e + 1]);
-    } else {
-      const uint32_t par = code_row<BITS, D, L::kSets>(v, w);
-      if (mine && it.c0 == 0) pl.par[L::kHeads * n * pl.head_par] = par;
-    }
-    char *out = pl.codes + L::kHeads * n * pl.head_codes;
-    constexpr int kStep = BITS == 4 ? 2 : 1;   // channels of a unit
+    const uint32_t par = code_lane<BITS, D, NW>(it, one, w);
+    if (!mine) continue;
+    const int64_t page = slot >> a.page_shift;
+    const int t0 = slot & mask;
+    if (BITS != 16 && it.c0 == 0) it.par[page * it.page_par + t0] = par;
 #pragma unroll
     for (int b = 0; b < L::kSets; ++b) {
-      if (it.is_v && quad) rows_to_quad<BITS>(w[b]);
-      char *to = out + pl.at(it.is_v, quad, it.c0, b);
-      if (!mine) continue;
-      if (!it.is_v || quad) {
+      char *to = it.codes + page * it.page_codes + it.piece(t0, false, b);
+      if (!it.is_v) {
         store_piece<BITS>(to, w[b]);
         continue;
       }
 #pragma unroll
-      for (int e = 0; e < 8 / kStep; ++e) {   // one token of a quad
+      for (int e = 0; e < (BITS == 4 ? 4 : 8); ++e) {   // a unit each, the quad's other tokens between them
         if constexpr (BITS == 16)
           reinterpret_cast<uint16_t *>(to)[4 * e] = (uint16_t)(w[b][e / 2] >> (16 * (e & 1)));
         else
@@ -479,96 +553,81 @@ __device__ __forceinline__ void write_rows(const RowArgs &a, const Item<BITS, D,
   }
 }
 
-template <int BITS, int D, int NH>
-__device__ __forceinline__ void read_rows(const RowArgs &a, const Item<BITS, D, NH> &it, int64_t token, bool live,
-                                          bool in, bool quad) {
-  using L = Layout<BITS, D>;
-  const Place<BITS, D> pl(a, it, token, in ? a.slots[token] : 0);
-  constexpr int kStep = BITS == 4 ? 2 : 1;
-  uint32_t w[NH][L::kSets][L::kWords], par[NH], flips[NH][L::kSets];
-#pragma unroll
-  for (int n = 0; n < NH; ++n) {
-    const int head = it.head + L::kHeads * n;
-    const bool mine = in && head < a.kv_heads;
-    const char *from = pl.codes + L::kHeads * n * pl.head_codes;
-    par[n] = 0;
-    if (BITS != 16 && mine) par[n] = pl.par[L::kHeads * n * pl.head_par];
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b) {
-#pragma unroll
-      for (int e = 0; e < L::kWords; ++e) w[n][b][e] = 0;
-      flips[n][b] = 0;
-      if (!mine) continue;
-      if (D >= 128 && a.signs) flips[n][b] = a.signs[(head * D + it.c0 + 128 * b) >> 5];
-      const char *p = from + pl.at(it.is_v, quad, it.c0, b);
-      if (!it.is_v || quad) {
-        load_piece<BITS>(p, w[n][b]);
-        continue;
-      }
-#pragma unroll
-      for (int e = 0; e < 8 / kStep; ++e) {
-        if constexpr (BITS == 16)
-          w[n][b][e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[4 * e] << (16 * (e & 1));
-        else
-          w[n][b][e / 4] |= (uint32_t)(uint8_t)p[4 * e] << (8 * (e & 3));
-      }
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < NH; ++n) {
-    const float s = half_bits_to_float(par[n] & 0xFFFF);
-#pragma unroll
-    for (int b = 0; b < L::kSets; ++b) {
-      if (it.is_v && quad) quad_to_rows<BITS>(w[n][b]);
-      float v[8];
-      if (D >= 128 && a.signs) {
-        // x = D H (code - zero) (scale / sqrt(128)); H is symmetric
-        const int jj = threadIdx.x & 15;
-        hadamard_codes<BITS>(w[n][b], as_half2(par[n])[1], jj, v);
-        const float sc = fwht_lane_sign(jj) * (BITS == 16 ? kInvSqrt128 : rounded(s * kInvSqrt128));
-        const uint32_t sb = flips[n][b] >> (it.c0 & 31);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = rounded(flip(v[e] * sc, sb << (31 - e)));
-      } else {
-        codes_to_float<BITS>(w[n][b], as_half2(par[n])[1], v);
-        if (BITS != 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = rounded(v[e] * s);
-      }
-      if (live && it.head + L::kHeads * n < a.kv_heads) {
-        const u32x4 y = {pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7])};
-        u32x4 *to = reinterpret_cast<u32x4 *>(pl.x + L::kHeads * n * D + 128 * b);
-        // many rows: streamed past the caches (30011 int4 rows 44 -> 38 us)
-        if constexpr (NH > 1)
-          __builtin_nontemporal_store(y, to);
-        else
-          *to = y;
-      }
-    }
-  }
-}
-
-template <int BITS, int D, int NH>
-__global__ __launch_bounds__(kRowThreads) void kv_write_kernel(RowArgs a) {
-  const Item<BITS, D, NH> it(a);
-  if (4 * it.window >= a.tokens) return;   // whole waves leave together
-  const Window w = find_window(a, it.window);
-  const int t = (threadIdx.x >> 4) & 3;
-  if (w.quad >= 0) write_rows<BITS, D, NH>(a, it, w.quad + t, true, true);
-  if (w.rest) write_rows<BITS, D, NH>(a, it, 4 * it.window + t, (w.rest >> t) & 1u, false);
-}
-
-template <int BITS, int D, int NH>
+template <int BITS, int D, int NW>
 __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(RowArgs a) {
-  const Item<BITS, D, NH> it(a);
-  if (4 * it.window >= a.tokens) return;
-  const Window w = find_window(a, it.window);
-  const int t = (threadIdx.x >> 4) & 3;
-  if (w.quad >= 0) read_rows<BITS, D, NH>(a, it, w.quad + t, true, true, true);
+  using L = Layout<BITS, D>;
+  const Item<BITS, D, NW> it(a);
+  if (4 * NW * it.span >= a.tokens) return;
+  const Span<NW> sp(a, it.span);
+  const int mask = (1 << a.page_shift) - 1;
+  auto give = [&](int64_t token, const u32x4 &y, int b) {
+    u32x4 *to = reinterpret_cast<u32x4 *>(it.x + token * it.ld + 128 * b);
+    // many rows: streamed past the caches (30011 int4 rows 44 -> 38 us)
+    if constexpr (NW > 1)
+      __builtin_nontemporal_store(y, to);
+    else
+      *to = y;
+  };
+
+  int at[NW];
+  uint32_t w[NW][L::kSets][L::kWords], par[NW];
+  const int count = __builtin_popcount(sp.quads);
+  uint32_t left = sp.quads;
+  if (count) {
+#pragma unroll
+    for (int n = 0; n < NW; ++n) {
+      at[n] = left ? __builtin_ctz(left) : at[n ? n - 1 : 0];
+      left &= left - 1;
+      const int32_t slot = sp.slot_of(at[n]);
+      const int64_t page = slot >> a.page_shift;
+      const int t0 = slot & mask;
+      const char *from = it.codes + page * it.page_codes;
+      par[n] = BITS == 16 ? 0 : it.par[page * it.page_par + t0 + it.t];
+#pragma unroll
+      for (int b = 0; b < L::kSets; ++b) load_piece<BITS>(from + it.piece(it.is_v ? t0 : t0 + it.t, true, b), w[n][b]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NW; ++n) {
+    if (n >= count) break;
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      if (it.is_v) quad_to_rows<BITS>(w[n][b]);
+      const u32x4 y = decode_lane<BITS, D, NW>(it, w[n][b], par[n], b);
+      if (it.live) give(sp.first + at[n] + it.t, y, b);
+    }
+  }
+
   // tokens in no quad, those outside the cache (zeros) among them
-  if (w.rest | w.outside) {
-    const bool in = (w.rest >> t) & 1u;
-    read_rows<BITS, D, NH>(a, it, 4 * it.window + t, in || ((w.outside >> t) & 1u), in, false);
+#pragma unroll 1
+  for (int n = 0; n < NW; ++n) {
+    const uint32_t four = (sp.rest >> (4 * n)) & 0xFu, none = (sp.outside >> (4 * n)) & 0xFu;
+    if (!(four | none)) continue;
+    const bool mine = ((four >> it.t) & 1u) && it.live;
+    const int64_t token = sp.first + 4 * n + it.t;
+    const int32_t slot = mine ? a.slots[token] : 0;
+    const int64_t page = slot >> a.page_shift;
+    const int t0 = slot & mask;
+    const uint32_t one = BITS != 16 && mine ? it.par[page * it.page_par + t0] : 0u;
+#pragma unroll
+    for (int b = 0; b < L::kSets; ++b) {
+      const char *from = it.codes + page * it.page_codes + it.piece(t0, false, b);
+      uint32_t c[L::kWords];
+#pragma unroll
+      for (int e = 0; e < L::kWords; ++e) c[e] = 0;
+      if (mine && !it.is_v) load_piece<BITS>(from, c);
+      if (mine && it.is_v) {
+#pragma unroll
+        for (int e = 0; e < (BITS == 4 ? 4 : 8); ++e) {
+          if constexpr (BITS == 16)
+            c[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(from)[4 * e] << (16 * (e & 1));
+          else
+            c[e / 4] |= (uint32_t)(uint8_t)from[4 * e] << (8 * (e & 3));
+        }
+      }
+      const u32x4 y = decode_lane<BITS, D, NW>(it, c, one, b);
+      if (it.live && (((four | none) >> it.t) & 1u)) give(token, y, b);
+    }
   }
 }
 
@@ -593,22 +652,21 @@ RowArgs row_args(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, con
   return a;
 }
 
-template <int BITS, int D, int NH>
+template <int BITS, int D, int NW>
 hipError_t launch_rows(const RowArgs &a, bool write, hipStream_t s) {
-  constexpr int kHeads = Layout<BITS, D>::kHeads * NH;
-  const int64_t waves = (a.tokens + 3) / 4 * ((a.kv_heads + kHeads - 1) / kHeads) * 2;
-  // several heads a wave once that still gives every SIMD two waves
-  if constexpr (NH == 1) {
+  constexpr int kHeads = Layout<BITS, D>::kHeads;
+  const int64_t waves = (a.tokens + 4 * NW - 1) / (4 * NW) * ((a.kv_heads + kHeads - 1) / kHeads) * 2;
+  // several quads a wave once that still gives every SIMD two waves
+  if constexpr (NW == 1) {
     constexpr int kMore = D == 256 ? 2 : 4;
-    if (waves >= kManyWaves * kMore && a.kv_heads > Layout<BITS, D>::kHeads)
-      return launch_rows<BITS, D, kMore>(a, write, s);
+    if (waves >= kManyWaves * kMore) return launch_rows<BITS, D, kMore>(a, write, s);
   }
   const int64_t wgs = (waves + kRowThreads / 64 - 1) / (kRowThreads / 64);
   if (wgs > INT32_MAX) return hipErrorInvalidValue;
   if (write)
-    hipLaunchKernelGGL((kv_write_kernel<BITS, D, NH>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_write_kernel<BITS, D, NW>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((kv_read_kernel<BITS, D, NH>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_read_kernel<BITS, D, NW>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
   return hipGetLastError();
 }
 

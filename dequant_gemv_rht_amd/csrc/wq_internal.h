@@ -376,6 +376,13 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return (uint32_t)__builtin_bit_cast(uint16_t, a) | ((uint32_t)__builtin_bit_cast(uint16_t, b) << 16);
 }
 
+// The same in one instruction (gfx950's v_cvt_pk_f16_f32).
+__device__ __forceinline__ uint32_t cvt_pk_half2(float lo, float hi) {
+  typedef float float2_t __attribute__((ext_vector_type(2)));
+  const float2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, half2_t));
+}
+
 __device__ __forceinline__ float half_bits_to_float(uint32_t h) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)h);
 }
