@@ -700,16 +700,16 @@ hipError_t launch_bits(int d, const AttnArgs &a, hipStream_t s) {
 }  // namespace
 
 size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window) {
-  // a bound that grows with seqs and max_len: plan_for gives units * splits
-  // below units + workgroups() unless runs are of kMaxSplit tokens, and none
-  // shorter than kMinSplit
-  const int64_t group = q_heads / c.kv_heads, qtiles = (group + 15) / 16, units = seqs * c.kv_heads * qtiles;
-  const int64_t seen = seen_at_most(max_len, window);
+  // A bound that grows with seqs and max_len: plan_for splits a unit (a
+  // sequence and up to 16 heads) at most once for every workgroups() / units
+  // units, unless runs are of kMaxSplit tokens, and makes none shorter than
+  // kMinSplit.
+  const int64_t seen = seen_at_most(max_len, window), heads = seqs * q_heads, group = q_heads / c.kv_heads;
   if (seen <= kMinSplit) return 0;
-  const int64_t few = units * ((seen + kMinSplit - 1) / kMinSplit), many = units * ((seen + kMaxSplit - 1) / kMaxSplit);
-  const int64_t fill = units + workgroups(c.bits, c.head_dim), filled = fill > many ? fill : many;
-  const int64_t runs = few < filled ? few : filled;
-  return (size_t)((runs * group + qtiles - 1) / qtiles) * (size_t)(c.head_dim + 4) * sizeof(float);
+  const int64_t fill = heads + workgroups(c.bits, c.head_dim) * (group < 16 ? group : 16);
+  const int64_t few = heads * ((seen + kMinSplit - 1) / kMinSplit), many = heads * ((seen + kMaxSplit - 1) / kMaxSplit);
+  const int64_t filled = fill > many ? fill : many, rows = few < filled ? few : filled;
+  return (size_t)rows * (size_t)(c.head_dim + 4) * sizeof(float);
 }
 
 hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, hipStream_t s) {

@@ -82,8 +82,8 @@ wq_status check_attn(const wq_kv_cache *c, int64_t seqs, int32_t q_heads, int64_
   if (max_len < 0 || window < 0)
     return set_error(WQ_E_ARG, "%s: max_len=%lld and window=%lld must not be negative", who, (long long)max_len,
                      (long long)window);
-  if (max_len > (int64_t)INT32_MAX - 4096)
-    return set_error(WQ_E_UNSUPPORTED, "%s: max_len above 2^31-4097", who);
+  if (max_len > (int64_t)INT32_MAX - 16384)   // positions past the last run stay in 32 bits
+    return set_error(WQ_E_UNSUPPORTED, "%s: max_len above 2^31-16385", who);
   if (q_heads > INT32_MAX / c->head_dim || seqs > (int64_t)INT32_MAX / q_heads)
     return set_error(WQ_E_UNSUPPORTED, "%s: q_heads * head_dim or seqs * q_heads above 2^31-1", who);
   return WQ_OK;

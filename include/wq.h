@@ -326,7 +326,10 @@ wq_status wq_embed(const wq_weight *w, const int32_t *ids, int64_t count, void *
  *    units with the four tokens side by side: unit u of the quad's token t
  *    is at 4 u + t.
  *  - k_params, v_params: fp16 [pages][kv_heads][page_size][2], a row's
- *    scale and zero (not read or written for 16 bits; may be NULL).
+ *    scale and zero (not read or written for 16 bits; may be NULL).  A zero
+ *    is a whole number from 0 to 2^bits - 1, as wq_kv_write stores it; codes
+ *    brought in from elsewhere have to keep to that (the kernels form code -
+ *    zero in fp16, exact for whole numbers only).
  * The layouts hand the attention kernel's matrix instructions their
  * operands in whole 16-byte loads.  int32 arrays (slots, tables, lengths,
  * positions) need 4-byte alignment only. */
@@ -382,9 +385,10 @@ wq_status wq_kv_read(const wq_kv_cache *cache, const int32_t *slots, int64_t tok
  * products as fp16, a rotated query as two fp16 parts (22 bits).
  *   q        fp16 [seqs][ldq]: q_heads rows of head_dim; q_heads a multiple
  *            of kv_heads
- *   table    device int32 [seqs][ld_table] page numbers; only entries of
- *            attended positions are read.  A page outside [0, pages) takes
- *            no part: its positions count as masked.
+ *   table    device int32 [seqs][ld_table] page numbers, rows of at least
+ *            ceil(max_len / page_size); only entries of attended positions
+ *            matter.  A page outside [0, pages) takes no part: its positions
+ *            count as masked.
  *   lens     device int32 [seqs].  A length above max_len counts as
  *            max_len; a sequence with nothing to attend to (length 0 or
  *            less, or only pages that take no part) gives zeros.
@@ -393,12 +397,14 @@ wq_status wq_kv_read(const wq_kv_cache *cache, const int32_t *slots, int64_t tok
  *   out      fp16 [seqs][ldo]
  *   workspace  device scratch of wq_attn_decode_workspace bytes (partial
  *            results where a sequence is split over workgroups; NULL when
- *            that is 0); no initialisation needed, contents not preserved
+ *            that is 0); no initialisation needed, contents not preserved.
+ *            The size never shrinks as seqs or max_len grow
  * What is stored past a sequence's length, NaN and infinity included, never
  * reaches its output.  Results do not depend on timing: the same inputs
  * give the same bits.  seqs 0 does nothing.
  * Errors (before anything is launched): WQ_E_ARG, WQ_E_ALIGN (ldq, ldo not
- * a multiple of 8), WQ_E_UNSUPPORTED (as above; seqs * heads past 2^31 - 1),
+ * a multiple of 8), WQ_E_UNSUPPORTED (as above; seqs * heads past 2^31 - 1,
+ * max_len above 2^31 - 16385),
  * WQ_E_WORKSPACE; WQ_E_HIP. */
 size_t wq_attn_decode_workspace(const wq_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_len,
                                 int64_t window);

@@ -82,7 +82,7 @@ def test_nothing_to_do(lib):
     (dict(out=None), A, "non-NULL"), (dict(q_heads=0), A, "q_heads=0"), (dict(q_heads=3), A, "q_heads=3"),
     (dict(q_heads=-2), A, "q_heads"), (dict(q_heads=1 << 30), U, "q_heads"), (dict(seqs=-1), A, "seqs=-1"),
     (dict(seqs=1 << 40), U, "seqs"), (dict(max_len=-1), A, "max_len=-1"), (dict(window=-1), A, "window=-1"),
-    (dict(max_len=2 ** 31), U, "max_len"), (dict(max_len=65), A, "ld_table=4"), (dict(ld_table=-1), A, "ld_table"),
+    (dict(max_len=2 ** 31 - 16384), U, "max_len"), (dict(max_len=65), A, "ld_table=4"), (dict(ld_table=-1), A, "ld_table"),
     (dict(ldq=1016), A, "ldq=1016"), (dict(ldo=8), A, "ldo=8"), (dict(ldq=1028), L, "multiples of 8"),
     (dict(scale=float("nan")), A, "scale"), (dict(scale=float("inf")), A, "scale"), (dict(q=P + 8), L, "aligned"),
     (dict(out=P + 2), L, "aligned"), (dict(table=P + 2), L, "aligned"), (dict(lens=P + 1), L, "aligned"),
@@ -110,8 +110,10 @@ def test_attention_workspace_is_checked(lib):
     sizes = [lib.wq_attn_decode_workspace(cache(pages=10000), 4, 8, n, 0) for n in (0, 1, 100, 1000, 10000, 100000)]
     assert sizes == sorted(sizes)
     assert lib.wq_attn_decode_workspace(cache(), 0, 8, 64, 0) == 0
-    big = lib.wq_attn_decode_workspace(cache(), 2 ** 31 // 8 - 1, 8, 2 ** 31 - 4097, 0)   # no overflow
-    assert big == 0 or big > 2 ** 31
+    wide = dq.WqKvCache(8, 64, 1, 16, 10, P, P, P, P, None, 0)   # one head shared by 2^25
+    assert lib.wq_attn_decode_workspace(ctypes.byref(wide), 1, 2 ** 25 - 1, 2 ** 31 - 16385, 0) < 2 ** 63
+    big = lib.wq_attn_decode_workspace(cache(), 2 ** 31 // 8 - 1, 8, 2 ** 31 - 16385, 0)   # no overflow
+    assert 2 ** 31 < big < 2 ** 63
 
 
 def rope(lib, **kw):
