@@ -1,7 +1,9 @@
 """Python binding of libwq (the rotated grouped-affine low-bit linear layer).
 
 Argument marshalling only: every step runs in the HIP kernels of
-``_lib/libwq.so``, built for gfx950 by ``dequant_gemv_rht_amd.build``.
+``_lib/libwq.so``, built for gfx950 by ``dequant_gemv_rht_amd.build`` (which
+also builds ``_lib/_wqpy.so``, the native half of this binding for the calls
+of a decode step).
 PyTorch supplies device memory and the current stream.  There is no CPU
 fallback: if the library is missing, importing the functions raises.
 
@@ -24,8 +26,8 @@ Functions mirror the C ABI in ``include/wq.h``:
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -113,6 +115,26 @@ def lib():
             f.argtypes = args
         _lib = l
     return _lib
+
+
+_native = None
+
+
+def _calls():
+    """The native half of the binding (csrc/binding.cpp), on this library's
+    functions; raises if it has not been built."""
+    global _native
+    if _native is None:
+        path = os.path.join(_HERE, "_lib", "_wqpy.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"the binding is not built ({path} missing): run `python -m dequant_gemv_rht_amd.build`")
+        spec = importlib.util.spec_from_file_location("_wqpy", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in
+                      ("wq_kv_write", "wq_kv_read", "wq_attn_decode_workspace", "wq_attn_decode", "wq_rope")))
+        _native = module
+    return _native
 
 
 def _check(fn: str, status: int):
@@ -344,40 +366,6 @@ def wq_embed(table: QWeight, ids: torch.Tensor, out_dtype=torch.float16, out: Op
     return y
 
 
-# A decode step issues these calls every few microseconds, so the checks
-# below ask each tensor for as little as they can.
-_F16, _INT32 = torch.float16, torch.int32
-
-
-def _rows(t: torch.Tensor, name: str):
-    """(rows, columns, row stride) of fp16 GPU rows with any row stride."""
-    if t.dtype is not _F16 or not t.is_cuda:
-        raise ValueError(f"{name} must be a float16 GPU tensor")
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be [rows][columns], got {tuple(shape)}")
-    rows, cols = shape
-    if t.is_contiguous():
-        return rows, cols, cols
-    if t.stride(1) != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
-    return rows, cols, t.stride(0) if rows > 1 else cols   # torch leaves a single row's stride arbitrary
-
-
-def _ints(t: torch.Tensor, name: str) -> torch.Tensor:
-    if t.dtype is not _INT32 or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 GPU tensor")
-    return t
-
-
-def _new(rows: int, cols: int, device) -> torch.Tensor:
-    return torch.empty(rows, cols, dtype=_F16, device=device)
-
-
-def _new_like(x: torch.Tensor, rows: int, cols: int) -> torch.Tensor:
-    return torch.empty_like(x) if x.is_contiguous() else _new(rows, cols, x.device)
-
-
 @dataclass
 class KVCache:
     """One layer's paged key-value cache in libwq's layout (``wq_kv_cache``
@@ -395,6 +383,9 @@ class KVCache:
     def __post_init__(self):
         if self.bits not in (4, 8, 16):
             raise ValueError(f"bits={self.bits} (4, 8 or 16)")
+        if self.head_dim not in (64, 128, 256) or self.kv_heads < 1 or self.page_size < 1:
+            raise ValueError(f"head_dim={self.head_dim} (64, 128 or 256), kv_heads={self.kv_heads}, "
+                             f"page_size={self.page_size}")
         units = self.head_dim // 2 if self.bits == 4 else self.head_dim
         dt = torch.float16 if self.bits == 16 else torch.uint8
         pages = self.k.shape[0]
@@ -419,9 +410,7 @@ class KVCache:
         self._c = WqKvCache(self.bits, self.head_dim, self.kv_heads, self.page_size, pages, _ptr(self.k),
                             _ptr(self.v), _ptr(self.k_params), _ptr(self.v_params), _ptr(self.signs),
                             128 if self.signs is not None else 0)
-        self._ref = ctypes.byref(self._c)
-        self._cols = self.kv_heads * self.head_dim
-        self._workspace = {}     # wq_attn_decode_workspace by shape
+        self._at = ctypes.addressof(self._c)
 
     @classmethod
     def new(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int,
@@ -436,46 +425,31 @@ class KVCache:
         return cls(bits, head_dim, kv_heads, page_size, k, v, kp, vp, signs)
 
 
+# A decode step issues these calls every few microseconds, so the questions
+# to the tensors, the outputs' allocation and the call itself are native
+# (csrc/binding.cpp); each returns its result, or the library's status.
+
 def wq_kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
-    """Code the rows of ``k`` and ``v`` (fp16 [tokens][kv_heads * head_dim]) into
-    the cache at ``slots`` (int32 [tokens]; outside the cache: skipped)."""
-    rows_k, cols_k, ldk = _rows(k, "k")
-    rows_v, cols_v, ldv = _rows(v, "v")
-    n = _ints(slots, "slots").numel()
-    if cols_k != cache._cols or cols_v != cache._cols or rows_k != n or rows_v != n:
-        raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} are not [{n} slots][{cache._cols} channels]")
-    _check("wq_kv_write", lib().wq_kv_write(cache._ref, k.data_ptr(), ldk, v.data_ptr(), ldv, slots.data_ptr(), n,
-                                            _stream()))
+    """Code the rows of ``k`` and ``v`` (fp16 [tokens][kv_heads * head_dim], any
+    row stride) into the cache at ``slots`` (int32 [tokens]; outside the
+    cache: skipped)."""
+    st = (_native or _calls()).kv_write(cache._at, k, v, slots)
+    if st:
+        _check("wq_kv_write", st)
 
 
 def wq_kv_read(cache: KVCache, slots: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None):
     """The cached rows at ``slots`` as fp16: (k, v), each [tokens][kv_heads * head_dim]."""
-    n, cols = _ints(slots, "slots").numel(), cache._cols
-    if out is None:
-        k = _new(n, cols, slots.device)
-        v = torch.empty_like(k)
-        ldk = ldv = cols
-    else:
-        k, v = out
-        rows_k, cols_k, ldk = _rows(k, "out[0]")
-        rows_v, cols_v, ldv = _rows(v, "out[1]")
-        if cols_k != cols or cols_v != cols or rows_k != n or rows_v != n:
-            raise ValueError(f"out {tuple(k.shape)} and {tuple(v.shape)} are not [{n} slots][{cols} channels]")
-    _check("wq_kv_read", lib().wq_kv_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), ldk, v.data_ptr(), ldv,
-                                          _stream()))
-    return k, v
+    r = (_native or _calls()).kv_read(cache._at, slots, out)
+    if type(r) is int:
+        _check("wq_kv_read", r)
+    return r
 
 
 def wq_attn_decode_workspace(cache: KVCache, seqs: int, q_heads: int, max_len: int, window: int = 0) -> int:
-    key = (seqs, q_heads, max_len, window)
-    size = cache._workspace.get(key)
-    if size is None:
-        size = lib().wq_attn_decode_workspace(cache._ref, seqs, q_heads, max_len, window)
-        if size == ctypes.c_size_t(-1).value:
-            raise WqError("wq_attn_decode_workspace", WQ_E_ARG, lib().wq_last_error().decode())
-        if len(cache._workspace) >= 4096:
-            cache._workspace.clear()
-        cache._workspace[key] = size
+    size = lib().wq_attn_decode_workspace(ctypes.byref(cache._c), seqs, q_heads, max_len, window)
+    if size == ctypes.c_size_t(-1).value:
+        raise WqError("wq_attn_decode_workspace", WQ_E_ARG, lib().wq_last_error().decode())
     return size
 
 
@@ -486,102 +460,27 @@ def wq_attn_decode(cache: KVCache, q: torch.Tensor, table: torch.Tensor, lens: t
     head_dim] over the pages ``table`` (int32 [seqs][pages]) and lengths
     ``lens`` (int32 [seqs]) name.  ``max_len``: an upper bound of the lengths
     (default: what the table's pages hold); ``scale``: default
-    head_dim ** -0.5."""
-    seqs, cols, ldq = _rows(q, "q")
-    heads = cols // cache.head_dim
-    if heads * cache.head_dim != cols:
-        raise ValueError(f"q: {cols} columns are not heads of {cache.head_dim}")
-    if table.dtype is not _INT32 or not table.is_cuda:
-        raise ValueError("table must be an int32 GPU tensor")
-    shape = table.shape
-    if len(shape) != 2 or shape[0] != seqs:
-        raise ValueError(f"table must be [{seqs}][pages], got {tuple(shape)}")
-    pages = ld_table = shape[1]
-    if not table.is_contiguous():
-        if pages > 1 and table.stride(1) != 1:
-            raise ValueError(f"table must have contiguous rows, got strides {table.stride()}")
-        if seqs > 1:
-            ld_table = table.stride(0)
-    if _ints(lens, "lens").shape != (seqs,):
-        raise ValueError(f"lens must be [{seqs}], got {tuple(lens.shape)}")
-    if max_len is None:
-        max_len = pages * cache.page_size
-    elif max_len > pages * cache.page_size:
-        raise ValueError(f"max_len={max_len}: {pages} pages of {cache.page_size} tokens hold {pages * cache.page_size}")
-    if out is None:
-        y, ldo = _new_like(q, seqs, cols), cols
-    else:
-        y = out
-        rows_y, cols_y, ldo = _rows(y, "out")
-        if rows_y != seqs or cols_y != cols:
-            raise ValueError(f"out must be [{seqs}][{cols}], got {tuple(y.shape)}")
-    if workspace is None:
-        wp, wn = None, wq_attn_decode_workspace(cache, seqs, heads, max_len, window)
-        if wn:
-            workspace = torch.empty(wn, dtype=torch.uint8, device=q.device)
-            wp = workspace.data_ptr()
-    else:
-        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check("wq_attn_decode", lib().wq_attn_decode(
-        cache._ref, q.data_ptr(), ldq, heads, seqs, table.data_ptr(), ld_table, lens.data_ptr(), max_len, window,
-        cache.head_dim ** -0.5 if scale is None else scale, y.data_ptr(), ldo, wp, wn, _stream()))
-    return y
-
-
-_PACK64 = [struct.Struct(f"{c}q") for c in range(WQ_MAX_BATCH + 1)]
-_PACK32 = [struct.Struct(f"{c}i") for c in range(WQ_MAX_BATCH + 1)]
+    head_dim ** -0.5; ``workspace``: wq_attn_decode_workspace bytes (default:
+    allocated here)."""
+    r = (_native or _calls()).attn_decode(cache._at, q, table, lens, max_len, window, scale, workspace, out)
+    if type(r) is int:
+        _check("wq_attn_decode", r)
+    return r
 
 
 def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
             head_dim: int, pair_axis: Optional[Sequence[int]] = None, adjacent: bool = False,
             out: Optional[Sequence[torch.Tensor]] = None):
     """Rotary positions on every array of ``xs`` (fp16 [tokens][heads *
-    head_dim]) in one launch; ``cos``, ``sin`` fp32 [rows][rot / 2],
-    ``positions`` int32 [axes][tokens] (or [tokens]), ``pair_axis`` the axis
-    of each pair.  ``out`` may be ``xs`` itself (in place)."""
-    _dev(cos, torch.float32, "cos")
-    _dev(sin, torch.float32, "sin")
-    shape = _ints(positions, "positions").shape
-    axes, tokens = shape if len(shape) == 2 else (1, positions.numel())
-    shape = cos.shape
-    if len(shape) != 2 or shape != sin.shape:
-        raise ValueError(f"cos and sin must be [rows][rot / 2], got {tuple(shape)} and {tuple(sin.shape)}")
-    rows, half = shape
+    head_dim], any row stride) in one launch; ``cos``, ``sin`` fp32 [rows][rot
+    / 2], ``positions`` int32 [axes][tokens] (or [tokens]), ``pair_axis`` the
+    axis of each pair.  ``out`` may be ``xs`` itself (in place)."""
     if pair_axis is not None:
-        if len(pair_axis) != half:
-            raise ValueError(f"pair_axis: {len(pair_axis)} entries for {half} pairs")
         pair_axis = bytes(pair_axis)
-    if head_dim <= 0:
-        raise ValueError(f"head_dim={head_dim} must be positive")
-    count = len(xs)
-    if not 0 < count <= WQ_MAX_BATCH or (out is not None and len(out) != count):
-        raise ValueError(f"xs: {count} arrays (1 to {WQ_MAX_BATCH}), and as many in out")
-    ys, px, ldx, py, ldy, heads = [], [], [], [], [], []
-    for i, x in enumerate(xs):
-        n, cols, ld = _rows(x, "xs")
-        h = cols // head_dim
-        if n != tokens or h * head_dim != cols:
-            raise ValueError(f"an array of {tuple(x.shape)} is not [{tokens}][heads * {head_dim}]")
-        px.append(x.data_ptr())
-        ldx.append(ld)
-        heads.append(h)
-        if out is None:
-            y = _new_like(x, n, cols)
-            ld = cols
-        else:
-            y = out[i]
-            rows_y, cols_y, ld = _rows(y, "out")
-            if rows_y != n or cols_y != cols:
-                raise ValueError(f"out must be [{n}][{cols}], got {tuple(y.shape)}")
-        ys.append(y)
-        py.append(y.data_ptr())
-        ldy.append(ld)
-    p64 = _PACK64[count].pack
-    _check("wq_rope", lib().wq_rope(
-        count, p64(*px), p64(*ldx), p64(*py), p64(*ldy), _PACK32[count].pack(*heads), tokens, head_dim, 2 * half,
-        cos.data_ptr(), sin.data_ptr(), rows, positions.data_ptr(), tokens, axes, pair_axis,
-        WQ_ROPE_ADJACENT if adjacent else 0, _stream()))
-    return ys
+    r = (_native or _calls()).rope(xs, cos, sin, positions, head_dim, pair_axis, adjacent, out)
+    if type(r) is int:
+        _check("wq_rope", r)
+    return r
 
 
 def stream_read(src: torch.Tensor, sink: torch.Tensor, nbytes: Optional[int] = None) -> None:

@@ -4,7 +4,9 @@
     python -m dequant_gemv_rht_amd.build --asm    # also keep the AMD assembly
 
 Each source file compiles to its own object in parallel; the library lands
-in ``dequant_gemv_rht_amd/_lib/libwq.so``.
+in ``dequant_gemv_rht_amd/_lib/libwq.so``.  ``csrc/binding.cpp``, the native
+half of the Python binding, compiles against torch's headers with the host
+compiler into ``_lib/_wqpy.so``; it holds no device code.
 """
 
 from __future__ import annotations
@@ -29,8 +31,38 @@ COMMON = [
 ]
 
 
+BINDING = "binding.cpp"
+BINDING_LIB = os.path.join(OUT, "_wqpy.so")
+
+
 def sources():
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")))
+    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".hip", ".cpp")) and f != BINDING)
+
+
+def _replace(cmd, out: str, what: str) -> None:
+    """Run `cmd` + an output file of this process's own, then put that in place of `out`."""
+    tmp = out + ".tmp%d" % os.getpid()
+    r = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stderr}")
+    os.replace(tmp, out)
+
+
+def build_binding() -> str:
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(t, "lib")
+    _replace([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+              "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+              *(a for i in inc for a in ("-isystem", i)), os.path.join(CSRC, BINDING), f"-L{lib}", "-ltorch_python",
+              "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", f"-Wl,-rpath,{lib}"], BINDING_LIB, f"{BINDING}: g++")
+    return BINDING_LIB
 
 
 def _compile(src: str, asm: bool) -> str:
@@ -54,14 +86,11 @@ def build(asm: bool = False, jobs: int | None = None) -> str:
     os.makedirs(OUT, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), max(1, (os.cpu_count() or 4)))
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(lambda s: _compile(s, asm), srcs))
-    tmp = LIB + ".tmp%d" % os.getpid()
-    r = subprocess.run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs,
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stderr)
-    os.replace(tmp, LIB)
+        binding.result()
+    _replace([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC"] + objs, LIB, "link")
     return LIB
 
 

@@ -6,6 +6,7 @@ wq_rope)."""
 import ctypes
 
 import pytest
+import torch
 
 import dequant_gemv_rht_amd as dq
 
@@ -151,9 +152,30 @@ def test_rope_nothing_to_do(lib):
 
 
 def test_binding_refuses_host_tensors():
-    import torch
-
     with pytest.raises(ValueError, match="GPU tensor"):
         dq.KVCache(8, 64, 1, 16, torch.zeros((1, 1, 1024), dtype=torch.uint8), torch.zeros((1, 1, 1024), dtype=torch.uint8))
     with pytest.raises(ValueError, match="bits=5"):
         dq.KVCache(5, 64, 1, 16, None, None)
+    with pytest.raises(ValueError, match="head_dim=0"):
+        dq.KVCache(8, 0, 1, 16, None, None)
+
+
+def test_native_binding_refuses_before_any_call():
+    # the native half loads and asks its questions without a GPU
+    c = dq.WqKvCache(8, 128, 2, 16, 10, P, P, P, P, None, 0)
+    at, m = ctypes.addressof(c), dq._calls()
+    x, i, f = torch.zeros((3, 256), dtype=torch.float16), torch.zeros(3, dtype=torch.int32), torch.zeros((4, 64))
+    calls = [lambda: m.kv_write(at, x, x, i), lambda: m.kv_read(at, i, None), lambda: m.kv_read(at, i, (x, x)),
+             lambda: m.attn_decode(at, x, i, i, None, 0, None, None, None),
+             lambda: m.rope((x,), f, f, i, 128, None, False, None)]
+    for call in calls:
+        with pytest.raises(ValueError, match="GPU tensor"):
+            call()
+    with pytest.raises(TypeError, match="k must be a tensor, got list"):
+        m.kv_write(at, [1], x, i)
+    with pytest.raises(TypeError, match="4 arguments"):
+        m.kv_write(at)
+    with pytest.raises(ValueError, match="no cache"):
+        m.kv_read(0, i, None)
+    with pytest.raises(ValueError, match="arrays"):
+        m.rope((), f, f, i, 128, None, False, None)
