@@ -426,7 +426,9 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
     _Float16 top = w[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = __builtin_fmaxf16(top, w[i]);
-    if (__any(!(top <= (_Float16)(1 << (kGain + kSlack))))) {
+    float sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    // (the sum: an infinite p of a row of scale 0 does not show in the w)
+    if (__any(!(top <= (_Float16)(1 << (kGain + kSlack))) || !(sum < INFINITY))) {
       // move the reference: the largest term so far becomes 2^kGain (2^-24:
       // the smallest positive scale, so that rows of scale 0 do not leave
       // it unset)
@@ -443,8 +445,9 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n) o[n] *= keep;
       weigh();
+      sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
     }
-    l += ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
+    l += sum;
     // weights as the second operand, in the values' token order: 4-bit
     // codes of tokens 0, 2 and 1, 3 come out of a word together
     constexpr int o1 = BITS == 4 ? 2 : 1, o2 = BITS == 4 ? 1 : 2;

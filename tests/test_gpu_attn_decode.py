@@ -235,6 +235,37 @@ def test_value_scales_far_apart(bits):
     check(got, reference(host, bits, d, page, q, table, [n], 1.0), "scales")
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_value_scales_of_zero(bits):
+    """Rows of scale 0 are zeros, whatever their weights: alone in a sequence,
+    in all of it, and in the tokens of the largest scores (spread over some
+    hundred powers of two) among others.  Where such a token takes all the
+    weight the output is nearly 0, so errors are taken against the values'
+    own size, 1."""
+    d, heads, group, page = 128, 2, 4, 16
+    rng = np.random.default_rng(23)
+    lens = [1, 5, 33, 200, 300, 129]
+    host, cache, table, q = problem(rng, bits, d, heads, group, page, lens, q_scale=60.0)
+    k = values(host, "k", bits, d, page)
+    zero = host["v_params"]
+    for b, n in enumerate(lens):
+        for h in range(heads):
+            if b < 2:
+                gone = range(n)
+            else:
+                rows = np.stack([k[table[b, t // page], h, t % page] for t in range(n)])
+                top = (q[b, h * group:(h + 1) * group].astype(np.float64) @ rows.T).argsort(-1)
+                gone = {int(t) for r in top[: 2] for t in r[-3:]}   # half of the heads
+            for t in gone:
+                zero[table[b, t // page], h, t % page, 0] = 0
+    cache = device_cache(host, page, heads, d, bits)
+    got = dq.wq_attn_decode(cache, dev(q.reshape(len(lens), -1)), dev(table), dev(np.array(lens, np.int32)))
+    want = reference(host, bits, d, page, q, table, lens, d ** -0.5)
+    g = got.float().cpu().numpy().astype(np.float64).reshape(want.shape)
+    assert np.isfinite(g).all() and not g[:2].any()
+    assert np.abs(g - want).max() <= MAX * np.abs(values(host, "v", bits, d, page)).max()
+
+
 def test_large_scores():
     # scores of several hundred: the softmax is one token, no overflow
     say("attn large scores")
