@@ -18,11 +18,17 @@
 // never leave their lane.  The cache's layout gives V in that order (quads
 // of tokens side by side) and K as panels, both in whole 16-byte loads.
 //
-// Codes become fp16 by placing them in the significand of 1024: 0x6400 | c
-// is 1024 + c.  Values have 1024 + zero subtracted (exact).  Keys keep the
-// bias, 1024 + c (8 bits) or 16 (64 + c) (4 bits, the code four places up),
-// and the score takes it out with the zero, in fp32:
-//   s (dot(q, bias + c) - (bias + z) sum(q)).
+// Codes enter the products as they are: 16 bits whose value c is below 2^10
+// are fp16's subnormal c 2^-24, which the matrix instructions take without
+// loss, so 8-bit codes only have their bytes spread and 4-bit codes are
+// masked out of their words.  Zeros come off in fp32, after the products:
+//   s (dot(q, c) - z sum(q))   and   sum(w c) - sum(w z).
+// The instructions line terms up by their exponents, a subnormal's being
+// that of 2^10 codes, and cut them 24 bits or so below the largest; 4-bit
+// values are therefore all brought to the upper half of a byte, as 16 c
+// (left as c, half of the channels were off by 5e-4 of 16000 tokens' sum,
+// now by 2.3e-4 as the others).  Keys' scores do not need that: their lower
+// nibbles have sums of their own, taken 16-fold.
 // The values' scale goes into the weight, p s, before it is rounded to
 // fp16; the running reference m therefore tracks max(u + log2 s), so that
 // p s of the largest term stays near 2^kGain and weights down to 2^-20 of
@@ -33,10 +39,10 @@
 // What bounds it: traffic where there is enough of it (64 sequences of 16381
 // tokens, 8 key-value heads of 128, 8 bits: 2.21 GB in 339 us, 6.5 TB/s,
 // what a plain read reaches); the longest sequences' last workgroups in a
-// ragged batch (64 up to 4099 tokens, 4 bits: 146 MB in 41 us); the way from
+// ragged batch (64 up to 4099 tokens, 4 bits: 146 MB in 38 us); the way from
 // the arguments over page table and cache to the join for few tokens (77
 // tokens: 5.5 us, an empty kernel 2.2).  A step of 128 tokens takes a
-// workgroup 0.83 us with 4 bits and 1.3 us with 8 where three share a CU.
+// workgroup 0.76 us with 4 bits and 1.3 us with 8 where three share a CU.
 // Three waves a SIMD with one set of registers for the codes, asked for
 // again as soon as a half is used, were faster than two waves with two sets
 // (64 ragged sequences: 42.6 against 63 us), and four spill.
@@ -49,6 +55,7 @@ using namespace dev;
 
 namespace {
 
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef const __attribute__((address_space(4))) int32_t *const_i32;   // scalar loads
@@ -72,8 +79,8 @@ struct Fmt {
   static constexpr int kWords = kRow / 16;         // 32-bit words a lane holds of 16 tokens (keys; values)
   static constexpr int kPiece = kWords < 4 ? kWords : 4;   // words per load
   static constexpr int kKeyMfma = D / 32, kOutMfma = D / 16;
-  static constexpr float kBias = BITS == 8 ? 1024.0f : 64.0f;   // of a key operand
-  // first of the 8 channels of key operand m in lane group g
+  static constexpr float kUnit = BITS == 16 ? 1.0f : BITS == 8 ? 0x1p24f : 0x1p20f;   // 1 / a code of 1 in the products
+  // first of the 8 channels of key operand m (4 bits: of word m) in lane group g
   __device__ static constexpr int key_channel(int m, int g) {
     if (BITS == 16) return 32 * m + 8 * g;
     if (BITS == 8) return 64 * (m >> 1) + 16 * g + 8 * (m & 1);
@@ -96,8 +103,6 @@ struct Side {
 
 __device__ __forceinline__ half2_t as_half2(uint32_t w) { return __builtin_bit_cast(half2_t, w); }
 __device__ __forceinline__ uint32_t as_u32(half2_t h) { return __builtin_bit_cast(uint32_t, h); }
-__device__ __forceinline__ half2_t both(float v) { return half2_t{(_Float16)v, (_Float16)v}; }
-
 struct Quad {
   uint32_t w[4];
 };
@@ -105,36 +110,22 @@ __device__ __forceinline__ half8_t as_half8(uint32_t a, uint32_t b, uint32_t c, 
   return __builtin_bit_cast(half8_t, Quad{{a, b, c, d}});
 }
 
-// two 8-bit codes -> 1024 + code
-__device__ __forceinline__ half2_t bytes01(uint32_t w) {
-  return as_half2(__builtin_amdgcn_perm(0x64646464u, w, 0x04010400u));
-}
-__device__ __forceinline__ half2_t bytes23(uint32_t w) {
-  return as_half2(__builtin_amdgcn_perm(0x64646464u, w, 0x04030402u));
-}
-// 4-bit codes at bits 0 and 16 -> 1024 + code; at bits 4 and 20 -> 1024 +
-// 16 code.  One and-or each: the constants are kept in registers, as two
-// literals would make it two instructions.
-struct Nibbles {
-  uint32_t low = 0x000F000Fu, high = 0x00F000F0u, one = 0x64006400u;
-  __device__ __forceinline__ Nibbles() { asm volatile("" : "+s"(low), "+s"(high), "+v"(one)); }
-  __device__ __forceinline__ half2_t lo(uint32_t w) const { return as_half2((w & low) | one); }
-  __device__ __forceinline__ half2_t hi(uint32_t w) const { return as_half2((w & high) | one); }
-};
+__device__ __forceinline__ uint32_t bytes01(uint32_t w) { return __builtin_amdgcn_perm(w, w, 0x0C010C00u); }
+__device__ __forceinline__ uint32_t bytes23(uint32_t w) { return __builtin_amdgcn_perm(w, w, 0x0C030C02u); }
+constexpr uint32_t kLowNibbles = 0x000F000Fu, kHighNibbles = 0x00F000F0u;
 
-// Key operand m of a block, as kBias + code (8 bits) or 16 (kBias + code)
-// (4 bits); the score takes the bias out again.
+// Key operand m of a block.  4 bits: the lower (even m) or upper nibbles of
+// words m & ~1 and the next, in channel order 0, 4, 2, 6 (1, 5, 3, 7) of
+// each.
 template <int BITS, int D>
-__device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>::kWords], int m, const Nibbles &nib) {
+__device__ __forceinline__ half8_t key_operand(const uint32_t (&k)[Fmt<BITS, D>::kWords], int m) {
   if constexpr (BITS == 16) {
     return as_half8(k[4 * m], k[4 * m + 1], k[4 * m + 2], k[4 * m + 3]);
   } else if constexpr (BITS == 8) {
-    return as_half8(as_u32(bytes01(k[2 * m])), as_u32(bytes23(k[2 * m])), as_u32(bytes01(k[2 * m + 1])),
-                    as_u32(bytes23(k[2 * m + 1])));
+    return as_half8(bytes01(k[2 * m]), bytes23(k[2 * m]), bytes01(k[2 * m + 1]), bytes23(k[2 * m + 1]));
   } else {
-    // channel order 0, 4, 1, 5, 2, 6, 3, 7
-    const uint32_t w = k[m];
-    return as_half8(as_u32(nib.hi(w << 4)), as_u32(nib.hi(w)), as_u32(nib.hi(w >> 4)), as_u32(nib.hi(w >> 8)));
+    const uint32_t a = k[m & ~1], b = k[m | 1], mask = m & 1 ? kHighNibbles : kLowNibbles;
+    return as_half8(a & mask, (a >> 8) & mask, b & mask, (b >> 8) & mask);
   }
 }
 
@@ -148,12 +139,10 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-constexpr float kLowScale = 2048.0f;   // of a query's low part
-
 template <int BITS>
 __device__ __forceinline__ uint4 pack_query(const float (&v)[8]) {
   if (BITS == 4)
-    return make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]), pack_half2(v[3], v[7]));
+    return make_uint4(pack_half2(v[0], v[4]), pack_half2(v[2], v[6]), pack_half2(v[1], v[5]), pack_half2(v[3], v[7]));
   return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
 }
 
@@ -286,9 +275,8 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 
   // The queries, rotated as the cache is, rounded to fp16, in the keys'
   // channel order.  A rotated query is no longer an fp16 value: what the
-  // rounding leaves (times 2^11) goes to columns 8 to 15 where there are at
-  // most 8 heads, else to operands of its own, and its scores are added to
-  // the heads' own.
+  // rounding leaves goes to columns 8 to 15 where there are at most 8 heads,
+  // else to operands of its own, and its scores are added to the heads' own.
   const bool split_q = !LOW && D >= 128 && a.signs && heads <= 8;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
@@ -313,46 +301,50 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
     *reinterpret_cast<uint4 *>(&sh.q[h][c0]) = w;
     if (split_q || LOW) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (v[e] - (float)(_Float16)v[e]) * kLowScale;
+      for (int e = 0; e < 8; ++e) v[e] -= (float)(_Float16)v[e];
       *reinterpret_cast<uint4 *>(&sh.q[h + (LOW ? 16 : 8)][c0]) = pack_query<BITS>(v);
     }
   }
   __syncthreads();
   half8_t q[F::kKeyMfma], ql[LOW ? F::kKeyMfma : 1];
-  float qsum = 0.0f, lsum = 0.0f;
+  float qsum = 0.0f;
+  auto operand = [&](int row, int m) {
+    half8_t h;
+    if constexpr (BITS == 4) {
+      const half4_t a = *reinterpret_cast<const half4_t *>(&sh.q[row][F::key_channel(m & ~1, g) + 4 * (m & 1)]);
+      const half4_t b = *reinterpret_cast<const half4_t *>(&sh.q[row][F::key_channel(m | 1, g) + 4 * (m & 1)]);
+      h = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    } else {
+      h = *reinterpret_cast<const half8_t *>(&sh.q[row][F::key_channel(m, g)]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) qsum += (float)h[e];
+    return h;
+  };
 #pragma unroll
   for (int m = 0; m < F::kKeyMfma; ++m) {
-    q[m] = *reinterpret_cast<const half8_t *>(&sh.q[col][F::key_channel(m, g)]);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) qsum += (float)q[m][e];
-    if constexpr (LOW) {
-      ql[m] = *reinterpret_cast<const half8_t *>(&sh.q[16 + col][F::key_channel(m, g)]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) lsum += (float)ql[m][e];
-    }
+    q[m] = operand(col, m);
+    if constexpr (LOW) ql[m] = operand(16 + col, m);
   }
   qsum = column_sum(qsum);
-  if (LOW) lsum = column_sum(lsum);
   __syncthreads();   // sh.q is free for sh.o
 
-  float m = kNone, l = 0.0f;
+  float m = kNone, l = 0.0f, lz = 0.0f;   // lz: sum of w z
   f32x4 o[F::kOutMfma];
 #pragma unroll
   for (int n = 0; n < F::kOutMfma; ++n) o[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const float to_log2 = a.scale * 1.4426950408889634f * (BITS == 4 ? 0.0625f : 1.0f);
-  const float bias_sum = (BITS == 4 ? -16.0f : -1.0f) * F::kBias * qsum, zero_sum = (BITS == 4 ? -16.0f : -1.0f) * qsum;
-  const Nibbles nib;
+  const float to_log2 = a.scale * 1.4426950408889634f * F::kUnit, zero_sum = -qsum / F::kUnit;
   for (; t < end; t += kStride) {
     // scores before the keys' scale, in units of log2
     float x[8];
     uint32_t kp[4];   // the keys' scales, two to a word
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, low = acc;   // low: 4 bits' lower nibbles
       if constexpr (BITS != 16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf((float)as_half2(ks.par[b][i])[1], zero_sum, bias_sum);
+        for (int i = 0; i < 4; ++i) acc[i] = (float)as_half2(ks.par[b][i])[1] * zero_sum;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           kp[2 * b + i] = __builtin_amdgcn_perm(ks.par[b][2 * i + 1], ks.par[b][2 * i], 0x05040100u);
@@ -361,23 +353,18 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
         }
       }
 #pragma unroll
-      for (int mm = 0; mm < F::kKeyMfma; ++mm)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm, nib), q[mm], acc, 0, 0, 0);
-      if constexpr (LOW) {
-        f32x4 low = {0.0f, 0.0f, 0.0f, 0.0f};
-        if constexpr (BITS != 16)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            low[i] = (F::kBias + (float)as_half2(ks.par[b][i])[1]) * ((BITS == 4 ? -16.0f : -1.0f) * lsum);
-#pragma unroll
-        for (int mm = 0; mm < F::kKeyMfma; ++mm)
-          low = __builtin_amdgcn_mfma_f32_16x16x32_f16(key_operand<BITS, D>(ks.w[b], mm, nib), ql[mm], low, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(low[i], 1.0f / kLowScale, acc[i]);
+      for (int mm = 0; mm < F::kKeyMfma; ++mm) {
+        const half8_t k = key_operand<BITS, D>(ks.w[b], mm);
+        f32x4 &sum = BITS == 4 && mm % 2 == 0 ? low : acc;
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[mm], sum, 0, 0, 0);
+        if constexpr (LOW) sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, ql[mm], sum, 0, 0, 0);
       }
+      if constexpr (BITS == 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(low[i], 16.0f, acc[i]);
       if (split_q) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(dpp<kRowRor8>(acc[i]), 1.0f / kLowScale, acc[i]);
+        for (int i = 0; i < 4; ++i) acc[i] += dpp<kRowRor8>(acc[i]);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[4 * b + i] = acc[i] * to_log2;
@@ -442,6 +429,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
       const float keep = __builtin_amdgcn_exp2f(m - high);
       m = high;
       l *= keep;
+      lz *= keep;
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n) o[n] *= keep;
       weigh();
@@ -452,50 +440,26 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
     // codes of tokens 0, 2 and 1, 3 come out of a word together
     constexpr int o1 = BITS == 4 ? 2 : 1, o2 = BITS == 4 ? 1 : 2;
     const half8_t pw = {w[0], w[o1], w[o2], w[3], w[4], w[4 + o1], w[4 + o2], w[7]};
-    half2_t z[2][2];
-    if constexpr (BITS != 16) {
+    if constexpr (BITS != 16)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        z[b][0] = as_half2(__builtin_amdgcn_perm(vs.par[b][o1], vs.par[b][0], 0x07060302u));
-        z[b][1] = as_half2(__builtin_amdgcn_perm(vs.par[b][3], vs.par[b][o2], 0x07060302u));
-      }
-    }
+      for (int i = 0; i < 8; ++i) lz = fmaf((float)w[i], (float)as_half2(vs.par[i >> 2][i & 3])[1], lz);
     if constexpr (BITS == 16) {
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n)
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
             as_half8(vs.w[0][2 * n], vs.w[0][2 * n + 1], vs.w[1][2 * n], vs.w[1][2 * n + 1]), pw, o[n], 0, 0, 0);
     } else if constexpr (BITS == 8) {
-      half2_t c[2][2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i >> 1][i & 1] = z[i >> 1][i & 1] + both(1024.0f);
 #pragma unroll
       for (int n = 0; n < F::kOutMfma; ++n)
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(as_u32(bytes01(vs.w[0][n]) - c[0][0]), as_u32(bytes23(vs.w[0][n]) - c[0][1]),
-                     as_u32(bytes01(vs.w[1][n]) - c[1][0]), as_u32(bytes23(vs.w[1][n]) - c[1][1])),
-            pw, o[n], 0, 0, 0);
+            as_half8(bytes01(vs.w[0][n]), bytes23(vs.w[0][n]), bytes01(vs.w[1][n]), bytes23(vs.w[1][n])), pw, o[n], 0, 0, 0);
     } else {
-      half2_t c[2][2], d[2][2];
-      const half2_t f = both(0.0625f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c[i >> 1][i & 1] = z[i >> 1][i & 1] + both(1024.0f);
-        d[i >> 1][i & 1] = -(z[i >> 1][i & 1] + both(64.0f));
-      }
-#pragma unroll
-      for (int n = 0; n < F::kOutMfma; n += 2) {
-        const uint32_t a0 = vs.w[0][n / 2], a1 = a0 >> 8, b0 = vs.w[1][n / 2], b1 = b0 >> 8;
+      for (int n = 0; n < F::kOutMfma; ++n) {
+        const uint32_t a = vs.w[0][n / 2], b = vs.w[1][n / 2], m = kHighNibbles;
         o[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(as_u32(nib.lo(a0) - c[0][0]), as_u32(nib.lo(a1) - c[0][1]),
-                     as_u32(nib.lo(b0) - c[1][0]), as_u32(nib.lo(b1) - c[1][1])),
-            pw, o[n], 0, 0, 0);
-        o[n + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-            as_half8(as_u32(__builtin_elementwise_fma(nib.hi(a0), f, d[0][0])),
-                     as_u32(__builtin_elementwise_fma(nib.hi(a1), f, d[0][1])),
-                     as_u32(__builtin_elementwise_fma(nib.hi(b0), f, d[1][0])),
-                     as_u32(__builtin_elementwise_fma(nib.hi(b1), f, d[1][1]))),
-            pw, o[n + 1], 0, 0, 0);
+            n & 1 ? as_half8(a & m, (a >> 8) & m, b & m, (b >> 8) & m)
+                  : as_half8((a << 4) & m, (a >> 4) & m, (b << 4) & m, (b >> 4) & m), pw, o[n], 0, 0, 0);
       }
     }
     __builtin_amdgcn_sched_barrier(0);
@@ -506,6 +470,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 
   // join the four waves
   l = column_sum(l);
+  lz = column_sum(lz);
   if (g == 0) {
     sh_m[wave][col] = m;
     sh_l[wave][col] = l;
@@ -514,7 +479,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 #pragma unroll
     for (int n = 0; n < F::kOutMfma; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sh.o[wave][col][F::out_channel(n, 4 * g + i)] = o[n][i];
+      for (int i = 0; i < 4; ++i) sh.o[wave][col][F::out_channel(n, 4 * g + i)] = fmaf(o[n][i], F::kUnit, -lz);
   }
   __syncthreads();
   for (int i = tid; i < heads * (D / 8); i += kAttnThreads) {
