@@ -15,9 +15,9 @@
 // tokens' slots may start anywhere in a quad, so waves look for quads among
 // the slots rather than at multiples of four.
 //
-// What bounds it: vector instructions when coding (about 200 for 8 channels
+// What bounds it: vector instructions when coding (about 190 for 8 channels
 // of a lane, one every 4 cycles on every SIMD: 8191 tokens of 8 heads of 128
-// to 8 bits move 51 MB in 18 us, 2.8 TB/s), so whatever does not depend on the
+// to 8 bits move 51 MB in 17 us, 3 TB/s), so whatever does not depend on the
 // token is kept out of the loop over a wave's quads: the signs, the lane's
 // offsets, the head (22 us before).  Reading takes about 110 and meets the
 // traffic: the same tokens back in 11.9 us, 30011 tokens from 4 bits (156 MB)
@@ -48,21 +48,23 @@ struct Layout {
   __device__ static int64_t value_unit(int t, int u) { return (int64_t)(t >> 2) * 4 * kUnits + 4 * u + (t & 3); }
 };
 
-// Reductions over the 16 lanes of a DPP row, or (D = 64) each 8 of them.
-template <int D>
-__device__ __forceinline__ float row_min(float v) {
-  v = fminf(v, dpp<kQuadXor1>(v));
-  v = fminf(v, dpp<kQuadXor2>(v));
-  v = fminf(v, dpp<kRowHalfMirror>(v));
-  return D == 64 ? v : fminf(v, dpp<kRowMirror>(v));
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_bits(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
 
-template <int D>
-__device__ __forceinline__ float row_max(float v) {
-  v = fmaxf(v, dpp<kQuadXor1>(v));
-  v = fmaxf(v, dpp<kQuadXor2>(v));
-  v = fmaxf(v, dpp<kRowHalfMirror>(v));
-  return D == 64 ? v : fmaxf(v, dpp<kRowMirror>(v));
+// The extreme of numbers of one sign over the 16 lanes of a DPP row, or (D =
+// 64) each 8 of them, by their bits: T int32_t, the largest of positive
+// ones; uint32_t, the smallest of negative ones (zeros of either sign among
+// them lose).  One instruction a step, where floats take three.
+template <int D, class T>
+__device__ __forceinline__ float row_extreme(float f) {
+  T v = __builtin_bit_cast(T, f);
+  v = max(v, (T)dpp_bits<kQuadXor1>((uint32_t)v));
+  v = max(v, (T)dpp_bits<kQuadXor2>((uint32_t)v));
+  v = max(v, (T)dpp_bits<kRowHalfMirror>((uint32_t)v));
+  if (D != 64) v = max(v, (T)dpp_bits<kRowMirror>((uint32_t)v));
+  return __builtin_bit_cast(float, v);
 }
 
 __device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {   // a's upper 32 lanes with b's lower 32
@@ -117,8 +119,8 @@ __device__ __forceinline__ void pair_stage(half2_t (&p)[4], half2_t beta) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t mine = __builtin_bit_cast(uint32_t, p[i]);
-    uint32_t other = (uint32_t)__builtin_amdgcn_mov_dpp((int)mine, CTRL, 0xF, 0xF, true);
-    if (CTRL == kRowHalfMirror) other = (uint32_t)__builtin_amdgcn_mov_dpp((int)other, kQuadRev, 0xF, 0xF, true);   // lane ^ 4
+    uint32_t other = dpp_bits<CTRL>(mine);
+    if (CTRL == kRowHalfMirror) other = dpp_bits<kQuadRev>(other);   // lane ^ 4
     p[i] = __builtin_elementwise_fma(p[i], beta, as_half2(other));
   }
 }
@@ -393,8 +395,8 @@ __device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t
       lo = fminf(lo, v[b][e]);
       hi = fmaxf(hi, v[b][e]);
     }
-  lo = row_min<D>(lo);
-  hi = row_max<D>(hi);
+  lo = row_extreme<D, uint32_t>(lo);
+  hi = row_extreme<D, int32_t>(hi);
   const float qmax = (float)((1 << BITS) - 1);
   _Float16 s16 = (_Float16)fminf(divide(hi - lo, qmax, 1.0f / qmax), 65504.0f);
   if (s16 == (_Float16)0.0f) s16 = (_Float16)1.0f;
@@ -406,8 +408,8 @@ __device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t
   for (int b = 0; b < SETS; ++b) {
     float c[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = rintf(divide(v[b][e], s, r) + z);
-    // whole numbers now; the conversion to a byte clamps to 0 .. 255
+    for (int e = 0; e < 8; ++e) c[e] = divide(v[b][e], s, r) + z;
+    // the conversion to a byte rounds half to even and clamps to 0 .. 255
 #pragma unroll
     for (int e = 0; e < 8 * BITS / 32; ++e) w[b][e] = 0;
     if constexpr (BITS == 8) {
@@ -415,7 +417,7 @@ __device__ __forceinline__ uint32_t code_row(const float (&v)[SETS][8], uint32_t
       for (int e = 0; e < 8; ++e) w[b][e / 4] = __builtin_amdgcn_cvt_pk_u8_f32(c[e], e & 3, w[b][e / 4]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = __builtin_amdgcn_fmed3f(c[e], 0.0f, 15.0f);
+      for (int e = 0; e < 8; ++e) c[e] = __builtin_amdgcn_fmed3f(rintf(c[e]), 0.0f, 15.0f);
 #pragma unroll
       for (int e = 0; e < 8; e += 2) w[b][0] = __builtin_amdgcn_cvt_pk_u8_f32(fmaf(c[e + 1], 16.0f, c[e]), e / 2, w[b][0]);
     }

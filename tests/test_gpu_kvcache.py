@@ -178,6 +178,37 @@ def test_non_finite_rows_stay_alone():
             assert np.array_equal(got[keep], back[w].reshape(8, heads, d)[keep])
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("d,rot", [(64, False), (128, False), (128, True), (256, False)])
+def test_ties_and_signed_zeros(bits, d, rot):
+    """Quotients half way between codes (scale 1), rows without a positive or
+    without a negative value but with zeros of either sign, all zeros, and
+    the smallest numbers."""
+    rng = np.random.default_rng(bits + d)
+    page, heads, qmax = 16, 2, 2 ** bits - 1
+    host, cache = random_cache(rng, 3, page, heads, d, bits, rot)
+    rows = []
+    for low in (0, -3, -qmax // 2, -qmax):
+        r = rng.integers(2 * low, 2 * (low + qmax) + 1, d) / 2
+        r[[1, d - 1]] = low, low + qmax
+        rows.append(r)
+    for sign in (1, -1):
+        r = sign * np.abs(rng.standard_normal(d))
+        r[::3] = 0.0
+        r[1::5] = -0.0
+        rows.append(r)
+        r = np.where(rng.random(d) < 0.5, 0.0, -0.0)
+        r[rng.integers(d)] = sign * 0.25
+        rows.append(r)
+        rows.append(np.full(d, sign * 2.0 ** -24))
+    rows += [np.zeros(d), np.full(d, -0.0), np.where(rng.random(d) < 0.5, 0.0, -0.0)]
+    n = len(rows)
+    x = {w: np.stack([np.stack([rows[i], rows[(i + 5) % n]]) for i in range(n)]).astype(np.float16) for w in "kv"}
+    slots = np.arange(3, 3 + n).astype(np.int32)
+    dq.wq_kv_write(cache, dev(x["k"].reshape(n, -1)), dev(x["v"].reshape(n, -1)), dev(slots))
+    _compare_cache(cache, _expect_write(host, x, slots, page, heads, d, bits), f"ties bits={bits} d={d}")
+
+
 def test_fp16_rows_pass_through():
     # 16 bits without rotation: every bit pattern but a NaN's payload
     say("kv write/read: fp16 bits")
