@@ -41,7 +41,7 @@
 // what a plain read reaches); the longest sequences' last workgroups in a
 // ragged batch (64 up to 4099 tokens, 4 bits: 146 MB in 38 us); the way from
 // the arguments over page table and cache to the join for few tokens (77
-// tokens: 5.5 us, an empty kernel 2.2).  A step of 128 tokens takes a
+// tokens: 5.6 us, an empty kernel 2.2).  A step of 128 tokens takes a
 // workgroup 0.76 us with 4 bits and 1.3 us with 8 where three share a CU.
 // Three waves a SIMD with one set of registers for the codes, asked for
 // again as soon as a half is used, were faster than two waves with two sets
