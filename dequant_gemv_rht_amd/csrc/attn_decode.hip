@@ -45,7 +45,8 @@
 // workgroup 0.76 us with 4 bits and 1.3 us with 8 where three share a CU.
 // Three waves a SIMD with one set of registers for the codes, asked for
 // again as soon as a half is used, were faster than two waves with two sets
-// (64 ragged sequences: 42.6 against 63 us), and four spill.
+// (64 ragged sequences: 42.6 against 63 us), and four spill (64 of 16384
+// tokens, 4 bits: 206 against 195 us).
 #include "wq_internal.h"
 
 #include <cmath>
