@@ -649,7 +649,7 @@ template <int BITS, int D>
 hipError_t launch(const AttnArgs &a, hipStream_t s) {
   const SplitPlan p = plan_for(BITS, D, a.seqs, a.kv_heads, a.group, a.max_len, a.window);
   const int64_t wgs = a.seqs * a.kv_heads * p.qtiles * p.splits;
-  if (wgs > INT32_MAX) return hipErrorInvalidValue;
+  if (wgs > kMaxGroups256) return hipErrorInvalidValue;
   if constexpr (D >= 128) {
     if (a.signs && a.group > 8)
       hipLaunchKernelGGL((attn_split_kernel<BITS, D, true>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);

@@ -667,7 +667,7 @@ hipError_t launch_rows(const RowArgs &a, bool write, hipStream_t s) {
     if (waves >= kManyWaves * kMore) return launch_rows<BITS, D, kMore>(a, write, s);
   }
   const int64_t wgs = (waves + kRowThreads / 64 - 1) / (kRowThreads / 64);
-  if (wgs > INT32_MAX) return hipErrorInvalidValue;
+  if (wgs > kMaxGroups256) return hipErrorInvalidValue;
   if (write)
     hipLaunchKernelGGL((kv_write_kernel<BITS, D, NW>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
   else

@@ -151,6 +151,8 @@ hipError_t launch_gemm_batch(int count, const wq_weight *w, const uint16_t *cons
 
 // Paged key-value cache (kvcache.hip) and attention over it
 // (attn_decode.hip), rotary positions (rope.hip); checks in kv_api.cpp.
+// workgroups of 256 threads that one launch takes (fewer than 2^32 threads)
+constexpr int64_t kMaxGroups256 = (1 << 24) - 1;
 hipError_t launch_kv_write(const wq_kv_cache &c, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
                            const int32_t *slots, int64_t tokens, hipStream_t s);
 hipError_t launch_kv_read(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, uint16_t *k, int64_t ldk,
