@@ -616,8 +616,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Spl
 // heads of 128: 16.5 and 15.2 us; four a CU 18.6).
 int64_t workgroups(int bits, int d) { return d * bits / 8 >= 256 ? 256 : 512; }
 
+// (the window is any number up to INT64_MAX: nothing is added to it before
+// it is known to be below max_len)
 int64_t seen_at_most(int64_t max_len, int64_t window) {
-  return window > 0 && window + 15 < max_len ? window + 15 : max_len;
+  return window > 0 && window < max_len - 15 ? window + 15 : max_len;
 }
 
 // How a call is split: enough workgroups to fill the card, in runs of one

@@ -1,0 +1,39 @@
+"""The host's plan of an attention call: workspace sizes at the extremes of
+their arguments (CPU only; pointers are never dereferenced)."""
+
+import ctypes
+
+import pytest
+
+import dequant_gemv_rht_amd as dq
+
+P = 1 << 20          # an aligned address that is never touched
+ENDS = (0, 1, 14, 15, 16)
+
+
+def cache(bits=8, head_dim=128, kv_heads=8, page_size=64):
+    return ctypes.byref(dq.WqKvCache(bits, head_dim, kv_heads, page_size, 10000, P, P, P, P, None, 0))
+
+
+@pytest.mark.parametrize("bits,head_dim", [(4, 64), (8, 128), (16, 256)])
+@pytest.mark.parametrize("seqs,max_len", [(1, 129), (1, 32001), (3, 5000), (64, 16381), (1, 2 ** 31 - 16385)])
+def test_a_window_past_the_lengths_hides_nothing(bits, head_dim, seqs, max_len):
+    size = lambda w: dq.lib().wq_attn_decode_workspace(cache(bits, head_dim), seqs, 32, max_len, w)   # noqa: E731
+    full = size(0)
+    assert 0 < full < 2 ** 63
+    for w in {max_len + e for e in ENDS} | {2 ** b - 1 - e for b in (32, 62, 63) for e in ENDS}:
+        assert size(w) == full, w
+    # and a call with such a window needs that workspace
+    need = ctypes.c_size_t(full)
+    table = -(-max_len // 64)
+    for w in (max_len, 2 ** 63 - 16, 2 ** 63 - 15, 2 ** 63 - 1):
+        a = (cache(bits, head_dim), P, 32 * head_dim, 32, seqs, P, table, P, max_len, w, 1.0, P, 32 * head_dim)
+        assert dq.lib().wq_attn_decode(*a, None, need, None) == dq.WQ_E_WORKSPACE
+        assert dq.lib().wq_attn_decode(*a, P, full - 1, None) == dq.WQ_E_WORKSPACE
+
+
+def test_a_wider_window_never_needs_less():
+    for seqs in (1, 3, 64):
+        sizes = [dq.lib().wq_attn_decode_workspace(cache(), seqs, 32, 32001, w)
+                 for w in (1, 15, 16, 17, 128, 129, 1000, 5105, 5106, 20000, 31985, 31986, 31987, 32000, 32001, 2 ** 63 - 1)]
+        assert sizes == sorted(sizes)
