@@ -61,10 +61,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef const __attribute__((address_space(4))) int32_t *const_i32;   // scalar loads
 
-constexpr int kAttnThreads = 256, kWaves = 4;
-constexpr int kStep = 32;            // tokens per wave and step
-constexpr int kMinSplit = kWaves * kStep;
-constexpr int kMaxSplit = 5120;
+constexpr int kWaves = kAttnWaves, kAttnThreads = 64 * kWaves, kStep = kAttnStep;
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 constexpr float kNone = -1e30f;      // no term seen yet
 constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
@@ -146,10 +143,6 @@ __device__ __forceinline__ uint4 pack_query(const float (&v)[8]) {
     return make_uint4(pack_half2(v[0], v[4]), pack_half2(v[2], v[6]), pack_half2(v[1], v[5]), pack_half2(v[3], v[7]));
   return make_uint4(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]), pack_half2(v[4], v[5]), pack_half2(v[6], v[7]));
 }
-
-struct SplitPlan {
-  int32_t splits, split_len, qtiles;
-};
 
 // One row's 8 channels in a 16-lane DPP row, rotated back and stored.
 template <int D>
@@ -522,7 +515,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 // holds all the plan's splits that way, else four that meet in LDS.  Latency
 // bound: 3.9 us for 63 splits of 32 heads (0.6 MB) as for 8 of 256, about 2
 // of it what any kernel takes.
-constexpr int kAhead = 4;
+constexpr int kAhead = kJoinAhead;
 template <int D, int HW>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, SplitPlan plan) {
   constexpr int kLanes = D / 8, kParts = 64 * HW / kLanes;
@@ -609,98 +602,42 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_kernel(AttnArgs a, Spl
   store_row<D>(a, v, seq, flips >> (ch & 31), head, c0);
 }
 
-// Workgroups that a call is split into where its sequences and heads alone
-// make fewer: one a CU where a row is 256 bytes or more (such a workgroup
-// keeps enough bytes on the way: 42 MB of 8-bit heads of 256 take 16.8 us
-// with 256 workgroups, 18.5 with 512), two a CU below that (33 MB of 4-bit
-// heads of 128: 16.5 and 15.2 us; four a CU 18.6).
-int64_t workgroups(int bits, int d) { return d * bits / 8 >= 256 ? 256 : 512; }
-
-// (the window is any number up to INT64_MAX: nothing is added to it before
-// it is known to be below max_len)
-int64_t seen_at_most(int64_t max_len, int64_t window) {
-  return window > 0 && window < max_len - 15 ? window + 15 : max_len;
-}
-
-// How a call is split: enough workgroups to fill the card, in runs of one
-// length, at most kMaxSplit tokens each.  A workgroup costs about 0.8 us of
-// its CU beside its tokens (64 x 8 heads of 16381 int8 tokens: 353 us in
-// runs of 4096, 365 of 2048, 379 of 1024), so runs are long where there are
-// workgroups enough, and bounded so that one long sequence among many short
-// ones is still shared out.
-SplitPlan plan_for(int bits, int d, int64_t seqs, int kv_heads, int group, int64_t max_len, int64_t window) {
-  SplitPlan p;
-  p.qtiles = (group + 15) / 16;
-  const int64_t seen = seen_at_most(max_len, window);
-  const int64_t units = seqs * kv_heads * p.qtiles;
-  const int64_t want = (workgroups(bits, d) + units - 1) / units;
-  int64_t splits = (seen + kMinSplit - 1) / kMinSplit;
-  if (splits > want) splits = want;
-  if (splits < (seen + kMaxSplit - 1) / kMaxSplit) splits = (seen + kMaxSplit - 1) / kMaxSplit;
-  if (splits < 1) splits = 1;
-  int64_t len = (seen + splits - 1) / splits;   // runs of one length
-  len = (len + kMinSplit - 1) / kMinSplit * kMinSplit;
-  if (len < kMinSplit) len = kMinSplit;
-  p.split_len = (int32_t)len;
-  p.splits = (int32_t)((seen + len - 1) / len);
-  if (p.splits < 1) p.splits = 1;
-  return p;
-}
-
+// (the caller has checked that both grids fit a launch)
 template <int BITS, int D>
-hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  const SplitPlan p = plan_for(BITS, D, a.seqs, a.kv_heads, a.group, a.max_len, a.window);
-  const int64_t wgs = a.seqs * a.kv_heads * p.qtiles * p.splits;
-  if (wgs > kMaxGroups256) return hipErrorInvalidValue;
+hipError_t launch(const AttnArgs &a, const SplitPlan &p, hipStream_t s) {
+  const dim3 grid((unsigned)p.groups), block(kAttnThreads);
   if constexpr (D >= 128) {
     if (a.signs && a.group > 8)
-      hipLaunchKernelGGL((attn_split_kernel<BITS, D, true>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+      hipLaunchKernelGGL((attn_split_kernel<BITS, D, true>), grid, block, 0, s, a, p);
     else
-      hipLaunchKernelGGL((attn_split_kernel<BITS, D, false>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+      hipLaunchKernelGGL((attn_split_kernel<BITS, D, false>), grid, block, 0, s, a, p);
   } else {
-    hipLaunchKernelGGL((attn_split_kernel<BITS, D, false>), dim3((unsigned)wgs), dim3(kAttnThreads), 0, s, a, p);
+    hipLaunchKernelGGL((attn_split_kernel<BITS, D, false>), grid, block, 0, s, a, p);
   }
-  if (p.splits > 1) {
-    const int64_t rows = a.seqs * a.kv_heads * a.group;
-    if (p.splits <= 64 / (D / 8) * kAhead)
-      hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kAttnThreads), 0, s,
-                         a, p);
-    else
-      hipLaunchKernelGGL((attn_join_kernel<D, kWaves>), dim3((unsigned)rows), dim3(kAttnThreads), 0, s, a, p);
-  }
+  if (p.join_waves == 1)
+    hipLaunchKernelGGL((attn_join_kernel<D, 1>), dim3((unsigned)p.join_groups), block, 0, s, a, p);
+  else if (p.join_waves)
+    hipLaunchKernelGGL((attn_join_kernel<D, kWaves>), dim3((unsigned)p.join_groups), block, 0, s, a, p);
   return hipGetLastError();
 }
 
 template <int BITS>
-hipError_t launch_bits(int d, const AttnArgs &a, hipStream_t s) {
+hipError_t launch_bits(int d, const AttnArgs &a, const SplitPlan &p, hipStream_t s) {
   switch (d) {
-    case 64: return launch<BITS, 64>(a, s);
-    case 128: return launch<BITS, 128>(a, s);
-    case 256: return launch<BITS, 256>(a, s);
+    case 64: return launch<BITS, 64>(a, p, s);
+    case 128: return launch<BITS, 128>(a, p, s);
+    case 256: return launch<BITS, 256>(a, p, s);
   }
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window) {
-  // A bound that grows with seqs and max_len: plan_for splits a unit (a
-  // sequence and up to 16 heads) at most once for every workgroups() / units
-  // units, unless runs are of kMaxSplit tokens, and makes none shorter than
-  // kMinSplit.
-  const int64_t seen = seen_at_most(max_len, window), heads = seqs * q_heads, group = q_heads / c.kv_heads;
-  if (seen <= kMinSplit) return 0;
-  const int64_t fill = heads + workgroups(c.bits, c.head_dim) * (group < 16 ? group : 16);
-  const int64_t few = heads * ((seen + kMinSplit - 1) / kMinSplit), many = heads * ((seen + kMaxSplit - 1) / kMaxSplit);
-  const int64_t filled = fill > many ? fill : many, rows = few < filled ? few : filled;
-  return (size_t)rows * (size_t)(c.head_dim + 4) * sizeof(float);
-}
-
-hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, hipStream_t s) {
+hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, const SplitPlan &p, hipStream_t s) {
   switch (bits) {
-    case 4: return launch_bits<4>(head_dim, a, s);
-    case 8: return launch_bits<8>(head_dim, a, s);
-    case 16: return launch_bits<16>(head_dim, a, s);
+    case 4: return launch_bits<4>(head_dim, a, p, s);
+    case 8: return launch_bits<8>(head_dim, a, p, s);
+    case 16: return launch_bits<16>(head_dim, a, p, s);
   }
   return hipErrorInvalidValue;
 }

@@ -52,13 +52,17 @@ wq_status check_cache(const wq_kv_cache *c, const char *who) {
 }
 
 wq_status check_rows(const wq_kv_cache *c, const void *k, int64_t ldk, const void *v, int64_t ldv,
-                     const int32_t *slots, int64_t tokens, const char *who) {
+                     const int32_t *slots, int64_t tokens, wq::RowPlan *plan, const char *who) {
   const wq_status st = check_cache(c, who);
   if (st != WQ_OK) return st;
   if (tokens < 0) return set_error(WQ_E_ARG, "%s: tokens=%lld", who, (long long)tokens);
   if (tokens > (int64_t)INT32_MAX / 2 / c->kv_heads)
     return set_error(WQ_E_UNSUPPORTED, "%s: tokens * kv_heads of 2^30 or more", who);
   if (tokens == 0) return WQ_OK;
+  *plan = wq::kv_row_plan(c->head_dim, tokens, c->kv_heads);
+  if (plan->groups > wq::kMaxGroups256)
+    return set_error(WQ_E_UNSUPPORTED, "%s: tokens * kv_heads of %lld heads of %d too many for one launch", who,
+                     (long long)(tokens * c->kv_heads), c->head_dim);
   if (!k || !v || !slots) return set_error(WQ_E_ARG, "%s: k, v and slots must be non-NULL", who);
   const int64_t row = (int64_t)c->kv_heads * c->head_dim;
   if (ldk < row || ldv < row)
@@ -96,17 +100,19 @@ extern "C" {
 wq_status wq_kv_write(const wq_kv_cache *cache, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
                       const int32_t *slots, int64_t tokens, void *stream) {
   wq::clear_error();
-  const wq_status st = check_rows(cache, k, ldk, v, ldv, slots, tokens, "wq_kv_write");
+  wq::RowPlan plan;
+  const wq_status st = check_rows(cache, k, ldk, v, ldv, slots, tokens, &plan, "wq_kv_write");
   if (st != WQ_OK || tokens == 0) return st;
-  return hip_status(wq::launch_kv_write(*cache, k, ldk, v, ldv, slots, tokens, (hipStream_t)stream), "wq_kv_write");
+  return hip_status(wq::launch_kv_write(*cache, plan, k, ldk, v, ldv, slots, tokens, (hipStream_t)stream), "wq_kv_write");
 }
 
 wq_status wq_kv_read(const wq_kv_cache *cache, const int32_t *slots, int64_t tokens, uint16_t *k, int64_t ldk,
                      uint16_t *v, int64_t ldv, void *stream) {
   wq::clear_error();
-  const wq_status st = check_rows(cache, k, ldk, v, ldv, slots, tokens, "wq_kv_read");
+  wq::RowPlan plan;
+  const wq_status st = check_rows(cache, k, ldk, v, ldv, slots, tokens, &plan, "wq_kv_read");
   if (st != WQ_OK || tokens == 0) return st;
-  return hip_status(wq::launch_kv_read(*cache, slots, tokens, k, ldk, v, ldv, (hipStream_t)stream), "wq_kv_read");
+  return hip_status(wq::launch_kv_read(*cache, plan, slots, tokens, k, ldk, v, ldv, (hipStream_t)stream), "wq_kv_read");
 }
 
 size_t wq_attn_decode_workspace(const wq_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_len,
@@ -139,6 +145,11 @@ wq_status wq_attn_decode(const wq_kv_cache *cache, const uint16_t *q, int64_t ld
     return set_error(WQ_E_UNSUPPORTED, "%s: seqs * ld past the address range", who);
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(table, 4) || !aligned(lens, 4))
     return set_error(WQ_E_ALIGN, "%s: q and out 16-byte, table and lens 4-byte aligned", who);
+  const wq::SplitPlan plan =
+      wq::attn_plan(cache->bits, cache->head_dim, seqs, cache->kv_heads, q_heads / cache->kv_heads, max_len, window);
+  if (plan.groups > wq::kMaxGroups256 || plan.join_groups > wq::kMaxGroups256)
+    return set_error(WQ_E_UNSUPPORTED, "%s: %lld sequences of %d heads up to %lld tokens are too many workgroups for one launch",
+                     who, (long long)seqs, q_heads, (long long)max_len);
   const size_t need = wq::attn_workspace(*cache, seqs, q_heads, max_len, window);
   if (need > workspace_bytes || (need && !workspace))
     return set_error(WQ_E_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need, workspace_bytes);
@@ -166,7 +177,7 @@ wq_status wq_attn_decode(const wq_kv_cache *cache, const uint16_t *q, int64_t ld
   a.max_len = (int32_t)max_len;
   a.window = (int32_t)(window < max_len ? window : 0);   // a window of max_len or more hides nothing
   a.scale = scale;
-  return hip_status(wq::launch_attn_decode(cache->bits, cache->head_dim, a, (hipStream_t)stream), who);
+  return hip_status(wq::launch_attn_decode(cache->bits, cache->head_dim, a, plan, (hipStream_t)stream), who);
 }
 
 wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, uint16_t *const *y, const int64_t *ldy,

@@ -30,7 +30,6 @@ using namespace dev;
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int64_t kManyWaves = 2048;
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 
 // unit u of token t of a block of 16 (keys) / a quad of 4 (values)
@@ -657,53 +656,51 @@ RowArgs row_args(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, con
   return a;
 }
 
+// (the caller has checked that the grid fits a launch)
 template <int BITS, int D, int NW>
-hipError_t launch_rows(const RowArgs &a, bool write, hipStream_t s) {
-  constexpr int kHeads = Layout<BITS, D>::kHeads;
-  const int64_t waves = (a.tokens + 4 * NW - 1) / (4 * NW) * ((a.kv_heads + kHeads - 1) / kHeads) * 2;
-  // several quads a wave once that still gives every SIMD two waves
-  if constexpr (NW == 1) {
-    constexpr int kMore = D == 256 ? 2 : 4;
-    if (waves >= kManyWaves * kMore) return launch_rows<BITS, D, kMore>(a, write, s);
-  }
-  const int64_t wgs = (waves + kRowThreads / 64 - 1) / (kRowThreads / 64);
-  if (wgs > kMaxGroups256) return hipErrorInvalidValue;
+hipError_t launch_rows(const RowArgs &a, const RowPlan &p, bool write, hipStream_t s) {
+  const dim3 grid((unsigned)p.groups), block(kRowThreads);
   if (write)
-    hipLaunchKernelGGL((kv_write_kernel<BITS, D, NW>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_write_kernel<BITS, D, NW>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((kv_read_kernel<BITS, D, NW>), dim3((unsigned)wgs), dim3(kRowThreads), 0, s, a);
+    hipLaunchKernelGGL((kv_read_kernel<BITS, D, NW>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
+template <int BITS, int D>
+hipError_t launch_rows_quads(const RowArgs &a, const RowPlan &p, bool write, hipStream_t s) {
+  return p.quads == 1 ? launch_rows<BITS, D, 1>(a, p, write, s) : launch_rows<BITS, D, kv_most_quads(D)>(a, p, write, s);
+}
+
 template <int BITS>
-hipError_t launch_rows_bits(int d, const RowArgs &a, bool write, hipStream_t s) {
+hipError_t launch_rows_bits(int d, const RowArgs &a, const RowPlan &p, bool write, hipStream_t s) {
   switch (d) {
-    case 64: return launch_rows<BITS, 64, 1>(a, write, s);
-    case 128: return launch_rows<BITS, 128, 1>(a, write, s);
-    case 256: return launch_rows<BITS, 256, 1>(a, write, s);
+    case 64: return launch_rows_quads<BITS, 64>(a, p, write, s);
+    case 128: return launch_rows_quads<BITS, 128>(a, p, write, s);
+    case 256: return launch_rows_quads<BITS, 256>(a, p, write, s);
   }
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_rows_any(const wq_kv_cache &c, const RowArgs &a, bool write, hipStream_t s) {
+hipError_t launch_rows_any(const wq_kv_cache &c, const RowArgs &a, const RowPlan &p, bool write, hipStream_t s) {
   switch (c.bits) {
-    case 4: return launch_rows_bits<4>(c.head_dim, a, write, s);
-    case 8: return launch_rows_bits<8>(c.head_dim, a, write, s);
-    case 16: return launch_rows_bits<16>(c.head_dim, a, write, s);
+    case 4: return launch_rows_bits<4>(c.head_dim, a, p, write, s);
+    case 8: return launch_rows_bits<8>(c.head_dim, a, p, write, s);
+    case 16: return launch_rows_bits<16>(c.head_dim, a, p, write, s);
   }
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_kv_write(const wq_kv_cache &c, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
-                           const int32_t *slots, int64_t tokens, hipStream_t s) {
-  return launch_rows_any(c, row_args(c, slots, tokens, k, ldk, v, ldv), true, s);
+hipError_t launch_kv_write(const wq_kv_cache &c, const RowPlan &p, const uint16_t *k, int64_t ldk, const uint16_t *v,
+                           int64_t ldv, const int32_t *slots, int64_t tokens, hipStream_t s) {
+  return launch_rows_any(c, row_args(c, slots, tokens, k, ldk, v, ldv), p, true, s);
 }
 
-hipError_t launch_kv_read(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, uint16_t *k, int64_t ldk,
-                          uint16_t *v, int64_t ldv, hipStream_t s) {
-  return launch_rows_any(c, row_args(c, slots, tokens, k, ldk, v, ldv), false, s);
+hipError_t launch_kv_read(const wq_kv_cache &c, const RowPlan &p, const int32_t *slots, int64_t tokens, uint16_t *k,
+                          int64_t ldk, uint16_t *v, int64_t ldv, hipStream_t s) {
+  return launch_rows_any(c, row_args(c, slots, tokens, k, ldk, v, ldv), p, false, s);
 }
 
 }  // namespace wq

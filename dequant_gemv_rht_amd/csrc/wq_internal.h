@@ -150,13 +150,37 @@ hipError_t launch_gemm_batch(int count, const wq_weight *w, const uint16_t *cons
                              const int *ksplit, float *const *part, bool pair_order, hipStream_t s);
 
 // Paged key-value cache (kvcache.hip) and attention over it
-// (attn_decode.hip), rotary positions (rope.hip); checks in kv_api.cpp.
+// (attn_decode.hip), rotary positions (rope.hip); checks in kv_api.cpp,
+// plans in kv_plan.cpp.
 // workgroups of 256 threads that one launch takes (fewer than 2^32 threads)
 constexpr int64_t kMaxGroups256 = (1 << 24) - 1;
-hipError_t launch_kv_write(const wq_kv_cache &c, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
-                           const int32_t *slots, int64_t tokens, hipStream_t s);
-hipError_t launch_kv_read(const wq_kv_cache &c, const int32_t *slots, int64_t tokens, uint16_t *k, int64_t ldk,
-                          uint16_t *v, int64_t ldv, hipStream_t s);
+
+// Plans (kv_plan.cpp): what a call launches.
+constexpr int64_t kManyRowWaves = 2048;
+constexpr int kv_most_quads(int d) { return d == 256 ? 2 : 4; }
+struct RowPlan {
+  int32_t quads;                // of tokens a wave takes: 1 or kv_most_quads
+  int64_t groups;
+};
+RowPlan kv_row_plan(int d, int64_t tokens, int kv_heads);
+
+constexpr int kAttnWaves = 4;
+constexpr int kAttnStep = 32;   // tokens per wave and step
+constexpr int kMinSplit = kAttnWaves * kAttnStep;
+constexpr int kMaxSplit = 5120;
+constexpr int kJoinAhead = 4;   // splits a lane of the joining kernel asks for at once
+struct SplitPlan {
+  int32_t splits, split_len, qtiles;
+  int32_t join_waves;           // a (sequence, head)'s waves in the joining kernel: 0 (one split), 1 or kAttnWaves
+  int64_t groups, join_groups;
+};
+SplitPlan attn_plan(int bits, int d, int64_t seqs, int kv_heads, int group, int64_t max_len, int64_t window);
+size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window);
+
+hipError_t launch_kv_write(const wq_kv_cache &c, const RowPlan &p, const uint16_t *k, int64_t ldk, const uint16_t *v,
+                           int64_t ldv, const int32_t *slots, int64_t tokens, hipStream_t s);
+hipError_t launch_kv_read(const wq_kv_cache &c, const RowPlan &p, const int32_t *slots, int64_t tokens, uint16_t *k,
+                          int64_t ldk, uint16_t *v, int64_t ldv, hipStream_t s);
 
 struct AttnArgs {
   const void *k, *v;
@@ -173,8 +197,7 @@ struct AttnArgs {
   int32_t max_len, window;      // window 0: none
   float scale;
 };
-size_t attn_workspace(const wq_kv_cache &c, int64_t seqs, int32_t q_heads, int64_t max_len, int64_t window);
-hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, hipStream_t s);
+hipError_t launch_attn_decode(int bits, int head_dim, const AttnArgs &a, const SplitPlan &p, hipStream_t s);
 
 struct RopeArray {
   const uint16_t *x;

@@ -362,7 +362,8 @@ typedef struct wq_kv_cache {
  * Errors: WQ_E_ARG (NULL pointer, tokens < 0, ldk or ldv < kv_heads *
  * head_dim, a bad cache descriptor), WQ_E_ALIGN (also ldk, ldv not a
  * multiple of 8), WQ_E_UNSUPPORTED (bits, head_dim, page_size or rht_block
- * not supported, tokens above 2^31 - 1, sizes past 2^31 - 1), WQ_E_HIP. */
+ * not supported, tokens * kv_heads * head_dim of about 2^36 or more, sizes
+ * past 2^31 - 1), WQ_E_HIP. */
 wq_status wq_kv_write(const wq_kv_cache *cache, const uint16_t *k, int64_t ldk, const uint16_t *v,
                       int64_t ldv, const int32_t *slots, int64_t tokens, void *stream);
 
@@ -404,8 +405,10 @@ wq_status wq_kv_read(const wq_kv_cache *cache, const int32_t *slots, int64_t tok
  * give the same bits.  seqs 0 does nothing.
  * Errors (before anything is launched): WQ_E_ARG, WQ_E_ALIGN (ldq, ldo not
  * a multiple of 8), WQ_E_UNSUPPORTED (as above; seqs * heads past 2^31 - 1,
- * max_len above 2^31 - 16385),
- * WQ_E_WORKSPACE; WQ_E_HIP. */
+ * max_len above 2^31 - 16385; more than 2^24 - 1 workgroups: one for each
+ * sequence, key-value head, up to 16 query heads of it and run of a few
+ * thousand tokens, then one for each sequence and query head), WQ_E_WORKSPACE;
+ * WQ_E_HIP. */
 size_t wq_attn_decode_workspace(const wq_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_len,
                                 int64_t window);
 wq_status wq_attn_decode(const wq_kv_cache *cache, const uint16_t *q, int64_t ldq, int32_t q_heads,
@@ -430,7 +433,7 @@ wq_status wq_attn_decode(const wq_kv_cache *cache, const uint16_t *q, int64_t ld
  *   pair_axis  HOST uint8 [rot / 2], each below axes, read during the call
  *              only; NULL: every pair on axis 0
  * head_dim a multiple of 8 up to 256, rot a multiple of 16 up to head_dim,
- * axes 1 to 4, heads up to 65535.  Errors as above. */
+ * axes 1 to 4, heads up to 65535, tokens below 2^25.  Errors as above. */
 #define WQ_ROPE_ADJACENT 1u
 #define WQ_ROPE_MAX_AXES 4
 wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, uint16_t *const *y,

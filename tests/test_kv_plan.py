@@ -1,12 +1,18 @@
-"""The host's plan of an attention call: workspace sizes at the extremes of
-their arguments (CPU only; pointers are never dereferenced)."""
+"""The host's plans of the attention side's calls: workspace sizes at the
+extremes of their arguments, grids too large for a launch, and the planning
+itself under AddressSanitizer and UndefinedBehaviorSanitizer
+(``tests/host/kv_plan_check.cpp``).  CPU only; pointers are never
+dereferenced."""
 
 import ctypes
+import os
+import subprocess
 
 import pytest
 
 import dequant_gemv_rht_amd as dq
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20          # an aligned address that is never touched
 ENDS = (0, 1, 14, 15, 16)
 
@@ -37,3 +43,38 @@ def test_a_wider_window_never_needs_less():
         sizes = [dq.lib().wq_attn_decode_workspace(cache(), seqs, 32, 32001, w)
                  for w in (1, 15, 16, 17, 128, 129, 1000, 5105, 5106, 20000, 31985, 31986, 31987, 32000, 32001, 2 ** 63 - 1)]
         assert sizes == sorted(sizes)
+
+
+@pytest.fixture(scope="module")
+def planner(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("plan") / "plan")
+    csrc = os.path.join(ROOT, "dequant_gemv_rht_amd", "csrc", "kv_plan.cpp")
+    r = subprocess.run(["g++", "-std=c++17", "-g", "-O1", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                        "-D__HIP_PLATFORM_AMD__", "-isystem", "/opt/rocm/include", csrc,
+                        os.path.join(ROOT, "tests", "host", "kv_plan_check.cpp"), "-o", exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    return exe
+
+
+def test_plans_under_asan_ubsan(planner):
+    r = subprocess.run([planner], capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, ASAN_OPTIONS="detect_leaks=0", UBSAN_OPTIONS="print_stacktrace=1"))
+    assert r.returncode == 0 and "checked" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+def test_too_many_workgroups_are_refused_on_the_host():
+    lib, d = dq.lib(), 256
+    # the joining kernel's workgroups are too many, the split kernel's are not
+    seqs, group, max_len = (1 << 20) + 5, 16, 9 * 5120
+    a = (cache(8, d, 1), P, group * d, group, seqs, P, -(-max_len // 64), P, max_len, 0, 1.0, P, group * d, P, 2 ** 63, None)
+    assert lib.wq_attn_decode(*a) == dq.WQ_E_UNSUPPORTED, lib.wq_last_error()
+    assert "workgroups" in lib.wq_last_error().decode()
+    # the split kernel's
+    seqs, group, max_len = 1 << 24, 2, 5120
+    a = (cache(8, d, 1), P, group * d, group, seqs, P, -(-max_len // 64), P, max_len, 0, 1.0, P, group * d, P, 2 ** 63, None)
+    assert lib.wq_attn_decode(*a) == dq.WQ_E_UNSUPPORTED, lib.wq_last_error()
+    # rows of a cache
+    tokens = (1 << 28) + 100
+    assert lib.wq_kv_write(cache(8, d, 1), P, d, P, d, P, tokens, None) == dq.WQ_E_UNSUPPORTED, lib.wq_last_error()
+    assert lib.wq_kv_read(cache(8, d, 1), P, tokens, P, d, P, d, None) == dq.WQ_E_UNSUPPORTED, lib.wq_last_error()
+    assert "too many for one launch" in lib.wq_last_error().decode()
