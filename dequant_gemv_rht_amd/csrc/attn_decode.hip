@@ -65,6 +65,7 @@ constexpr int kWaves = kAttnWaves, kAttnThreads = 64 * kWaves, kStep = kAttnStep
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 constexpr float kNone = -1e30f;      // no term seen yet
 constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
+constexpr float kMaxSum = 8.0f * (float)(1ull << (kGain + kSlack + 24));   // of a lane's 8 weights before the values' scales
 
 // waves per SIMD that the registers are kept for without spilling
 constexpr int occupancy(int bits, int d, bool low) {
@@ -408,8 +409,11 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = __builtin_fmaxf16(top, w[i]);
     float sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-    // (the sum: an infinite p of a row of scale 0 does not show in the w)
-    if (__any(!(top <= (_Float16)(1 << (kGain + kSlack))) || !(sum < INFINITY))) {
+    // (the sum: rows of scale 0 do not show in the w.  A positive scale is
+    // 2^-24 or more, so while the w are in range the other rows' p stay below
+    // 2^(kGain + kSlack + 24); a larger sum is theirs and moves the reference
+    // too, so that no number of them makes l infinite)
+    if (__any(!(top <= (_Float16)(1 << (kGain + kSlack))) || !(sum <= kMaxSum))) {
       // move the reference: the largest term so far becomes 2^kGain (2^-24:
       // the smallest positive scale, so that rows of scale 0 do not leave
       // it unset)
