@@ -369,7 +369,8 @@ def wq_embed(table: QWeight, ids: torch.Tensor, out_dtype=torch.float16, out: Op
 @dataclass
 class KVCache:
     """One layer's paged key-value cache in libwq's layout (``wq_kv_cache``
-    of include/wq.h); ``KVCache.new`` allocates one."""
+    of include/wq.h); ``KVCache.new`` allocates one.  To grow it, assign
+    larger tensors; they are checked together at the next call."""
     bits: int                     # 4, 8 (codes) or 16 (fp16 values)
     head_dim: int                 # 64, 128 or 256
     kv_heads: int
@@ -381,6 +382,28 @@ class KVCache:
     signs: Optional[torch.Tensor] = None       # int32 view of uint32 [kv_heads * head_dim / 32]
 
     def __post_init__(self):
+        self._c   # checks what was given
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        self.__dict__.pop("_c", None)
+        self.__dict__.pop("_at", None)
+
+    def __getattr__(self, name):
+        # the descriptor and the native calls' hold on it, made at the first
+        # use after the fields were assigned
+        if name == "_c":
+            value = self._describe()
+        elif name == "_at":
+            c = self.__dict__["_c"] = self._describe()
+            value = _calls().cache(ctypes.addressof(c), self.k, self.v, *(
+                (None, None) if self.bits == 16 else (self.k_params, self.v_params)), self.signs)
+        else:
+            raise AttributeError(f"{type(self).__name__!r} object has no attribute {name!r}")
+        self.__dict__[name] = value
+        return value
+
+    def _describe(self) -> WqKvCache:
         if self.bits not in (4, 8, 16):
             raise ValueError(f"bits={self.bits} (4, 8 or 16)")
         if self.head_dim not in (64, 128, 256) or self.kv_heads < 1 or self.page_size < 1:
@@ -407,10 +430,9 @@ class KVCache:
             _dev(self.signs, torch.int32, "signs")
             if self.signs.numel() * 32 != self.kv_heads * self.head_dim:
                 raise ValueError(f"signs: {self.signs.numel()} words for {self.kv_heads * self.head_dim} channels")
-        self._c = WqKvCache(self.bits, self.head_dim, self.kv_heads, self.page_size, pages, _ptr(self.k),
-                            _ptr(self.v), _ptr(self.k_params), _ptr(self.v_params), _ptr(self.signs),
-                            128 if self.signs is not None else 0)
-        self._at = ctypes.addressof(self._c)
+        return WqKvCache(self.bits, self.head_dim, self.kv_heads, self.page_size, pages, _ptr(self.k),
+                         _ptr(self.v), _ptr(self.k_params), _ptr(self.v_params), _ptr(self.signs),
+                         128 if self.signs is not None else 0)
 
     @classmethod
     def new(cls, pages: int, page_size: int, kv_heads: int, head_dim: int, bits: int,

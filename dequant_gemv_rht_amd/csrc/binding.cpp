@@ -18,6 +18,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <memory>
 
 #include "../../include/wq.h"
 
@@ -69,10 +70,61 @@ int64_t integer(PyObject *o) {
 
 void expect_args(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, want, " arguments expected, ", n, " given"); }
 
+// A cache as Python holds it: the descriptor, and the tensors it describes.
+struct Cache {
+  static constexpr int kTensors = 5;
+  wq_kv_cache c;
+  at::Tensor t[kTensors];       // k, v, k_params, v_params, signs; some undefined
+  size_t bytes[kTensors];
+};
+constexpr char kCacheName[] = "wq_kv_cache";
+const char *const kTensorNames[Cache::kTensors] = {"k", "v", "k_params", "v_params", "signs"};
+
+void free_cache(PyObject *o) { delete static_cast<Cache *>(PyCapsule_GetPointer(o, kCacheName)); }
+
+// The descriptor with the addresses that the tensors have at this call (a
+// tensor's storage can be replaced under it).  An integer is the address of
+// a descriptor that the caller keeps up itself.
 const wq_kv_cache *cache_at(PyObject *o) {
-  const wq_kv_cache *c = reinterpret_cast<const wq_kv_cache *>(integer(o));
-  TORCH_CHECK_VALUE(c && c->head_dim > 0, "no cache");
-  return c;
+  if (!PyCapsule_CheckExact(o)) {
+    const wq_kv_cache *c = reinterpret_cast<const wq_kv_cache *>(integer(o));
+    TORCH_CHECK_VALUE(c && c->head_dim > 0, "no cache");
+    return c;
+  }
+  Cache *h = static_cast<Cache *>(PyCapsule_GetPointer(o, kCacheName));
+  if (!h) throw python_error();
+  void *at[Cache::kTensors];
+  for (int i = 0; i < Cache::kTensors; ++i) {
+    const at::Tensor &t = h->t[i];
+    at[i] = t.defined() ? t.data_ptr() : nullptr;
+    TORCH_CHECK_VALUE(!t.defined() || (t.nbytes() == h->bytes[i] && t.is_contiguous() && t.is_cuda()), kTensorNames[i],
+                      " is not the contiguous GPU tensor of ", h->bytes[i],
+                      " bytes that was described: assign resized tensors to the KVCache");
+  }
+  h->c.k = at[0];
+  h->c.v = at[1];
+  h->c.k_params = static_cast<uint16_t *>(at[2]);
+  h->c.v_params = static_cast<uint16_t *>(at[3]);
+  h->c.rht_signs = static_cast<const uint32_t *>(at[4]);
+  return &h->c;
+}
+
+// cache(address, k, v, k_params, v_params, signs): a descriptor's copy and its tensors (or None), for the calls below
+PyObject *cache(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  expect_args(n, 1 + Cache::kTensors);
+  auto h = std::make_unique<Cache>();
+  h->c = *cache_at(a[0]);
+  for (int i = 0; i < Cache::kTensors; ++i) {
+    if (a[1 + i] == Py_None) continue;
+    h->t[i] = tensor(a[1 + i], kTensorNames[i]);
+    h->bytes[i] = h->t[i].nbytes();
+  }
+  PyObject *o = PyCapsule_New(h.get(), kCacheName, free_cache);
+  if (!o) throw python_error();
+  h.release();
+  return o;
+  END_HANDLE_TH_ERRORS
 }
 
 // bind(kv_write, kv_read, workspace, attn, rope): the library's functions
@@ -244,7 +296,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 #define WQ_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {WQ_METHOD(bind), WQ_METHOD(kv_write), WQ_METHOD(kv_read), WQ_METHOD(attn_decode), WQ_METHOD(rope),
+PyMethodDef methods[] = {WQ_METHOD(bind), WQ_METHOD(cache), WQ_METHOD(kv_write), WQ_METHOD(kv_read), WQ_METHOD(attn_decode), WQ_METHOD(rope),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_wqpy", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
