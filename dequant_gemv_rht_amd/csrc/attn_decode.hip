@@ -65,6 +65,7 @@ constexpr int kWaves = kAttnWaves, kAttnThreads = 64 * kWaves, kStep = kAttnStep
 constexpr float kInvSqrt128 = 0.08838834764831845f;
 constexpr float kNone = -1e30f;      // no term seen yet
 constexpr int kGain = 8, kSlack = 6; // 2^(kGain + kSlack) < 65504
+constexpr int kQueryTop = 15;        // a rotated query's largest value is 2^14 to 2^15
 constexpr float kMaxSum = 8.0f * (float)(1ull << (kGain + kSlack + 24));   // of a lane's 8 weights before the values' scales
 
 // waves per SIMD that the registers are kept for without spilling
@@ -138,6 +139,16 @@ __device__ __forceinline__ float column_sum(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// A maximum of positive numbers over the D / 8 lanes of a row.
+template <int D>
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<kQuadXor1>(v));
+  v = fmaxf(v, dpp<kQuadXor2>(v));
+  v = fmaxf(v, dpp<kRowHalfMirror>(v));
+  v = fmaxf(v, dpp<kRowMirror>(v));
+  return D == 256 ? fmaxf(v, __shfl_xor(v, 16)) : v;
+}
+
 template <int BITS>
 __device__ __forceinline__ uint4 pack_query(const float (&v)[8]) {
   if (BITS == 4)
@@ -183,7 +194,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
     _Float16 q[LOW ? 32 : 16][kQStride];
     float o[kWaves][16][kOStride];
   } sh;
-  __shared__ float sh_m[kWaves][16], sh_l[kWaves][16];
+  __shared__ float sh_m[kWaves][16], sh_l[kWaves][16], sh_unit[16];
 
   int id = blockIdx.x;
   // the sequences' first splits first: the empty ones of short sequences last
@@ -269,9 +280,11 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
   }
 
   // The queries, rotated as the cache is, rounded to fp16, in the keys'
-  // channel order.  A rotated query is no longer an fp16 value: what the
-  // rounding leaves goes to columns 8 to 15 where there are at most 8 heads,
-  // else to operands of its own, and its scores are added to the heads' own.
+  // channel order.  A rotated query is no longer an fp16 value: each head is
+  // brought to 2^kQueryTop by a power of two (rotated it may be past fp16's
+  // largest number, or need bits below its smallest), what the rounding
+  // leaves goes to columns 8 to 15 where there are at most 8 heads, else to
+  // operands of its own, and its scores are added to the heads' own.
   const bool split_q = !LOW && D >= 128 && a.signs && heads <= 8;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
@@ -287,7 +300,12 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = ((flips >> ((ch + e) & 31)) & 1u) ? -v[e] : v[e];
       fwht128_row16_signed(v, jj);
-      const float sc = fwht_lane_sign(jj) * kInvSqrt128;
+      float top = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+      const int shift = kQueryTop - __builtin_amdgcn_frexp_expf(row_max<D>(top) * kInvSqrt128);
+      if (c0 == 0) sh_unit[h] = ldexpf(1.0f, -shift);
+      const float sc = ldexpf(fwht_lane_sign(jj) * kInvSqrt128, shift);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] *= sc;
     }
@@ -322,6 +340,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
     if constexpr (LOW) ql[m] = operand(16 + col, m);
   }
   qsum = column_sum(qsum);
+  const float unit = D >= 128 && a.signs ? sh_unit[split_q ? col & 7 : col] : 1.0f;
   __syncthreads();   // sh.q is free for sh.o
 
   float m = kNone, l = 0.0f, lz = 0.0f;   // lz: sum of w z
@@ -329,7 +348,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
 #pragma unroll
   for (int n = 0; n < F::kOutMfma; ++n) o[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const float to_log2 = a.scale * 1.4426950408889634f * F::kUnit, zero_sum = -qsum / F::kUnit;
+  const float to_log2 = a.scale * 1.4426950408889634f * F::kUnit * unit, zero_sum = -qsum / F::kUnit;
   for (; t < end; t += kStride) {
     // scores before the keys' scale, in units of log2
     float x[8];
