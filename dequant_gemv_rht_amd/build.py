@@ -6,7 +6,9 @@
 Each source file compiles to its own object in parallel; the library lands
 in ``dequant_gemv_rht_amd/_lib/libwq.so``.  ``csrc/binding.cpp``, the native
 half of the Python binding, compiles against torch's headers with the host
-compiler into ``_lib/_wqpy.so``; it holds no device code.
+compiler into ``_lib/_wqpy.so``; it holds no device code, and where torch's
+headers or a host compiler are missing the library is built without it, with
+a warning.
 """
 
 from __future__ import annotations
@@ -15,6 +17,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -89,8 +92,15 @@ def build(asm: bool = False, jobs: int | None = None) -> str:
     with cf.ThreadPoolExecutor(jobs + 1) as ex:
         binding = ex.submit(build_binding)
         objs = list(ex.map(lambda s: _compile(s, asm), srcs))
-        binding.result()
-    _replace([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC"] + objs, LIB, "link")
+        _replace([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC"] + objs, LIB, "link")
+        try:
+            binding.result()
+        except (RuntimeError, OSError, ImportError) as e:
+            # the linears do not need it; the calls that do say so when used
+            if os.path.exists(BINDING_LIB):
+                os.remove(BINDING_LIB)
+            warnings.warn(f"built without the cache, attention and rotary calls of the Python binding: {e}",
+                          RuntimeWarning, stacklevel=2)
     return LIB
 
 
