@@ -4,7 +4,7 @@
 
 One block's query, key, value and output projections (int4, rotated), rotary
 positions, a paged key-value cache and attention over it.  Weights and
-activations are synthetic.  A decode step is five calls:
+activations are synthetic.  A decode step, or a prompt, is five calls:
 
     q, k, v = the three projections, one launch      (wq_linear_batch)
     q, k    = rotary positions                       (wq_rope)
@@ -70,13 +70,18 @@ class AttentionBlock:
         return page * self.page_size + (positions % self.page_size).to(torch.int32)
 
     def prompt(self, seq, x):
-        """The tokens x [n][hidden] of sequence `seq`, which is empty so far, into the cache."""
+        """The tokens x [n][hidden] of sequence `seq`, which is empty so far, into the cache -> the block's attention
+        output [n][hidden].  Every token is a sequence of its own to the attention call, one longer than the one
+        before, over the same pages."""
         n = x.shape[0]
         positions = torch.arange(n, dtype=torch.int32, device="cuda")
-        _, k, v = self._qkv(x, positions)
+        q, k, v = self._qkv(x, positions)
         dq.wq_kv_write(self.cache, k, v, self._slots(seq, positions).contiguous())
         self.lens[seq] = n
         self.longest = max(self.longest, n)
+        pages = self.table[seq, : -(-n // self.page_size)]
+        y = dq.wq_attn_decode(self.cache, q, pages.repeat(n, 1), positions + 1, max_len=n)
+        return dq.wq_linear(self.weights["o"], y)
 
     def step(self, x):
         """One new token per sequence, x [seqs][hidden] -> the block's attention output [seqs][hidden]."""

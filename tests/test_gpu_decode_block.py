@@ -110,6 +110,24 @@ def test_prompt_and_steps(bits, tol):
             assert rel <= tol
 
 
+@pytest.mark.parametrize("bits,tol", [(16, 5e-3), (8, 1e-2)])
+def test_prompt_outputs(bits, tol):
+    """Every prompt token's output: attention over itself and the tokens before it."""
+    say(f"decode block prompts bits={bits}")
+    hidden, qh, kvh, d, seed = 512, 8, 2, 128, 7
+    b = DB.AttentionBlock(2, 80, hidden, qh, kvh, d, 4, bits, 16, True, 1e4, seed)
+    c = Chain(b, hidden, qh, kvh, d, bits, bits < 16, seed)
+    rng = np.random.default_rng(8)
+    for s, n in enumerate((1, 53)):
+        x = rng.standard_normal((n, hidden)).astype(np.float16)
+        got = b.prompt(s, torch.from_numpy(x).cuda()).float().cpu().numpy()
+        k, v = c.rows(x, np.arange(n))
+        for i in range(n):
+            want = c.attend(x[i:i + 1], k[:i + 1], v[:i + 1])[0]
+            rel = np.linalg.norm(got[i] - want) / np.linalg.norm(want)
+            assert rel <= tol, (s, i, rel)
+
+
 def test_command():
     out = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "decode_block.py"), "--seqs", "2", "--prompt",
                           "70", "--steps", "3", "--bits", "4"], capture_output=True, text=True, timeout=100)
