@@ -75,4 +75,12 @@ RowPlan kv_row_plan(int d, int64_t tokens, int kv_heads) {
   return p;
 }
 
+int32_t rope_rounds(int64_t tokens, int32_t rot, int32_t count, const int32_t *heads) {
+  constexpr int64_t kManyWaves = 8192;   // 8 a SIMD
+  const int32_t slots = 64 / (rot / 16);
+  int64_t waves = 0;   // with one round each
+  for (int32_t i = 0; i < count; ++i) waves += tokens * ((heads[i] + (int64_t)slots - 1) / slots);
+  return waves >= kManyWaves ? kRopeRounds : 1;
+}
+
 }  // namespace wq

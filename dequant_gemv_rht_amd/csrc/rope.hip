@@ -3,11 +3,12 @@
 // token's position on the pair's axis.
 //
 // A lane turns 8 pairs (16 channels), a head is rot / 16 lanes, and a wave
-// takes one token: several heads side by side, then the next ones with the
-// same cosines and sines, which each lane looked up once.  Traffic bound:
-// every value is read and written once, in 16-byte pieces: 6001 tokens of 40
-// heads of 128 with three axes (126 MB) in 24 us, 5.2 TB/s (54 us with a
-// look-up for each head).  16 tokens: 3.4 us, launch and latency.
+// takes several heads of one token side by side: one such round where there
+// are few waves, four with many, for one look-up of the cosines and sines.
+// Traffic bound: every value is read and written once, in 16-byte pieces:
+// 6001 tokens of 40 heads of 128 with three axes (126 MB) in 24 us, 5.2 TB/s
+// (54 us with a look-up for each head).  16 tokens: 3.4 us, launch and
+// latency.
 #include "wq_internal.h"
 
 #include <climits>
@@ -19,7 +20,7 @@ using namespace dev;
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int64_t kManyWaves = 8192;   // 8 a SIMD
+constexpr int kRounds = kRopeRounds;
 
 __device__ __forceinline__ void unpack8(uint4 r, float (&v)[8]) {
   v[0] = half_bits_to_float(r.x & 0xFFFF); v[1] = half_bits_to_float(r.x >> 16);
@@ -37,7 +38,7 @@ struct RopeShape {
   uint32_t axis[WQ_ROPE_MAX_AXES][4];   // the pairs of each axis, one bit each
   int32_t turns, slots;         // lanes of a head; heads side by side in a wave
   uint32_t inv;                 // ceil(2^16 / turns)
-  int32_t rounds;               // times `slots` heads a wave takes
+  int32_t rounds;               // times `slots` heads a wave takes: 1 or kRounds
 };
 
 template <bool ADJACENT>
@@ -76,18 +77,14 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, RopeShap
     const int half = a.rot / 2;
     // the 16 channels as two groups of 8: pairs (lo[e], hi[e]), or neighbours within each
     const int at = ADJACENT ? 2 * p0 : p0, to = ADJACENT ? 2 * p0 + 8 : p0 + half;
-    constexpr int kRounds = 4;   // heads a lane has on the way at once
     uint4 rl[kRounds], rh[kRounds];
-    auto fetch = [&](int h0) {
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const int h = h0 + r * sh.slots + slot;
-        if (h >= last) continue;
-        rl[r] = *reinterpret_cast<const uint4 *>(x + (int64_t)h * a.head_dim + at);
-        rh[r] = *reinterpret_cast<const uint4 *>(x + (int64_t)h * a.head_dim + to);
-      }
-    };
-    fetch(first);
+    for (int r = 0; r < kRounds; ++r) {
+      const int h = first + r * sh.slots + slot;
+      if (h >= last) continue;
+      rl[r] = *reinterpret_cast<const uint4 *>(x + (int64_t)h * a.head_dim + at);
+      rh[r] = *reinterpret_cast<const uint4 *>(x + (int64_t)h * a.head_dim + to);
+    }
     float c[8], s[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -111,19 +108,16 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, RopeShap
         s[e] = (mine >> e) & 1u ? sv[e] : s[e];
       }
     }
-    for (int h0 = first; h0 < last; h0 += kRounds * sh.slots) {
-      if (h0 != first) fetch(h0);
 #pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const int h = h0 + r * sh.slots + slot;
-        if (h >= last) continue;
-        float lo[8], hi[8], out_lo[8], out_hi[8];
-        unpack8(rl[r], lo);
-        unpack8(rh[r], hi);
-        turn<ADJACENT>(lo, hi, c, s, out_lo, out_hi);
-        store8(y + (int64_t)h * a.head_dim + at, out_lo);
-        store8(y + (int64_t)h * a.head_dim + to, out_hi);
-      }
+    for (int r = 0; r < kRounds; ++r) {
+      const int h = first + r * sh.slots + slot;
+      if (h >= last) continue;
+      float lo[8], hi[8], out_lo[8], out_hi[8];
+      unpack8(rl[r], lo);
+      unpack8(rh[r], hi);
+      turn<ADJACENT>(lo, hi, c, s, out_lo, out_hi);
+      store8(y + (int64_t)h * a.head_dim + at, out_lo);
+      store8(y + (int64_t)h * a.head_dim + to, out_hi);
     }
   }
   // channels past `rot`
@@ -145,13 +139,12 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t s) {
   sh.turns = a.rot / 16;
   sh.slots = 64 / sh.turns;
   sh.inv = (65536 + sh.turns - 1) / sh.turns;
-  int most = 0;
-  int64_t waves = 0;   // with one round each
+  int32_t heads[kMaxBatch], most = 0;
   for (int i = 0; i < a.count; ++i) {
-    if (a.arr[i].heads > most) most = a.arr[i].heads;
-    waves += a.tokens * ((a.arr[i].heads + sh.slots - 1) / sh.slots);
+    heads[i] = a.arr[i].heads;
+    if (heads[i] > most) most = heads[i];
   }
-  sh.rounds = waves >= kManyWaves ? 4 : 1;
+  sh.rounds = rope_rounds(a.tokens, a.rot, a.count, heads);
   const int64_t x = (a.tokens + kRopeThreads / 64 - 1) / (kRopeThreads / 64);
   const int64_t y = ((int64_t)most + (int64_t)sh.slots * sh.rounds - 1) / ((int64_t)sh.slots * sh.rounds);
   if (x > INT32_MAX || y > 65535) return hipErrorInvalidValue;

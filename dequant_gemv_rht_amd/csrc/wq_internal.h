@@ -213,6 +213,8 @@ struct RopeArgs {
   int32_t count, head_dim, rot, axes, table_rows, adjacent;
   uint8_t pair_axis[128];       // axis of each pair
 };
+constexpr int kRopeRounds = 4;  // times that many heads side by side, at most: a lane asks for all its heads at once
+int32_t rope_rounds(int64_t tokens, int32_t rot, int32_t count, const int32_t *heads);   // 1 or kRopeRounds
 hipError_t launch_rope(const RopeArgs &a, hipStream_t s);
 
 }  // namespace wq

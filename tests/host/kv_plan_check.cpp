@@ -6,6 +6,7 @@
 // one a line, and prints their plans:
 //   attn bits head_dim seqs kv_heads group max_len window -> splits split_len join_waves
 //   rows head_dim tokens kv_heads -> quads groups
+//   rope tokens rot heads -> rounds
 #include <climits>
 #include <cstdint>
 #include <cstdio>
@@ -64,6 +65,9 @@ int query() {
     if (want == 7) {
       const wq::SplitPlan p = wq::attn_plan((int)v[0], (int)v[1], v[2], (int)v[3], (int)v[4], v[5], v[6]);
       std::printf("%d %d %d\n", p.splits, p.split_len, p.join_waves);
+    } else if (!std::strcmp(kind, "rope")) {
+      const int32_t heads = (int32_t)v[2];
+      std::printf("%d\n", wq::rope_rounds(v[0], (int)v[1], 1, &heads));
     } else {
       const wq::RowPlan p = wq::kv_row_plan((int)v[0], v[1], (int)v[2]);
       std::printf("%d %lld\n", p.quads, (long long)p.groups);
@@ -98,6 +102,13 @@ int main(int argc, char **argv) {
         const int64_t rows = 4 * p.groups * 4 * p.quads * (d == 64 ? 2 : 1);   // of keys and values
         expect(p.quads == 1 || p.quads == wq::kv_most_quads(d), "quads", d, tokens, heads);
         expect(rows >= 2 * tokens * heads, "row grid", d, tokens, heads);
+      }
+  for (int rot = 16; rot <= 256; rot += 16)
+    for (int heads : {1, 8, 65535})
+      for (int64_t tokens : {1LL, 100LL, 33554431LL}) {
+        const int32_t all[wq::kMaxBatch] = {heads, heads, heads, heads, heads, heads, heads, heads};
+        const int r = wq::rope_rounds(tokens, rot, wq::kMaxBatch, all);
+        expect(r == 1 || r == wq::kRopeRounds, "rope", tokens, rot, heads);
       }
   std::printf("checked %ld answers\n", checked);
   return failures ? 1 : 0;

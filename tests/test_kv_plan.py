@@ -11,6 +11,7 @@ import subprocess
 import pytest
 
 import dequant_gemv_rht_amd as dq
+import large_cases as LC
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 P = 1 << 20          # an aligned address that is never touched
@@ -78,3 +79,30 @@ def test_too_many_workgroups_are_refused_on_the_host():
     assert lib.wq_kv_write(cache(8, d, 1), P, d, P, d, P, tokens, None) == dq.WQ_E_UNSUPPORTED, lib.wq_last_error()
     assert lib.wq_kv_read(cache(8, d, 1), P, tokens, P, d, P, d, None) == dq.WQ_E_UNSUPPORTED, lib.wq_last_error()
     assert "too many for one launch" in lib.wq_last_error().decode()
+
+
+def plans(planner, lines):
+    r = subprocess.run([planner, "-"], input="\n".join(lines) + "\n", capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stderr
+    return [tuple(map(int, line.split())) for line in r.stdout.splitlines()]
+
+
+def test_large_cases_enter_the_large_forms(planner):
+    ask = lambda cases: plans(planner, [f"attn {c.bits} {c.d} {c.seqs} {c.heads} {c.group} {c.max_len} {c.window}"   # noqa: E731
+                                        for c in cases])
+    for c, (splits, run, _) in zip(LC.STEPS, ask(LC.STEPS)):
+        assert splits == 1 and run >= 4 * 128, c
+    for c, (splits, run, _) in zip(LC.MASKED + LC.MOVING, ask(LC.MASKED + LC.MOVING)):
+        assert splits == 1 and run >= 3 * 128, c
+    for c, (splits, run, _) in zip(LC.UNWRITTEN, ask(LC.UNWRITTEN)):
+        assert splits == 64 // c.seqs and run == 2048 // splits, c
+    for c, (splits, run, _) in zip(LC.SPLIT_STEPS, ask(LC.SPLIT_STEPS)):
+        assert splits > 1 and run >= 4 * 128, c
+    for c, (splits, _, waves) in zip(LC.JOINS, ask(LC.JOINS)):
+        assert waves == 4 and splits > 4 * (4 * 64 * 8 // c.d), c   # four asked for at once by each of a head's groups of lanes
+    for c, (quads, _) in zip(LC.ROWS, plans(planner, [f"rows {c.d} {c.tokens} {c.heads}" for c in LC.ROWS])):
+        assert quads == (2 if c.d == 256 else 4), c
+    for c, (rounds,) in zip(LC.ROPE, plans(planner, [f"rope {c.tokens} {c.rot} {c.heads}" for c in LC.ROPE])):
+        assert rounds == 4, c
+    more = [c for c in LC.ROPE if c.heads > 4 * (64 // (c.rot // 16))]
+    assert more and len(more) < len(LC.ROPE)
