@@ -424,12 +424,13 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
       }
     };
     weigh();
-    _Float16 top = w[0];
+    // (absolute values: a scale may be negative)
+    _Float16 top = __builtin_fabsf16(w[0]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) top = __builtin_fmaxf16(top, w[i]);
+    for (int i = 1; i < 8; ++i) top = __builtin_fmaxf16(top, __builtin_fabsf16(w[i]));
     float sum = ((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7]));
-    // (the sum: rows of scale 0 do not show in the w.  A positive scale is
-    // 2^-24 or more, so while the w are in range the other rows' p stay below
+    // (the sum: rows of scale 0 do not show in the w.  Other scales are 2^-24
+    // or more, so while the w are in range the other rows' p stay below
     // 2^(kGain + kSlack + 24); a larger sum is theirs and moves the reference
     // too, so that no number of them makes l infinite)
     if (__any(!(top <= (_Float16)(1 << (kGain + kSlack))) || !(sum <= kMaxSum))) {
@@ -441,7 +442,7 @@ __global__ __launch_bounds__(kAttnThreads, occupancy(BITS, D, LOW)) void attn_sp
       for (int i = 0; i < 8; ++i)
         high = fmaxf(high, BITS == 16 ? x[i]
                                       : (float)as_half2(kp[i >> 1])[i & 1] * x[i] +
-                                            fmaxf(__builtin_amdgcn_logf((float)as_half2(vs.par[i >> 2][i & 3])[0]), -24.0f));
+                                            fmaxf(__builtin_amdgcn_logf(fabsf((float)as_half2(vs.par[i >> 2][i & 3])[0])), -24.0f));
       high = column_max(high) - (float)kGain;
       const float keep = __builtin_amdgcn_exp2f(m - high);
       m = high;

@@ -144,6 +144,37 @@ def test_scores_and_value_scales_move_from_step_to_step(bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("part", [1.0, 0.5])
+def test_negative_scales(bits, part):
+    """Codes from elsewhere: (c, z, s) and (qmax - c, qmax - z, -s) stand for
+    the same value.  All rows, or half of them, in the second form, scores
+    that rise by about 60: weights far above the running reference show in
+    negative products only."""
+    say(f"attn negative scales bits={bits} part={part}")
+    rng = np.random.default_rng(95 + bits)
+    heads, group, d, page, seqs, n = next((c.heads, c.group, c.d, c.page, c.seqs, c.max_len) for c in MOVING if c.bits == bits)
+    pages, qmax = -(-n // page), 2 ** bits - 1
+    at = np.arange(pages * page).reshape(pages, 1, page)
+    k = 0.1 * rng.standard_normal((pages, heads, page, d)).astype(np.float32)
+    k[..., 0] = at * (60.0 / n)
+    host = {"signs": None}
+    for w, x in (("k", k), ("v", rng.standard_normal(k.shape).astype(np.float32))):
+        c, s, z = OK.code_rows(x, bits)
+        turned = rng.random(s.shape) < part
+        c = np.where(turned[..., None], qmax - c, c).astype(np.uint8)
+        z, s = np.where(turned, np.float16(qmax) - z, z), np.where(turned, -s, s)
+        host[w], host[w + "_params"] = OK.pack_pages(w, c, bits), np.stack([s, z], -1).astype(np.float16)
+    cache = device_cache(host, page, heads, d, bits)
+    q = rng.standard_normal((1, heads * group, d)).astype(np.float16)
+    q[..., 0] = 1.0
+    table = np.arange(pages, dtype=np.int32)[None]
+    got = dq.wq_attn_decode(cache, dev(q.reshape(1, -1)).repeat(seqs, 1), dev(table).repeat(seqs, 1),
+                            torch.full((seqs,), n, dtype=torch.int32, device="cuda"), scale=1.0)
+    check(got[:1], reference(host, bits, d, page, q, table, [n], 1.0), "negative scales")
+    assert torch.equal(got, got[:1].repeat(seqs, 1))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("seqs", [64, 32])
 def test_many_value_rows_of_scale_zero(bits, seqs):
     """Most rows of a sequence were never written (a cleared page: scale 0,
