@@ -22,11 +22,19 @@ int64_t seen_at_most(int64_t max_len, int64_t window) {
 }  // namespace
 
 // How a call is split: enough workgroups to fill the card, in runs of one
-// length, at most kMaxSplit tokens each.  A workgroup costs about 0.8 us of
-// its CU beside its tokens (64 x 8 heads of 16381 int8 tokens: 353 us in
-// runs of 4096, 365 of 2048, 379 of 1024), so runs are long where there are
-// workgroups enough, and bounded so that one long sequence among many short
-// ones is still shared out.
+// length from kMinSplit (a step of each wave) to kMaxSplit tokens.
+// kMaxSplit: short runs cost a workgroup's start and end each and more to
+// join, long ones leave uneven sequences uneven.  Time over that of the
+// traffic alone, geometric means over 64 x 8 heads of 128, 4 and 8 bits, 1500
+// to 16381 tokens and five batches of 40 to 128 sequences:
+//   runs of at most      1024  2048  4096  8192  16384
+//   up to that length    1.41  1.37  1.36  1.39  1.39
+//   all of that length   1.21  1.15  1.14  1.11  1.10
+// 4096, the best where lengths differ, also bounds what one long sequence
+// among short ones waits for.
+// kMinSplit: two runs and their join are slower than one run up to about 512
+// tokens (one sequence of 8 heads, 8 bits: 256 tokens 8.9 us, 6.6 as one run;
+// 512 8.9 and 7.9) and faster from 1024 (9.2 and 11.3).
 SplitPlan attn_plan(int bits, int d, int64_t seqs, int kv_heads, int group, int64_t max_len, int64_t window) {
   SplitPlan p;
   p.qtiles = (group + 15) / 16;

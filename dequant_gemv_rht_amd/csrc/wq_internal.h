@@ -167,7 +167,7 @@ RowPlan kv_row_plan(int d, int64_t tokens, int kv_heads);
 constexpr int kAttnWaves = 4;
 constexpr int kAttnStep = 32;   // tokens per wave and step
 constexpr int kMinSplit = kAttnWaves * kAttnStep;
-constexpr int kMaxSplit = 5120;
+constexpr int kMaxSplit = 4096;
 constexpr int kJoinAhead = 4;   // splits a lane of the joining kernel asks for at once
 struct SplitPlan {
   int32_t splits, split_len, qtiles;
