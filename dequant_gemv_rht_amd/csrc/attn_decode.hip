@@ -30,7 +30,7 @@
 // now by 2.3e-4 as the others).  Keys' scores do not need that: their lower
 // nibbles have sums of their own, taken 16-fold.
 // The values' scale goes into the weight, p s, before it is rounded to
-// fp16; the running reference m therefore tracks max(u + log2 s), so that
+// fp16; the running reference m therefore tracks max(u + log2 |s|), so that
 // p s of the largest term stays near 2^kGain and weights down to 2^-20 of
 // it keep fp16's 11 bits whatever the scales are.  m moves only when a term
 // exceeds 2^kSlack above it, which after the first steps is rare: the

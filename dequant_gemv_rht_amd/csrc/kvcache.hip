@@ -566,7 +566,7 @@ __global__ __launch_bounds__(kRowThreads) void kv_read_kernel(RowArgs a) {
   const int mask = (1 << a.page_shift) - 1;
   auto give = [&](int64_t token, const u32x4 &y, int b) {
     u32x4 *to = reinterpret_cast<u32x4 *>(it.x + token * it.ld + 128 * b);
-    // many rows: streamed past the caches (30011 4-bit rows: 38 us, 44 without)
+    // many rows: streamed past the caches (30011 4-bit rows read again and again: 38 us a pass, 45 without)
     if constexpr (NW > 1)
       __builtin_nontemporal_store(y, to);
     else

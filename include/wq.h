@@ -328,8 +328,9 @@ wq_status wq_embed(const wq_weight *w, const int32_t *ids, int64_t count, void *
  *  - k_params, v_params: fp16 [pages][kv_heads][page_size][2], a row's
  *    scale and zero (not read or written for 16 bits; may be NULL).  A zero
  *    is a whole number from 0 to 2^bits - 1, as wq_kv_write stores it; codes
- *    brought in from elsewhere have to keep to that (the kernels form code -
- *    zero in fp16, exact for whole numbers only).
+ *    brought in from elsewhere have to keep to that (wq_kv_read forms code -
+ *    zero in fp16, exact for whole numbers only); their scales may have
+ *    either sign.
  * The layouts hand the attention kernel's matrix instructions their
  * operands in whole 16-byte loads.  int32 arrays (slots, tables, lengths,
  * positions) need 4-byte alignment only. */
