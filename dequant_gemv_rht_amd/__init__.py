@@ -21,6 +21,10 @@ Functions mirror the C ABI in ``include/wq.h``:
   wq_kv_read(cache, slots, out=None)                 -> (k, v) rows as fp16
   wq_attn_decode(cache, q, table, lens, max_len=None, window=0, scale=None, ...) -> out
   wq_rope(xs, cos, sin, positions, head_dim, pair_axis=None, adjacent=False, out=None) -> [y]
+  wq_kv_slots(page_size, pages, table, lens, new_tokens, free_pages, used, tokens, out=None)
+                                                     -> (slots, positions, seq_of, lens, last, used)
+  wq_lora(a, b, xs, ids, bases, scales=None, ...)    -> (y, ...): each row's adapter beside shared linears
+  wq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, ...) -> (ids, logprobs)
 """
 
 from __future__ import annotations
@@ -58,6 +62,10 @@ class WqWeight(ctypes.Structure):
                 ("block_bits_host", _vp)]
 
 
+class WqAdapters(ctypes.Structure):
+    _fields_ = [("n", _i64), ("k", _i64), ("count", _i32), ("rank", _i32), ("a", _vp), ("b", _vp), ("scales", _vp)]
+
+
 class WqKvCache(ctypes.Structure):
     _fields_ = [("bits", _i32), ("head_dim", _i32), ("kv_heads", _i32), ("page_size", _i32),
                 ("pages", _i64), ("k", _vp), ("v", _vp), ("k_params", _vp), ("v_params", _vp),
@@ -89,6 +97,13 @@ SIGNATURES = {
                               ctypes.c_float, _vp, _i64, _vp, _sz, _vp]),
     "wq_rope": (_i32, [_i32, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _i32, _vp,
                        _u32, _vp]),
+    "wq_kv_slots": (_i32, [_i32, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                           _vp, _vp, _vp]),
+    "wq_lora_workspace": (_sz, [_i32, ctypes.POINTER(WqAdapters), _i64]),
+    "wq_lora": (_i32, [_i32, ctypes.POINTER(WqAdapters), _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                       _vp]),
+    "wq_sample_workspace": (_sz, [_i64, _i64]),
+    "wq_sample": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 64 << 20   # WQ_NOALLOC_SCRATCH_BYTES
 
@@ -131,8 +146,11 @@ def _calls():
         spec = importlib.util.spec_from_file_location("_wqpy", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.bind(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in
-                      ("wq_kv_write", "wq_kv_read", "wq_attn_decode_workspace", "wq_attn_decode", "wq_rope")))
+        for bind, names in ((module.bind, ("wq_kv_write", "wq_kv_read", "wq_attn_decode_workspace", "wq_attn_decode",
+                                           "wq_rope")),
+                            (module.bind_serve, ("wq_kv_slots", "wq_lora_workspace", "wq_lora", "wq_sample_workspace",
+                                                 "wq_sample"))):
+            bind(*(ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in names))
         _native = module
     return _native
 
@@ -502,6 +520,67 @@ def wq_rope(xs: Sequence[torch.Tensor], cos: torch.Tensor, sin: torch.Tensor, po
     r = (_native or _calls()).rope(xs, cos, sin, positions, head_dim, pair_axis, adjacent, out)
     if type(r) is int:
         _check("wq_rope", r)
+    return r
+
+
+def wq_kv_slots(page_size: int, pages: int, table: torch.Tensor, lens: torch.Tensor, new_tokens: torch.Tensor,
+                free_pages: torch.Tensor, used: torch.Tensor, tokens: int,
+                out: Optional[Sequence[torch.Tensor]] = None):
+    """Pages, slots and positions of the ``new_tokens`` (int32 [seqs]) that a
+    step of ``tokens`` rows adds to sequences of ``lens`` tokens: new pages go
+    from ``free_pages[used:]`` into ``table`` (int32 [seqs][pages of one],
+    changed in place).  Returns (slots, positions, seq_of), each int32
+    [tokens], (lens, last), each int32 [seqs], and used, int32 [1], all new
+    tensors or those of ``out``.  -1 marks rows of no served sequence."""
+    r = (_native or _calls()).kv_slots(page_size, pages, table, lens, new_tokens, free_pages, used, tokens, out)
+    if type(r) is int:
+        _check("wq_kv_slots", r)
+    return r
+
+
+def wq_lora_workspace(a: Sequence[torch.Tensor], b: Sequence[torch.Tensor], m: int) -> int:
+    size = (_native or _calls()).lora_workspace(a, b, m)
+    if size < 0:
+        raise WqError("wq_lora_workspace", WQ_E_ARG, lib().wq_last_error().decode())
+    return size
+
+
+def wq_lora(a: Sequence[torch.Tensor], b: Sequence[torch.Tensor], xs: Sequence[torch.Tensor], ids: torch.Tensor,
+            bases: Sequence[torch.Tensor], scales=None, workspace: Optional[torch.Tensor] = None,
+            out: Optional[Sequence[torch.Tensor]] = None):
+    """Low-rank adapters beside up to WQ_MAX_BATCH shared linears: for every
+    linear i, y[i] = bases[i] + scales[d] * (xs[i] @ a[i][d].T) @ b[i][d].T
+    with d = ids[row] (int32 [rows]; outside the adapters: bases[i]).  ``a[i]``
+    fp16 [adapters][rank][k], ``b[i]`` fp16 [adapters][n][rank], ``bases`` what
+    wq_linear or wq_linear_batch gave for ``xs`` (fp16 or fp32), ``scales`` fp32
+    [adapters], one for all linears or one each.  ``out`` may be ``bases``
+    itself (in place); ``workspace``: wq_lora_workspace bytes."""
+    r = (_native or _calls()).lora(a, b, xs, ids, bases, scales, workspace, out)
+    if type(r) is int:
+        _check("wq_lora", r)
+    return r
+
+
+def wq_sample_workspace(rows: int, vocab: int) -> int:
+    size = lib().wq_sample_workspace(rows, vocab)
+    if size == ctypes.c_size_t(-1).value:
+        raise WqError("wq_sample_workspace", WQ_E_ARG, lib().wq_last_error().decode())
+    return size
+
+
+def wq_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+              top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+              min_p: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              out: Optional[Sequence[torch.Tensor]] = None):
+    """The next token of each row of ``logits`` (fp16 or fp32 [rows][vocab],
+    any row stride), drawn with the given ``u`` (fp32 [rows] in [0, 1)) under
+    the row's own ``temperature`` (fp32; 0: greedy), ``top_k`` (int32; 0: off),
+    ``top_p`` (fp32; 1: off) and ``min_p`` (fp32; 0: off).  Returns (ids int32
+    [rows], logprobs fp32 [rows]), new tensors or those of ``out``; id -1
+    where a row has nothing to draw."""
+    r = (_native or _calls()).sample(logits, u, temperature, top_k, top_p, min_p, workspace, out)
+    if type(r) is int:
+        _check("wq_sample", r)
     return r
 
 

@@ -217,6 +217,46 @@ constexpr int kRopeRounds = 4;  // times that many heads side by side, at most: 
 int32_t rope_rounds(int64_t tokens, int32_t rot, int32_t count, const int32_t *heads);   // 1 or kRopeRounds
 hipError_t launch_rope(const RopeArgs &a, hipStream_t s);
 
+// A serving step's slots (kv_slots.hip), adapters (lora.hip) and tokens
+// (sample.hip); checks and plans in serve_api.cpp.
+struct SlotsArgs {
+  int32_t *table;
+  const int32_t *lens, *new_tokens, *free_pages, *used;
+  int32_t *slots, *positions, *seq_of, *lens_out, *last, *used_out;
+  int64_t ld_table;
+  int32_t table_pages, seqs, free_count, tokens, pages, page_shift;
+};
+hipError_t launch_kv_slots(const SlotsArgs &a, hipStream_t s);
+
+struct LoraDesc {
+  const uint16_t *a, *b;
+  const float *scales;
+  const uint16_t *x;
+  const void *base;
+  void *y;
+  float *t;                     // A x: [m][rank]
+  int64_t ldx, ldb, ldy;
+  int32_t n, k, count, rank, f32;
+};
+struct LoraArgs {
+  LoraDesc lin[kMaxBatch];
+  const int32_t *ids;
+  int32_t count, m;
+};
+hipError_t launch_lora(const LoraArgs &a, hipStream_t s);
+
+struct SampleArgs {
+  const void *logits;
+  int64_t ldl;
+  const float *u, *temperature, *top_p, *min_p;
+  const int32_t *top_k;
+  int32_t *ids;
+  float *logprobs;
+  int32_t rows, vocab, f32;
+  int32_t unit;                 // weights are counted in 2^-unit
+};
+hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
+
 }  // namespace wq
 
 // ---------------------------------------------------------------------------

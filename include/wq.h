@@ -442,6 +442,133 @@ wq_status wq_rope(int32_t count, const uint16_t *const *x, const int64_t *ldx, u
                   const float *cos, const float *sin, int64_t table_rows, const int32_t *positions,
                   int64_t ld_pos, int32_t axes, const uint8_t *pair_axis, uint32_t flags, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What a serving step of many requests needs around the calls above: pages
+ * and slots for its tokens, each request's low-rank adapter beside the
+ * shared projections, and each request's next token.
+ */
+
+/* Pages, cache slots and positions of the tokens that a step adds to its
+ * sequences.  Sequence s holds lens[s] tokens and gets new_tokens[s] more;
+ * their rows follow each other, sequence by sequence, from row 0 on.  A
+ * sequence needs ceil((lens + new) / page_size) - ceil(lens / page_size)
+ * pages, the next ones of the free list from place used[0] on, in the
+ * sequences' order.  It is served if
+ *  - its last row is below `tokens`,
+ *  - lens + new tokens fit table_pages pages, and
+ *  - it needs no page, or the free list holds the pages that it and the
+ *    sequences before it need (those that fail one of the first two need
+ *    none).
+ * Every row gets
+ *   slots      page * page_size + position % page_size (wq_kv_write), with
+ *              the page of the table or of the free list; -1 for a page
+ *              outside [0, pages)
+ *   positions  lens[s], lens[s] + 1, ... (wq_rope)
+ *   seq_of     s
+ * and -1 in all three where it belongs to no served sequence: wq_kv_write
+ * skips it, wq_rope leaves it as it is.  Every sequence gets
+ *   lens_out   lens + new, or lens where it is not served
+ *   last       the row of its last new token; -1 if it has none or is not
+ *              served
+ *   table      [s][j] of the pages it was given; all else is left as it was
+ * and used_out[0] is used[0] plus the pages given out.  So a call repeated
+ * with the same inputs gives the same again.
+ *   page_size  a power of two, at least 16; pages * page_size at most
+ *              2^31 - 1 (the cache's)
+ *   table      device int32 [seqs][ld_table], table_pages <= ld_table columns
+ *   lens, new_tokens  device int32 [seqs]; negative values count as 0
+ *              (lens_out keeps a negative length of a sequence not served)
+ *   free_pages device int32 [free_count]; used: device int32 [1], a value
+ *              outside [0, free_count] counts as an empty list
+ *   tokens     rows of the step, at most 2^30 (more than the sequences have:
+ *              a captured step's padding)
+ *   slots, positions, seq_of  out: device int32 [tokens]
+ *   lens_out, last  out: device int32 [seqs];  used_out  out: device int32 [1]
+ * No output may overlap an input or another output.  int32 arrays need
+ * 4-byte alignment.  Errors (before anything is launched): WQ_E_ARG (also an
+ * output that overlaps another array), WQ_E_ALIGN, WQ_E_UNSUPPORTED (a page
+ * size or count as above, seqs above 2^20); WQ_E_HIP. */
+wq_status wq_kv_slots(int32_t page_size, int64_t pages, int32_t *table, int64_t ld_table, int64_t table_pages,
+                      const int32_t *lens, const int32_t *new_tokens, int64_t seqs, const int32_t *free_pages,
+                      int64_t free_count, const int32_t *used, int64_t tokens, int32_t *slots, int32_t *positions,
+                      int32_t *seq_of, int32_t *lens_out, int32_t *last, int32_t *used_out, void *stream);
+
+/* The low-rank adapters of one linear: adapter i adds scales[i] B_i A_i to
+ * its weight. */
+typedef struct wq_adapters {
+  int64_t n, k;                 /* the linear's: output rows, input channels (a multiple of 128) */
+  int32_t count;                /* adapters */
+  int32_t rank;                 /* a multiple of 8, 8 to 128 */
+  const uint16_t *a;            /* fp16 [count][rank][k] */
+  const uint16_t *b;            /* fp16 [count][n][rank] */
+  const float *scales;          /* fp32 [count], or NULL for 1 */
+} wq_adapters;
+
+/* The adapters of many requests beside shared projections (up to
+ * WQ_MAX_BATCH linears in one call, whose results `base` wq_linear or
+ * wq_linear_batch left):
+ *   y[i][r] = base[i][r] + scales[d] B_d (A_d x[i][r]),  d = ids[r],
+ * for rows r = 0 .. m - 1 of every linear i.  A row whose id is outside
+ * [0, count) gets base[i][r].  x is what the linear was given, not rotated.
+ * Sums are fp32; A x enters the second product as two fp16 parts under a
+ * power of two of its row (22 bits), and y is rounded once.  Rows with one
+ * adapter share its weights wherever they stand, up to 256 rows; above, up
+ * to 64 of them in each 64 rows in succession, so rows of one request should
+ * then stand together.  An infinity or a NaN in a row of x or base reaches
+ * that row of y only.  Results do not depend on timing.
+ *   w          host array [count] of descriptors
+ *   x          fp16 [m][ldx[i]]
+ *   ids        device int32 [m], one for all linears
+ *   base, y    fp16 or fp32 (dtype[i]) [m][ldb[i]], [m][ldy[i]]; y[i] may
+ *              equal base[i] when ldy == ldb, and overlaps no other array;
+ *              ldb and ldy at least n, of any alignment
+ *   workspace  device scratch of wq_lora_workspace bytes (A x of every row)
+ * m 0 does nothing.  Errors (before anything is launched): WQ_E_ARG,
+ * WQ_E_ALIGN (also ldx not a multiple of 8; ids need 4-byte alignment),
+ * WQ_E_UNSUPPORTED (rank or k as above, m of 2^24 or more, n of 2^30 or
+ * more), WQ_E_WORKSPACE; WQ_E_HIP. */
+size_t wq_lora_workspace(int32_t count, const wq_adapters *w, int64_t m);
+wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x, const int64_t *ldx, int64_t m,
+                  const int32_t *ids, const void *const *base, const int64_t *ldb, void *const *y,
+                  const int64_t *ldy, const wq_dtype *dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The next token of every row of logits (a head's wq_linear; its ids are
+ * wq_embed's), under settings of the row's own.  With T = temperature,
+ *   w_i = exp((logit_i - max) / T),
+ * and the tokens by falling logit, equal ones by rising index:
+ *   top_k  the first top_k of them;
+ *   top_p  of these, those before which less than top_p of their sum of w
+ *          lies (the first one always);
+ *   min_p  of these, those with w_i >= min_p.
+ * The token drawn is the first by index at which the sum of the w kept so
+ * far passes u times all of it; logprob is the log of the chance it had,
+ * ln(w / sum of the w kept).
+ *   logits   fp16 or fp32 (dtype) [rows][ldl], ldl >= vocab of any
+ *            alignment; -infinity and NaN are never drawn; with +infinity
+ *            in a row, only these are (w = 1)
+ *   u        device fp32 [rows] in [0, 1) (outside, NaN: the nearest of 0
+ *            and 1)
+ *   temperature, top_k, top_p, min_p  device fp32 (top_k int32) [rows], or
+ *            NULL for 1, 0, 1, 0.  T of 0 or less, or NaN, is greedy: the
+ *            largest logit of lowest index, logprob 0.  top_k of 0 or less,
+ *            top_p of 1 or more or NaN, min_p of 0 or less or NaN are off;
+ *            a min_p above 1 counts as 1.
+ *   ids      out: device int32 [rows]; -1 for a row in which nothing can
+ *            be drawn
+ *   logprobs out: device fp32 [rows], or NULL; -infinity for such a row
+ *   workspace  device scratch of wq_sample_workspace bytes; no
+ *            initialisation needed
+ * Sums of w are whole multiples of 2^-44 or less of the largest (for vocab
+ * up to 2^18; twice that for each doubling), added exactly in 64 bits: the
+ * same inputs give the same token, whatever the timing.  rows 0 does
+ * nothing.  Errors (before anything is launched): WQ_E_ARG, WQ_E_ALIGN (int32
+ * and fp32 arrays other than logits need 4-byte alignment), WQ_E_UNSUPPORTED
+ * (vocab above 2^20, rows above 2^20), WQ_E_WORKSPACE; WQ_E_HIP. */
+size_t wq_sample_workspace(int64_t rows, int64_t vocab);
+wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vocab, int64_t ldl, const float *u,
+                    const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                    int32_t *ids, float *logprobs, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Message for the last failed call on this thread ("" if none). */
 const char *wq_last_error(void);
 
