@@ -33,11 +33,6 @@ bool overlap(const Range &a, const Range &b) {
   return a.begin != a.end && b.begin != b.end && a.begin < b.end && b.begin < a.end;
 }
 
-// the workspace of each linear's A x, in succession
-size_t inner_bytes(const wq_adapters &w, int64_t m) {
-  return ((size_t)m * (size_t)w.rank * sizeof(float) + 255) / 256 * 256;
-}
-
 wq_status check_adapters(int32_t count, const wq_adapters *w, int64_t m, const char *who) {
   if (count <= 0 || count > WQ_MAX_BATCH)
     return set_error(WQ_E_ARG, "%s: count=%d (1 to %d)", who, count, WQ_MAX_BATCH);
@@ -125,7 +120,7 @@ size_t wq_lora_workspace(int32_t count, const wq_adapters *w, int64_t m) {
   wq::clear_error();
   if (check_adapters(count, w, m, "wq_lora_workspace") != WQ_OK) return (size_t)-1;
   size_t bytes = 0;
-  for (int i = 0; i < count; ++i) bytes += inner_bytes(w[i], m);
+  for (int i = 0; i < count; ++i) bytes += wq::lora_workspace(w[i], m);
   return bytes;
 }
 
@@ -166,7 +161,7 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
     out[i] = rows(y[i], m, ldy[i], w[i].n, size);
     a.lin[i] = {w[i].a, w[i].b, w[i].scales, x[i], base[i], y[i], nullptr, ldx[i], ldb[i], ldy[i],
                 (int32_t)w[i].n, (int32_t)w[i].k, w[i].count, w[i].rank, dtype[i] == WQ_F32};
-    need += inner_bytes(w[i], m);
+    need += wq::lora_workspace(w[i], m);
   }
   for (int i = 0; i < count; ++i) {
     for (int j = 0; j < ins; ++j) {
@@ -182,12 +177,15 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   char *at = static_cast<char *>(workspace);
   for (int i = 0; i < count; ++i) {
     a.lin[i].t = reinterpret_cast<float *>(at);
-    at += inner_bytes(w[i], m);
+    at += wq::lora_workspace(w[i], m);
   }
   a.ids = ids;
   a.count = count;
   a.m = (int32_t)m;
-  return hip_status(wq::launch_lora(a, (hipStream_t)stream), who);
+  const wq::LoraPlan plan = wq::lora_plan(count, w, m);
+  a.splits = plan.splits;
+  a.chunk = plan.chunk;
+  return hip_status(wq::launch_lora(a, plan, (hipStream_t)stream), who);
 }
 
 size_t wq_sample_workspace(int64_t rows, int64_t vocab) {
