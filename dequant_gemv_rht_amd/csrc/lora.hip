@@ -28,9 +28,9 @@ namespace {
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kLoraThreads = 256;
-constexpr int kWaves = kLoraThreads / 64;
-constexpr int kBlockRows = 64;
+constexpr int kWaves = 4;
+constexpr int kLoraThreads = 64 * kWaves;
+static_assert(kWholeRows == kLoraThreads, "a thread looks at one id");
 
 __device__ __forceinline__ half8_t zero8() {
   half8_t z;
@@ -41,7 +41,8 @@ __device__ __forceinline__ half8_t zero8() {
 
 __device__ __forceinline__ uint64_t below(int n) { return n >= 64 ? ~0ull : (1ull << n) - 1; }
 
-// Runs f(id, rows in list) for the workgroup's groups; id -1: no adapter.
+// Runs f(id, rows in list) for the workgroup's groups, of at most 16 CT rows;
+// id -1: no adapter.
 template <bool WHOLE, int CT, typename F>
 __device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, int32_t *list, uint64_t *masks, F f) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
@@ -66,8 +67,8 @@ __device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, 
     __syncthreads();
     f(id, rows);
   } else {
-    const int64_t row = (int64_t)b * kBlockRows + lane;
-    const bool live = row < g.m;
+    const int64_t row = (int64_t)b * (16 * CT) + lane;
+    const bool live = lane < 16 * CT && row < g.m;
     const int32_t mine = live ? known(g.ids[row]) : -1;
     uint64_t left = __ballot(live);
     while (left) {
@@ -82,100 +83,132 @@ __device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, 
   }
 }
 
-// One wave's part of A x over 32-wide steps [u0, u1): RT x NC tiles
-template <int RT, int NC, int CT>
-__device__ __forceinline__ void inner_steps(const _Float16 *const (&ap)[RT], const _Float16 *const (&xp)[CT], int u0, int u1,
-                                            float4_t (&acc)[RT][CT]) {
-#pragma unroll 4
-  for (int u = u0; u < u1; ++u) {
-    half8_t a[RT], x[NC];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) a[r] = *reinterpret_cast<const half8_t *>(ap[r] + 32 * (int64_t)u);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) x[c] = *reinterpret_cast<const half8_t *>(xp[c] + 32 * (int64_t)u);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < NC; ++c) acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[r], x[c], acc[r][c], 0, 0, 0);
-  }
-}
+constexpr int kStage = 256;            // channels staged in LDS at once
+constexpr int kStageLd = kStage + 8;   // 16 rows of 16 bytes on different banks
 
+// t of RT x CT sixteens of ranks and rows over the workgroup's channels.
+// Rows come through LDS, 512 bytes of each at a time: loaded straight into
+// the matrix instructions' layout they would be fetched in pieces of 64.  The
+// next piece is on its way while this one is multiplied, two 32-wide steps a
+// wave; what the waves have is added at the end.
 template <bool WHOLE, int RT, int CT>
 __global__ __launch_bounds__(kLoraThreads) void lora_inner_kernel(LoraArgs g) {
-  __shared__ int32_t list[kBlockRows];
+  constexpr int kRanks = 16 * RT, kRows = 16 * CT, kSumLd = kRanks + 4;
+  __shared__ int32_t list[kRows];
   __shared__ uint64_t masks[kWaves];
-  __shared__ float sums[kWaves][16][RT * 16 + 4];
+  __shared__ union alignas(16) {
+    _Float16 rows[kRanks + kRows][kStageLd];
+    float sums[kWaves][16][kSumLd];
+  } lds;
   const int part = (int)blockIdx.z / g.count;
   const LoraDesc L = g.lin[blockIdx.z - part * g.count];
-  const int r0 = part * RT * 16;   // first rank
-  if (r0 >= L.rank) return;
+  const int r0 = part * kRanks, k0 = (int)blockIdx.y * g.steps * 32, k1 = min(L.k, k0 + g.steps * 32);
+  if (r0 >= L.rank || k0 >= k1) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
-  const int units = L.k / 32, slice = (int)blockIdx.y * kWaves + wave, slices = (int)gridDim.y * kWaves;
-  const int u0 = (int)((int64_t)units * slice / slices), u1 = (int)((int64_t)units * (slice + 1) / slices);
+  const int row = tid >> 5, at = 8 * (tid & 31);   // a thread's rows row + 8 i and its 8 channels
   for_groups<WHOLE, CT>(g, L.count, list, masks, [&](int32_t id, int rows) {
     if (id < 0) return;
-    const _Float16 *ap[RT], *xp[CT];
+    // ranks and rows past the last repeat it and are not stored; channels
+    // past the last are zeros
+    half8_t a[2 * RT], x[2 * CT];
+    const _Float16 *ap[2 * RT], *xp[2 * CT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int rank = min(r0 + 16 * r + c, L.rank - 1);   // ranks past the last are not stored
-      ap[r] = reinterpret_cast<const _Float16 *>(L.a) + ((int64_t)id * L.rank + rank) * L.k + 8 * q;
-    }
+    for (int i = 0; i < 2 * RT; ++i)
+      ap[i] = reinterpret_cast<const _Float16 *>(L.a) + ((int64_t)id * L.rank + min(r0 + row + 8 * i, L.rank - 1)) * L.k;
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-      xp[t] = reinterpret_cast<const _Float16 *>(L.x) + list[min(16 * t + c, rows - 1)] * L.ldx + 8 * q;
+    for (int i = 0; i < 2 * CT; ++i)
+      xp[i] = reinterpret_cast<const _Float16 *>(L.x) + list[min(row + 8 * i, rows - 1)] * L.ldx;
+    const auto load = [&](int k) {
+      const int from = min(k + at, k1 - 8);
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) a[i] = *reinterpret_cast<const half8_t *>(ap[i] + from);
+#pragma unroll
+      for (int i = 0; i < 2 * CT; ++i) x[i] = *reinterpret_cast<const half8_t *>(xp[i] + from);
+    };
+    const auto clear = [&](int k) {
+      const bool in = k + at < k1;
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) a[i] = in ? a[i] : zero8();
+#pragma unroll
+      for (int i = 0; i < 2 * CT; ++i) x[i] = in ? x[i] : zero8();
+    };
     float4_t acc[RT][CT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int t = 0; t < CT; ++t) acc[r][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    if (CT == 1 || rows <= 16)
-      inner_steps<RT, 1, CT>(ap, xp, u0, u1, acc);
-    else
-      inner_steps<RT, CT, CT>(ap, xp, u0, u1, acc);
+    load(k0);
+    for (int k = k0; k < k1; k += kStage) {
+      __syncthreads();   // the last piece is multiplied
+      if (k + kStage > k1) clear(k);
+#pragma unroll
+      for (int i = 0; i < 2 * RT; ++i) *reinterpret_cast<half8_t *>(&lds.rows[row + 8 * i][at]) = a[i];
+#pragma unroll
+      for (int i = 0; i < 2 * CT; ++i) *reinterpret_cast<half8_t *>(&lds.rows[kRanks + row + 8 * i][at]) = x[i];
+      __syncthreads();
+      if (k + kStage < k1) load(k + kStage);
+#pragma unroll
+      for (int s = 0; s < kStage / 32 / kWaves; ++s) {
+        const int from = 32 * (wave * (kStage / 32 / kWaves) + s) + 8 * q;
+        half8_t am[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) am[r] = *reinterpret_cast<const half8_t *>(&lds.rows[16 * r + c][from]);
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+          const half8_t xm = *reinterpret_cast<const half8_t *>(&lds.rows[kRanks + 16 * t + c][from]);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(am[r], xm, acc[r][t], 0, 0, 0);
+        }
+      }
+    }
     const float scale = L.scales ? L.scales[id] : 1.0f;
+    float *out = L.t + (int64_t)blockIdx.y * g.m * L.rank + r0;
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       if (16 * t >= rows) break;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) *reinterpret_cast<float4_t *>(&sums[wave][c][16 * r + 4 * q]) = acc[r][t];
       __syncthreads();
-      const int col = tid >> 4;
-      if (16 * t + col < rows) {
-        float *out = L.t + ((int64_t)blockIdx.y * g.m + list[16 * t + col]) * L.rank;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const int at = 16 * r + (tid & 15);
-          float sum = sums[0][col][at];
+      for (int r = 0; r < RT; ++r) *reinterpret_cast<float4_t *>(&lds.sums[wave][c][16 * r + 4 * q]) = acc[r][t];
+      __syncthreads();
+      for (int i = tid; i < 16 * kRanks; i += kLoraThreads) {
+        const int col = i / kRanks, rank = i % kRanks;
+        if (16 * t + col < rows && r0 + rank < L.rank) {
+          float sum = lds.sums[0][col][rank];
 #pragma unroll
-          for (int w = 1; w < kWaves; ++w) sum += sums[w][col][at];
-          if (r0 + at < L.rank) out[r0 + at] = sum * scale;
+          for (int w = 1; w < kWaves; ++w) sum += lds.sums[w][col][rank];
+          out[(int64_t)list[16 * t + col] * L.rank + rank] = sum * scale;
         }
       }
-      __syncthreads();
     }
   });
 }
 
-// 8 or 16 neighbours of a row at any alignment
-template <typename T, int N>
+// 16 neighbours of a row, at any alignment
+template <typename T>
 struct Run {
-  T v[N];
+  T v[16];
 };
 
 template <typename T>
-__device__ __forceinline__ void add_out(const LoraDesc &L, int32_t row, int n, const float (&add)[16]) {
-  const T *base = static_cast<const T *>(L.base) + row * L.ldb + n;
-  T *y = static_cast<T *>(L.y) + row * L.ldy + n;
-  if (n + 16 <= L.n) {
-    Run<T, 16> r;
-    __builtin_memcpy(&r, base, sizeof r);
+__device__ __forceinline__ Run<T> load_run(const T *row, int n, int end) {
+  Run<T> r;
+  if (n + 16 <= end) {
+    __builtin_memcpy(&r, row + n, sizeof r);
+  } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r.v[i] = (T)((float)r.v[i] + add[i]);
-    __builtin_memcpy(y, &r, sizeof r);
+    for (int i = 0; i < 16; ++i) r.v[i] = n + i < end ? row[n + i] : (T)0.0f;
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_run(T *row, int n, int end, const Run<T> &r) {
+  if (n + 16 <= end) {
+    __builtin_memcpy(row + n, &r, sizeof r);
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (n + i < L.n) y[i] = (T)((float)base[i] + add[i]);
+      if (n + i < end) row[n + i] = r.v[i];
   }
 }
 
@@ -189,150 +222,190 @@ __device__ __forceinline__ void copy_rows(const LoraDesc &L, const int32_t *list
   }
 }
 
-// KK: 32-wide steps over the ranks; PACK (ranks up to 16): both parts of t in one step
+// B's part of 64 outputs from n on: instruction j's output row r is output
+// n + 16 (r / 4) + 4 j + r % 4, so that a lane ends up with 16 neighbours.
+template <int KK, bool PACK>
+__device__ __forceinline__ void load_b(const LoraDesc &L, int32_t id, int n, half8_t (&b)[4][KK]) {
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int at = min(n + 16 * (c >> 2) + 4 * j + (c & 3), L.n - 1);
+    const _Float16 *bp = reinterpret_cast<const _Float16 *>(L.b) + ((int64_t)id * L.n + at) * L.rank;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
+      b[j][k] = rank < L.rank ? *reinterpret_cast<const half8_t *>(bp + rank) : zero8();
+    }
+  }
+}
+
+// The outputs of one group: T base's and y's type.  KK: 32-wide steps over
+// the ranks; PACK (ranks up to 16): both parts of t in one step.
+template <typename T, int KK, bool PACK, int CT>
+__device__ __forceinline__ void outer_group(const LoraArgs &g, const LoraDesc &L, const int32_t *list,
+                                            half8_t (*parts)[KK][PACK ? 1 : 2][64], int32_t (*powers)[16], int32_t id, int rows,
+                                            int n0, int n1) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+  int n = n0 + 64 * wave;
+  const T *base[CT];
+  T *y[CT];
+#pragma unroll
+  for (int t = 0; t < CT; ++t) {
+    const int32_t row = list[min(16 * t + c, rows - 1)];
+    base[t] = static_cast<const T *>(L.base) + row * L.ldb;
+    y[t] = static_cast<T *>(L.y) + row * L.ldy;
+  }
+  // B and base do not wait for t
+  half8_t b[4][KK];
+  Run<T> out[CT];
+  const auto load = [&](int at) {
+    load_b<KK, PACK>(L, id, at, b);
+#pragma unroll
+    for (int t = 0; t < CT; ++t)
+      if (16 * t < rows) out[t] = load_run(base[t], at + 16 * q, at + 16 * q < n1 ? L.n : 0);
+  };
+  if (n < n1) load(n);
+  // wave w makes the parts of the group's rows 16 w .. 16 w + 15
+  if (16 * wave < rows && wave < CT) {
+    const int32_t row = list[min(16 * wave + c, rows - 1)];
+    const int splits = (L.k / 32 + g.steps - 1) / g.steps;
+    float v[KK][8], most = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
+      const bool has = rank < L.rank;
+      const float *t = L.t + (int64_t)row * L.rank + (has ? rank : 0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+      for (int s0 = 0; s0 < splits; s0 += 4) {   // four splits asked for at once
+        float4_t lo[4], hi[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float4_t *at = reinterpret_cast<const float4_t *>(t + (int64_t)min(s0 + s, splits - 1) * g.m * L.rank);
+          lo[s] = at[0];
+          hi[s] = at[1];
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const bool adds = has && s0 + s < splits;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[k][e] += adds ? lo[s][e] : 0.0f;
+            v[k][4 + e] += adds ? hi[s][e] : 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[k][e]));
+    }
+    most = fmaxf(most, __shfl_xor(most, 16));
+    most = fmaxf(most, __shfl_xor(most, 32));
+    // the row's largest into [2^13, 2^14); infinities as they are
+    const int power = most > 0.0f && most <= 3.4028234e38f ? 14 - __builtin_amdgcn_frexp_expf(most) : 0;
+    if (q == 0) powers[wave][c] = -power;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      half8_t hi, lo;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = ldexpf(v[k][e], power);
+        hi[e] = (_Float16)x;
+        const float rest = x - (float)hi[e];
+        lo[e] = (_Float16)(rest - rest == 0.0f ? rest : 0.0f);
+      }
+      if (PACK) {
+        parts[wave][k][0][lane] = q < 2 ? hi : lo;
+      } else {
+        parts[wave][k][0][lane] = hi;
+        parts[wave][k][1][lane] = lo;
+      }
+    }
+  }
+  __syncthreads();
+  for (; n < n1;) {
+    const int mine = n + 16 * q, end = mine < n1 ? L.n : 0;
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+      if (16 * t >= rows) break;
+      float4_t acc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < KK; ++k)
+#pragma unroll
+        for (int p = 0; p < (PACK ? 1 : 2); ++p) {
+          const half8_t part = parts[t][k][p][lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j][k], part, acc[j], 0, 0, 0);
+        }
+      const int power = powers[t][c];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[t].v[4 * j + e] = (T)((float)out[t].v[4 * j + e] + ldexpf(acc[j][e], power));
+      if (16 * t + c < rows) store_run(y[t], mine, end, out[t]);
+    }
+    n += 64 * kWaves;
+    if (n < n1) load(n);
+  }
+}
+
 template <bool WHOLE, int KK, bool PACK, int CT>
 __global__ __launch_bounds__(kLoraThreads) void lora_outer_kernel(LoraArgs g) {
-  __shared__ int32_t list[kBlockRows];
+  __shared__ int32_t list[16 * CT];
   __shared__ uint64_t masks[kWaves];
-  __shared__ half8_t parts[CT][KK][PACK ? 1 : 2][64];
+  __shared__ alignas(16) half8_t parts[CT][KK][PACK ? 1 : 2][64];
   __shared__ int32_t powers[CT][16];
   const LoraDesc L = g.lin[blockIdx.z];
   const int n0 = (int)blockIdx.y * g.chunk;
   if (n0 >= L.n) return;
   const int n1 = min(n0 + g.chunk, L.n);
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   for_groups<WHOLE, CT>(g, L.count, list, masks, [&](int32_t id, int rows) {
     if (id < 0) {
       if (L.f32)
         copy_rows<float>(L, list, rows, n0, n1);
       else
         copy_rows<_Float16>(L, list, rows, n0, n1);
-      return;
+    } else if (L.f32) {
+      outer_group<float, KK, PACK, CT>(g, L, list, parts, powers, id, rows, n0, n1);
+    } else {
+      outer_group<_Float16, KK, PACK, CT>(g, L, list, parts, powers, id, rows, n0, n1);
     }
-    // wave w makes the parts of the group's rows 16 w .. 16 w + 15
-    if (16 * wave < rows && wave < CT) {
-      const int32_t row = list[min(16 * wave + c, rows - 1)];
-      float v[KK][8], most = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KK; ++k) {
-        const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
-        if (rank < L.rank)
-          for (int s = 0; s < g.splits; ++s) {
-            const float4_t *t = reinterpret_cast<const float4_t *>(L.t + ((int64_t)s * g.m + row) * L.rank + rank);
-            const float4_t lo = t[0], hi = t[1];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[k][e] += lo[e];
-              v[k][4 + e] += hi[e];
-            }
-          }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[k][e]));
-      }
-      most = fmaxf(most, __shfl_xor(most, 16));
-      most = fmaxf(most, __shfl_xor(most, 32));
-      // the row's largest into [2^13, 2^14); infinities as they are
-      const int power = most > 0.0f && most <= 3.4028234e38f ? 14 - __builtin_amdgcn_frexp_expf(most) : 0;
-      if (q == 0) powers[wave][c] = -power;
-#pragma unroll
-      for (int k = 0; k < KK; ++k) {
-        half8_t hi, lo;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x = ldexpf(v[k][e], power);
-          hi[e] = (_Float16)x;
-          const float rest = x - (float)hi[e];
-          lo[e] = (_Float16)(rest - rest == 0.0f ? rest : 0.0f);
-        }
-        if (PACK) {
-          parts[wave][k][0][lane] = q < 2 ? hi : lo;
-        } else {
-          parts[wave][k][0][lane] = hi;
-          parts[wave][k][1][lane] = lo;
-        }
-      }
-    }
-    __syncthreads();
-    for (int n = n0 + 64 * wave; n < n1; n += 64 * kWaves) {
-      // instruction j's output row r is output n + 16 (r / 4) + 4 j + r % 4,
-      // so that a lane ends up with 16 neighbours
-      half8_t b[4][KK];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int at = min(n + 16 * (c >> 2) + 4 * j + (c & 3), L.n - 1);
-        const _Float16 *bp = reinterpret_cast<const _Float16 *>(L.b) + ((int64_t)id * L.n + at) * L.rank;
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-          const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
-          b[j][k] = rank < L.rank ? *reinterpret_cast<const half8_t *>(bp + rank) : zero8();
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < CT; ++t) {
-        if (16 * t >= rows) break;
-        float4_t acc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < KK; ++k)
-#pragma unroll
-          for (int p = 0; p < (PACK ? 1 : 2); ++p) {
-            const half8_t part = parts[t][k][p][lane];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j][k], part, acc[j], 0, 0, 0);
-          }
-        if (16 * t + c < rows && n + 16 * q < n1) {
-          const int power = powers[t][c];
-          float add[16];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) add[4 * j + e] = ldexpf(acc[j][e], power);
-          if (L.f32)
-            add_out<float>(L, list[16 * t + c], n + 16 * q, add);
-          else
-            add_out<_Float16>(L, list[16 * t + c], n + 16 * q, add);
-        }
-      }
-    }
-    if (!WHOLE) __syncthreads();   // the parts are read
   });
 }
 
-template <bool WHOLE, int CT>
+// CI, CO: sixteens of rows of a group in the inner and the outer kernel
+template <bool WHOLE, int CI, int CO>
 hipError_t launch(const LoraArgs &a, const LoraPlan &p, hipStream_t s) {
-  const dim3 threads(kLoraThreads);
   const auto inner = [&](auto kernel, int tiles) {
     const unsigned parts = (unsigned)((p.rank + 16 * tiles - 1) / (16 * tiles));
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.tiles, (unsigned)p.splits, parts * (unsigned)a.count), threads, 0, s, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.inner_tiles, (unsigned)p.splits, parts * (unsigned)a.count), dim3(kLoraThreads),
+                       0, s, a);
   };
   if (p.rank <= 16)
-    inner(lora_inner_kernel<WHOLE, 1, CT>, 1);
+    inner(lora_inner_kernel<WHOLE, 1, CI>, 1);
   else if (p.rank <= 32)
-    inner(lora_inner_kernel<WHOLE, 2, CT>, 2);
+    inner(lora_inner_kernel<WHOLE, 2, CI>, 2);
   else
-    inner(lora_inner_kernel<WHOLE, 4, CT>, 4);
+    inner(lora_inner_kernel<WHOLE, 4, CI>, 4);
   const auto outer = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.tiles, (unsigned)p.chunks, (unsigned)a.count), threads, 0, s, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.outer_tiles, (unsigned)p.chunks, (unsigned)a.count), dim3(kLoraThreads), 0, s, a);
   };
   if (p.rank <= 16)
-    outer(lora_outer_kernel<WHOLE, 1, true, CT>);
+    outer(lora_outer_kernel<WHOLE, 1, true, CO>);
   else if (p.rank <= 32)
-    outer(lora_outer_kernel<WHOLE, 1, false, CT>);
+    outer(lora_outer_kernel<WHOLE, 1, false, CO>);
   else if (p.rank <= 64)
-    outer(lora_outer_kernel<WHOLE, 2, false, CT>);
+    outer(lora_outer_kernel<WHOLE, 2, false, CO>);
   else
-    outer(lora_outer_kernel<WHOLE, 4, false, CT>);
+    outer(lora_outer_kernel<WHOLE, 4, false, CO>);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_lora(const LoraArgs &a, const LoraPlan &p, hipStream_t s) {
-  if (!p.whole) return launch<false, 4>(a, p, s);
-  return p.narrow ? launch<true, 1>(a, p, s) : launch<true, 4>(a, p, s);
+  return p.whole ? launch<true, 1, 1>(a, p, s) : launch<false, 2, 4>(a, p, s);
 }
 
 }  // namespace wq

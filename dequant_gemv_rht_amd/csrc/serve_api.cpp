@@ -183,7 +183,7 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   a.count = count;
   a.m = (int32_t)m;
   const wq::LoraPlan plan = wq::lora_plan(count, w, m);
-  a.splits = plan.splits;
+  a.steps = plan.steps;
   a.chunk = plan.chunk;
   return hip_status(wq::launch_lora(a, plan, (hipStream_t)stream), who);
 }

@@ -6,15 +6,21 @@ namespace wq {
 
 namespace {
 
-constexpr int64_t kInnerWork = 512;     // workgroups that the first kernel's K is split for
-constexpr int64_t kOuterWork = 1024;    // and the second's outputs
+constexpr int64_t kWork = 2048;   // workgroups that K and the outputs are cut for
 
-// K splits of a call of `tiles` groups at least
-int32_t splits_for(int64_t tiles, int64_t k) {
-  int64_t s = (kInnerWork + tiles - 1) / tiles;
-  if (s > kLoraSplits) s = kLoraSplits;
-  if (s > k / 128) s = k / 128;
-  return (int32_t)(s < 1 ? 1 : s);
+// the smallest multiple of `unit` in which `pieces`, cut, make at most kWork
+// workgroups for each `tiles`, and at most `most` of the longest piece
+int64_t cut(int32_t count, const wq_adapters *w, int64_t wq_adapters::*length, int64_t tiles, int64_t unit, int64_t most) {
+  int64_t sum = 0, longest = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    sum += w[i].*length;
+    longest = w[i].*length > longest ? w[i].*length : longest;
+  }
+  int64_t piece = (sum * tiles + kWork - 1) / kWork;
+  if (piece > longest) piece = longest;
+  const int64_t least = (longest + most - 1) / most;
+  if (piece < least) piece = least;
+  return (piece + unit - 1) / unit * unit;
 }
 
 }  // namespace
@@ -22,8 +28,8 @@ int32_t splits_for(int64_t tiles, int64_t k) {
 LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
   LoraPlan p;
   p.whole = m <= kWholeRows;
-  p.narrow = m <= 16;
-  p.tiles = p.whole ? m : (m + 63) / 64;
+  p.inner_tiles = p.whole ? m : (m + 31) / 32;
+  p.outer_tiles = p.whole ? m : (m + 63) / 64;
   int64_t n = 0, k = 0;
   p.rank = 0;
   for (int32_t i = 0; i < count; ++i) {
@@ -31,20 +37,17 @@ LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
     k = w[i].k > k ? w[i].k : k;
     p.rank = w[i].rank > p.rank ? w[i].rank : p.rank;
   }
-  const int64_t groups = (p.whole ? (m + 15) / 16 : p.tiles) * count;
-  p.splits = splits_for(groups, k);
-  int64_t chunks = (kOuterWork + groups - 1) / groups;
-  if (chunks > (n + 255) / 256) chunks = (n + 255) / 256;
-  p.chunk = (int32_t)(((n + chunks - 1) / chunks + 255) / 256 * 256);
+  const int64_t piece = p.whole ? cut(count, w, &wq_adapters::k, m, 128, kLoraSplits) : k;
+  p.steps = (int32_t)(piece / 32);
+  p.splits = (int32_t)((k + piece - 1) / piece);
+  p.chunk = (int32_t)cut(count, w, &wq_adapters::n, p.outer_tiles, 256, INT32_MAX);
   p.chunks = (n + p.chunk - 1) / p.chunk;
   return p;
 }
 
 size_t lora_workspace(const wq_adapters &w, int64_t m) {
-  // a bound of splits * m that grows with m: ceil(work / tiles) m with tiles
-  // of at least m / 64 rows
-  const int64_t most = kLoraSplits * m, filled = m + 64 * kInnerWork;
-  const size_t bytes = (size_t)(most < filled ? most : filled) * (size_t)w.rank * sizeof(float);
+  const int64_t rows = (m <= kWholeRows ? m : kWholeRows) * kLoraSplits;
+  const size_t bytes = (size_t)(rows > m ? rows : m) * (size_t)w.rank * sizeof(float);
   return (bytes + 255) / 256 * 256;
 }
 

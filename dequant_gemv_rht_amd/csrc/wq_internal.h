@@ -234,7 +234,7 @@ struct LoraDesc {
   const uint16_t *x;
   const void *base;
   void *y;
-  float *t;                     // scale A x: [splits][m][rank]
+  float *t;                     // scale A x: [splits][m][rank], splits = k / 32 / steps rounded up
   int64_t ldx, ldb, ldy;
   int32_t n, k, count, rank, f32;
 };
@@ -242,14 +242,14 @@ struct LoraArgs {
   LoraDesc lin[kMaxBatch];
   const int32_t *ids;
   int32_t count, m;
-  int32_t splits, chunk;        // of K (first kernel); outputs of a workgroup, a multiple of 256 (second)
+  int32_t steps, chunk;         // 32s of K of a workgroup (first kernel); outputs, a multiple of 256 (second)
 };
 constexpr int kWholeRows = 256; // rows whose groups are gathered from all of the call
 constexpr int kLoraSplits = 8;  // at most
 struct LoraPlan {
-  int64_t tiles, chunks;        // workgroups: a row each, or 64 in succession; of the outputs
-  int32_t splits, chunk, rank;  // the largest rank
-  bool whole, narrow;           // narrow: groups of 16 rows
+  bool whole;                   // a workgroup for each row, or for rows in succession
+  int64_t inner_tiles, outer_tiles, chunks;
+  int32_t splits, steps, chunk, rank;   // the largest rank
 };
 LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m);
 size_t lora_workspace(const wq_adapters &w, int64_t m);   // of one linear
