@@ -194,7 +194,7 @@ size_t wq_sample_workspace(int64_t rows, int64_t vocab) {
     set_error(WQ_E_ARG, "wq_sample_workspace: rows=%lld, vocab=%lld (up to 2^20 each)", (long long)rows, (long long)vocab);
     return (size_t)-1;
   }
-  return 0;
+  return wq::sample_workspace(rows, vocab, nullptr, nullptr);
 }
 
 wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vocab, int64_t ldl, const float *u,
@@ -213,7 +213,8 @@ wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vo
   if (!aligned(logits, 16) || !aligned(u, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
       !aligned(min_p, 4) || !aligned(ids, 4) || !aligned(logprobs, 4))
     return set_error(WQ_E_ALIGN, "%s: logits 16-byte, the other arrays 4-byte aligned", who);
-  const size_t need = wq_sample_workspace(rows, vocab);
+  size_t sums_at, counts_at;
+  const size_t need = wq::sample_workspace(rows, vocab, &sums_at, &counts_at);
   if (workspace_bytes < need || (need && !workspace))
     return set_error(WQ_E_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need, workspace_bytes);
   if (need && !aligned(workspace, 16)) return set_error(WQ_E_ALIGN, "%s: workspace must be 16-byte aligned", who);
@@ -242,9 +243,13 @@ wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vo
   a.rows = (int32_t)rows;
   a.vocab = (int32_t)vocab;
   a.f32 = dtype == WQ_F32;
-  // the sum of vocab weights of at most 1 stays below 2^62
-  a.unit = 62;
-  while (a.unit > 62 - 18 || ((int64_t)1 << (62 - a.unit)) < vocab) --a.unit;
+  a.parts = (int32_t)((vocab + wq::kSamplePart - 1) / wq::kSamplePart);
+  a.heads = static_cast<wq::SamplePart *>(workspace);
+  a.sums = reinterpret_cast<uint64_t *>(static_cast<char *>(workspace) + sums_at);
+  a.counts = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + counts_at);
+  // the sum of vocab weights, each below 2, stays below 2^63
+  a.unit = 44;
+  while (((int64_t)1 << (62 - a.unit)) < vocab) --a.unit;
   return hip_status(wq::launch_sample(a, (hipStream_t)stream), who);
 }
 

@@ -51,4 +51,13 @@ size_t lora_workspace(const wq_adapters &w, int64_t m) {
   return (bytes + 255) / 256 * 256;
 }
 
+// heads, then bins' sums, then their counts
+size_t sample_workspace(int64_t rows, int64_t vocab, size_t *sums_at, size_t *counts_at) {
+  const size_t parts = (size_t)rows * (size_t)((vocab + kSamplePart - 1) / kSamplePart);
+  const size_t heads = (parts * sizeof(SamplePart) + 255) / 256 * 256, sums = parts * kSampleBins * sizeof(uint64_t);
+  if (sums_at) *sums_at = heads;
+  if (counts_at) *counts_at = heads + sums;
+  return heads + sums + parts * kSampleBins * sizeof(uint32_t);
+}
+
 }  // namespace wq

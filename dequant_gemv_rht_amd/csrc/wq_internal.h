@@ -255,6 +255,16 @@ LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m);
 size_t lora_workspace(const wq_adapters &w, int64_t m);   // of one linear
 hipError_t launch_lora(const LoraArgs &a, const LoraPlan &p, hipStream_t s);
 
+constexpr int kSamplePart = 8192;   // logits of a row that a workgroup takes at once
+constexpr int kSampleBins = 256;
+constexpr int64_t kSampleGroups = 2048;
+constexpr int32_t kFarPart = INT32_MIN;
+struct SamplePart {
+  uint64_t best;                // largest key, complement of its first index
+  uint64_t sum;                 // of weights, under `power`
+  int32_t power;                // kFarPart: weights not summed
+  uint32_t finite;
+};
 struct SampleArgs {
   const void *logits;
   int64_t ldl;
@@ -262,9 +272,13 @@ struct SampleArgs {
   const int32_t *top_k;
   int32_t *ids;
   float *logprobs;
-  int32_t rows, vocab, f32;
+  int32_t rows, vocab, f32, parts;
   int32_t unit;                 // weights are counted in 2^-unit
+  SamplePart *heads;            // [rows][parts]
+  uint64_t *sums;               // [rows][parts][kSampleBins]
+  uint32_t *counts;
 };
+size_t sample_workspace(int64_t rows, int64_t vocab, size_t *sums_at, size_t *counts_at);
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s);
 
 }  // namespace wq
