@@ -8,15 +8,20 @@
 //
 // Two launches.  The first reads every logit once: a workgroup takes a part
 // of a row, kPart logits in registers, and leaves its largest, its sum and,
-// for rows with top-k, top-p or min-p, counts and sums in kBins bins of
-// equal width (an eighth of a power of two, from its largest down).  Bins of
-// all parts line up, so the second launch, a workgroup for each row, finds in
-// which bin a cut lies, fetches that bin's logits alone (from the parts that
-// have any), finds the cut among them bit by bit, and with it every part's
+// for rows with top-k, top-p or min-p, running counts and sums over kBins
+// bins of equal width (an eighth of a power of two, from its largest down).
+// Bins of all parts line up, so the second launch, a workgroup for each row,
+// finds in which bin a cut lies, fetches that bin's logits alone (from the
+// parts that have any), finds the cut among them, and with it every part's
 // sum of what is kept; the part in which the sum passes u times all of it is
 // read again, token by token.  Rows for which that does not do (a cut below
-// the bins, more logits in its bin than fit in LDS, logits or temperatures
-// beyond 2^13 powers of two) are searched in as many passes as it takes.
+// the bins, more logits in its bin than fit in LDS, logits beyond 2^13 powers
+// of two) are searched in as many passes as it takes.
+//
+// The second launch runs once through its code, most of which then comes from
+// the L2 line by line: loops there stay rolled, each piece of work has one
+// place, and what a wave can find out alone every wave does, without waiting
+// for the others.
 #include "wq_internal.h"
 
 namespace wq {
@@ -27,7 +32,7 @@ namespace {
 constexpr uint32_t kNoKey = 0x007FFFFFu;     // of -infinity
 constexpr int kBins = kSampleBins;
 constexpr int kPart = kSamplePart;
-constexpr int kPartThreads = 256;
+constexpr int kPartThreads = 512;
 constexpr int kEach = kPart / kPartThreads;  // logits of a thread
 constexpr int kMaxParts = (1 << 20) / kPart;
 constexpr int kTable = 1024;
@@ -95,17 +100,16 @@ struct Settings {
 };
 
 __device__ __forceinline__ Settings settings(const SampleArgs &a, int64_t r) {
+  // every array is there (one that the caller left out stands for another), so all are asked for at once
+  const float heat = a.temperature[r], u = a.u[r], m = a.min_p[r], p = a.top_p[r];
+  const int k = a.top_k[r];
   Settings s;
-  s.heat = a.temperature ? a.temperature[r] : 1.0f;
+  s.heat = a.given & kGivenHeat ? heat : 1.0f;
   s.greedy = !(s.heat > 0.0f);
-  const float u = a.u[r];
   s.u = u > 0.0f ? (u < 1.0f ? (double)u : 1.0) : 0.0;
-  const float m = a.min_p ? a.min_p[r] : 0.0f;
-  s.at_least = m > 0.0f ? (m < 1.0f ? (double)m : 1.0) : 0.0;
-  const float p = a.top_p ? a.top_p[r] : 1.0f;
-  s.top_p = p < 1.0f ? (p > 0.0f ? p : 0.0f) : 1.0f;
-  s.top_k = a.top_k ? a.top_k[r] : 0;
-  if (s.top_k <= 0 || s.top_k > a.vocab) s.top_k = a.vocab;
+  s.at_least = a.given & kGivenMinP && m > 0.0f ? (m < 1.0f ? (double)m : 1.0) : 0.0;
+  s.top_p = a.given & kGivenTopP && p < 1.0f ? (p > 0.0f ? p : 0.0f) : 1.0f;
+  s.top_k = a.given & kGivenTopK && k > 0 && k < a.vocab ? k : a.vocab;
   s.cuts = s.top_k < a.vocab || s.top_p < 1.0f || s.at_least > 0.0;
   return s;
 }
@@ -178,6 +182,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
   __shared__ unsigned long long sums[kBins];
   __shared__ uint32_t counts[kBins];
   __shared__ uint64_t tmp[kPartThreads / 64];
+  __shared__ uint32_t tmp_counts[kBins / 64];
   const int tid = threadIdx.x;
   for (int j = tid; j < kTable; j += kPartThreads) table[j] = table_entry(j);
   const int items = a.rows * a.parts;
@@ -201,10 +206,9 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
       }
     }
     const Settings s = settings(a, r);
-    if (s.cuts) {
+    if (s.cuts && tid < kBins) {
       sums[tid] = 0;
       counts[tid] = 0;
-      static_assert(kBins == kPartThreads, "a thread a bin");
     }
     float top = -INFINITY;
     int where = 0, finite = 0;
@@ -220,7 +224,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
     SamplePart head;
     head.best = best;
     head.sum = 0;
-    head.power = 0;
+    head.power = kFarPart;   // no bins
     head.finite = 0;
     if (!s.greedy && (uint32_t)(best >> 32) > kNoKey) {
       Scale sc;
@@ -231,25 +235,56 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
       sc.power = floor(most);
       uint64_t sum = 0;
       if (near) {
+        // eight at a time: a table entry of one waits behind the sums of none
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const Split p = split(v[i], sc);
-          const uint64_t w = counted(p, sc, table);
-          sum += w;
-          const int bin = bin_of(p);
-          if (s.cuts && bin < kBins) {
-            atomicAdd(&sums[bin], (unsigned long long)w);
-            atomicAdd(&counts[bin], 1u);
-          }
+        for (int i = 0; i < kEach; i += 8) {
+          Split p[8];
+          uint64_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = split(v[i + e], sc);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = counted(p[e], sc, table);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sum += w[e];
+          if (!s.cuts) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (bin_of(p[e]) < kBins) {
+              atomicAdd(&sums[bin_of(p[e])], (unsigned long long)w[e]);
+              if (s.top_k < a.vocab) atomicAdd(&counts[bin_of(p[e])], 1u);
+            }
         }
         head.power = (int32_t)sc.power;
       }
       head.sum = block_reduce<kPartThreads>(sum, tmp, Sum());
       head.finite = (uint32_t)block_reduce<kPartThreads>((uint64_t)finite, tmp, Sum());
-      if (!near) head.power = kFarPart;
-      if (s.cuts) {
-        a.sums[(int64_t)item * kBins + tid] = sums[tid];
-        a.counts[(int64_t)item * kBins + tid] = counts[tid];
+      if (near && s.cuts) {
+        // sums up to and with each bin
+        uint64_t up = tid < kBins ? sums[tid] : 0;
+        uint32_t many = tid < kBins ? counts[tid] : 0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const uint64_t o = __shfl_up(up, d);
+          const uint32_t c = __shfl_up(many, d);
+          if ((tid & 63) >= d) {
+            up += o;
+            many += c;
+          }
+        }
+        __syncthreads();
+        if ((tid & 63) == 63 && tid < kBins) {
+          tmp[tid >> 6] = up;
+          tmp_counts[tid >> 6] = many;
+        }
+        __syncthreads();
+        if (tid < kBins) {
+          for (int w = 0; w < tid >> 6; ++w) {
+            up += tmp[w];
+            many += tmp_counts[w];
+          }
+          a.sums[(int64_t)item * kBins + tid] = up;
+          a.counts[(int64_t)item * kBins + tid] = many;
+        }
       }
     }
     if (tid == 0) a.heads[item] = head;
@@ -259,7 +294,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
 
 // ---------------------------------------------------------------- rows
 
-constexpr int kRowThreads = 1024;
+constexpr int kRowThreads = 512;
 constexpr int kList = 8192;                  // logits of a cut's bin, at most
 
 // the sum of v over the threads before this one
@@ -285,16 +320,15 @@ constexpr int kTurns = (1 << 20) / kTurn;
 struct Shared {
   double table[kTable];
   uint64_t tmp[kRowThreads / 64];
-  unsigned long long bins[kBins];            // the row's
-  uint32_t counts[kBins];
-  unsigned long long digits[256];            // of a search in the list
+  uint64_t sums[kBins], counts[kBins];       // the row's, up to and with each bin
+  unsigned long long digits[256];            // of a search in a long list
   unsigned long long kept[kMaxParts];        // of each part
-  SamplePart heads[kMaxParts];
   uint64_t above;
   int32_t found;
   uint32_t list_size;
   union {
     struct {
+      uint64_t weights[kList];
       uint32_t keys[kList], places[kList];
     } list;
     struct {
@@ -352,14 +386,21 @@ __device__ uint32_t search_row(const void *row, int n, const Far &s, uint32_t fl
       if (add) atomicAdd(&sh.slow.bins[(key >> next) & ((1u << bits) - 1)], (unsigned long long)add);
     });
     __syncthreads();
-    // from the highest down, two bins a thread
-    const int d = (1 << bits) - 1 - 2 * (int)threadIdx.x;
-    const uint64_t one = d >= 0 ? sh.slow.bins[d] : 0, two = d > 0 ? sh.slow.bins[d - 1] : 0;
-    const uint64_t before = above + block_before(one + two, sh.tmp);
-    if (d >= 0 && before < want && before + one + two >= want) {
-      sh.found = before + one >= want ? d : d - 1;
-      sh.above = before + one >= want ? before : before + one;
-    }
+    // from the highest down, four bins a thread
+    const int d = (1 << bits) - 1 - 4 * (int)threadIdx.x;
+    uint64_t here = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) here += d >= e ? sh.slow.bins[d - e] : 0;
+    uint64_t before = above + block_before(here, sh.tmp);
+    if (before < want && before + here >= want)
+      for (int e = 0; e < 4 && d >= e; ++e) {
+        const uint64_t one = sh.slow.bins[d - e];
+        if (before < want && before + one >= want) {
+          sh.found = d - e;
+          sh.above = before;
+        }
+        before += one;
+      }
     __syncthreads();
     prefix |= (uint32_t)sh.found << next;
     above = sh.above;
@@ -370,7 +411,7 @@ __device__ uint32_t search_row(const void *row, int n, const Far &s, uint32_t fl
 }
 
 template <bool F32>
-__device__ void sample_passes(const SampleArgs &a, int64_t r, const void *row, uint32_t top, const Settings &set, Shared &sh) {
+__device__ __forceinline__ void sample_passes(const SampleArgs &a, int64_t r, const void *row, uint32_t top, const Settings &set, Shared &sh) {
   const int tid = threadIdx.x, n = a.vocab;
   Far s;
   s.top = top;
@@ -490,94 +531,60 @@ __device__ void sample_passes(const SampleArgs &a, int64_t r, const void *row, u
 
 // ---- by the parts' bins
 
-// The value at which the sum over falling values, of 1 or of `add`, of the
-// list's entries with take(i) first reaches `want` (> 0), and the sum above
-// it; if it never does, the lowest.  Eight bits at a time, from the highest
-// that differs.
-template <typename Take, typename Value, typename Add>
-__device__ uint32_t search_list(int size, uint64_t want, uint64_t &above, Shared &sh, Take take, Value value, Add add) {
-  const int tid = threadIdx.x;
-  uint32_t low = 0xFFFFFFFFu, high = 0;
-  for (int i = tid; i < size; i += kRowThreads)
-    if (take(i)) {
-      const uint32_t v = value(i);
-      low = v < low ? v : low;
-      high = v > high ? v : high;
-    }
-  const uint64_t both = block_reduce<kRowThreads>((uint64_t)(~low) , sh.tmp, Larger());
-  const uint64_t top = block_reduce<kRowThreads>((uint64_t)high, sh.tmp, Larger());
-  low = ~(uint32_t)both;
-  high = (uint32_t)top;
-  above = 0;
-  if (low >= high) return low;
-  int shift = 32 - __clz((int)(low ^ high));   // bits from here up are alike
-  uint32_t prefix = shift < 32 ? high >> shift << shift : 0;
-  while (shift > 0) {
-    const int bits = shift < 8 ? shift : 8, next = shift - bits;
-    if (tid < 256) sh.digits[tid] = 0;
-    if (tid == 0) sh.found = -1;
-    __syncthreads();
-    for (int i = tid; i < size; i += kRowThreads)
-      if (take(i)) {
-        const uint32_t v = value(i);
-        if (shift == 32 || v >> shift == prefix >> shift)
-          atomicAdd(&sh.digits[(v >> next) & ((1u << bits) - 1)], (unsigned long long)add(i));
-      }
-    __syncthreads();
-    const int d = (1 << bits) - 1 - tid;
-    const uint64_t here = d >= 0 ? sh.digits[d] : 0;
-    const uint64_t before = above + block_before(here, sh.tmp);
-    if (d >= 0 && before < want && before + here >= want) {
-      sh.found = d;
-      sh.above = before;
-    }
-    __syncthreads();
-    if (sh.found < 0) return low;   // (above is that of the last digits)
-    prefix |= (uint32_t)sh.found << next;
-    above = sh.above;
-    shift = next;
-    __syncthreads();
-  }
-  return prefix;
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll 1
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
 }
 
-// The first of kBins bins in which the sum reaches `want`, and the sum before it; -1: none
 template <typename T>
-__device__ int find_bin(const T *bins, int end, uint64_t want, uint64_t &above, Shared &sh) {
-  const int tid = threadIdx.x;
-  if (tid == 0) sh.found = -1;
-  const uint64_t here = tid < end ? bins[tid] : 0;
-  const uint64_t before = block_before(here, sh.tmp);
-  if (tid < end && before < want && before + here >= want) {
-    sh.found = tid;
-    sh.above = before;
+__device__ __forceinline__ T wave_max(T v) {
+#pragma unroll 1
+  for (int d = 32; d; d >>= 1) {
+    const T o = __shfl_xor(v, d);
+    v = o > v ? o : v;
   }
-  __syncthreads();
-  const int found = sh.found;
-  above = sh.above;
-  __syncthreads();
-  return found;
+  return v;
 }
+
+// the sum of v over the lanes up to this one
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+
+// In turn: what top-k leaves, what top-p leaves of that, what min-p leaves of
+// that, and which of equal logits at the cut.
+enum Stage { kTopK, kTopP, kMinP, kPlace };
 
 template <bool F32>
 __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) {
   extern __shared__ char smem[];
   Shared &sh = *reinterpret_cast<Shared *>(smem);
   const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x, n = a.vocab, parts = a.parts;
+  const int tid = threadIdx.x, lane = tid & 63, n = a.vocab, parts = a.parts;
   const void *row = F32 ? (const void *)(static_cast<const float *>(a.logits) + r * a.ldl)
                         : (const void *)(static_cast<const uint16_t *>(a.logits) + r * a.ldl);
-  const Settings set = settings(a, r);
   const uint64_t *part_sums = a.sums + r * parts * kBins;
   const uint32_t *part_counts = a.counts + r * parts * kBins;
-
-  SamplePart head;
-  head.best = 0;
-  if (tid < parts) {
-    head = a.heads[r * parts + tid];
-    sh.heads[tid] = head;
-  }
-  const uint64_t best = block_reduce<kRowThreads>(head.best, sh.tmp, Larger());
+  // every wave: parts lane and lane + 64
+  static_assert(kMaxParts <= 128, "two parts a lane");
+  SamplePart head[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) head[h] = a.heads[r * parts + min(lane + 64 * h, parts - 1)];
+  const Settings set = settings(a, r);
+  const uint64_t best = wave_max(head[0].best > head[1].best ? head[0].best : head[1].best);
   const uint32_t top = (uint32_t)(best >> 32);
   if (top <= kNoKey || set.greedy) {
     if (tid == 0) {
@@ -586,230 +593,410 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     }
     return;
   }
+#pragma unroll 1
+  for (int j = tid; j < kTable; j += kRowThreads) sh.table[j] = table_entry(j);
   Scale sc;
   sc.per = 1.4426950408889634074 / (double)set.heat;
   sc.unit = a.unit;
   const double most = (double)value_of(top) * sc.per;
-  if (!(fabs(most) < kFar)) return sample_passes<F32>(a, r, row, top, set, sh);
   sc.power = floor(most);
-  const int power = (int)sc.power;
-  for (int j = tid; j < kTable; j += kRowThreads) sh.table[j] = table_entry(j);
-  // how far a part's powers are below the row's (64: its weights are nothing)
-  const auto behind = [&](int p) {
-    const int32_t own = sh.heads[p].power;
-    return own == kFarPart || power - own > 63 ? 64 : power - own;
-  };
-  const auto shifted = [](uint64_t v, int by) { return by < 64 ? v >> by : 0; };
-  const auto weight_of = [&](uint32_t key) { return key > kNoKey ? counted(split(value_of(key), sc), sc, sh.table) : 0; };
+  // as the first launch counted it: borders of equal weights are exact
+  const auto weight_of = [&](float l) { return counted(split(l, sc), sc, sh.table); };
+  bool passes = !(fabs(most) < kFar);
 
   // what is kept: keys above `cut`, and of those at it the ones whose index's
-  // complement is `last` or more; all of bins before `bin` and, in the list,
-  // the logits of that bin
+  // complement is `last` or more; all of the bins before `bin` and, in the
+  // list, the logits of that bin
   uint32_t cut = 0, last = 0;
-  uint64_t ties = ~0ull;
-  int bin = kBins;
-  uint64_t all = 0;   // sum of the weights kept
-  uint64_t finite = 0;
-  for (int p = 0; p < parts; ++p) {
-    finite += sh.heads[p].finite;
-    all += shifted(sh.heads[p].sum, behind(p));
-  }
-  int size = 0;       // of the list
-  if (set.cuts) {
-    if (tid < kBins) {
-      sh.bins[tid] = 0;
-      sh.counts[tid] = 0;
-    }
-    __syncthreads();
-    for (int i = tid; i < parts * kBins; i += kRowThreads) {
-      const int p = i / kBins, by = behind(p), to = i % kBins + 8 * by;
-      const uint32_t c = part_counts[i];
-      if (by < 64 && to < kBins && c) {
-        atomicAdd(&sh.bins[to], (unsigned long long)shifted(part_sums[i], by));
-        atomicAdd(&sh.counts[to], c);
-      }
-    }
-    __syncthreads();
-    // the logits of a bin into the list, from the parts that have some
-    const auto collect = [&](int which) {
-      if (which == bin) return true;
-      if (sh.counts[which] > (uint32_t)kList) return false;
-      __syncthreads();
-      if (tid == 0) sh.list_size = 0;
-      __syncthreads();
-      for (int p = 0; p < parts; ++p) {
-        const int by = behind(p), own = which - 8 * by;
-        if (by >= 64 || own < 0 || !part_counts[p * kBins + own]) continue;
-        Scale ps = sc;
-        ps.power = sh.heads[p].power;
-        const int from = p * kPart, to = min(n, from + kPart), first = from + 8 * tid;
-        float v[8];
-        if (first + 8 <= to) {
-          logits<F32, 8>(row, first, v);
-        } else {
-          for (int e = 0; e < 8; ++e) v[e] = first + e < to ? logit<F32>(row, first + e) : -INFINITY;
-        }
+  uint64_t ties = ~0ull, all = 0, whole[2];   // sum of the weights kept; of a part's
+  int bin = kBins, size = 0, by[2];           // by: how far a part's powers are below the row's (64: too far)
+  if (!passes) {
+    const int power = (int)sc.power;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (bin_of(split(v[e], ps)) == own) {
-            const uint32_t at = atomicAdd(&sh.list_size, 1u);
-            if (at < (uint32_t)kList) {
-              sh.list.keys[at] = key_of(v[e]);
-              sh.list.places[at] = (uint32_t)(first + e);
-            }
-          }
+    for (int h = 0; h < 2; ++h) {
+      const bool in = lane + 64 * h < parts && head[h].power != kFarPart && power - head[h].power < 64;
+      by[h] = in ? power - head[h].power : 64;
+      whole[h] = in ? head[h].sum >> by[h] : 0;
+    }
+    all = wave_sum(whole[0] + whole[1]);
+  }
+  if (!passes && set.cuts) {
+    const uint32_t finite = wave_sum((lane < parts ? head[0].finite : 0) + (lane + 64 < parts ? head[1].finite : 0));
+    const bool counting = (uint32_t)set.top_k < finite;
+    // the row's bins: a thread one bin, of every other part
+    {
+      const int j = tid & (kBins - 1);
+      uint64_t sum = 0, many = 0;
+#pragma unroll 4
+      for (int p = tid / kBins; p < parts; p += kRowThreads / kBins) {
+        const int late = __shfl(p < 64 ? by[0] : by[1], p & 63), own = j - 8 * late;   // p is the wave's
+        const int64_t i = (int64_t)p * kBins + max(own, 0);
+        const uint64_t w = part_sums[i];
+        const uint32_t c = part_counts[i];
+        sum += late < 64 && own >= 0 ? w >> late : 0;
+        many += late < 64 && own >= 0 ? c : 0;
+      }
+      if (tid >= kBins) {
+        sh.sums[j] = sum;
+        sh.counts[j] = many;
       }
       __syncthreads();
-      size = (int)min(sh.list_size, (uint32_t)kList);
-      bin = which;
-      return true;
-    };
-    static_assert(kPart == 8 * kRowThreads, "eight logits of a part to a thread");
-    // sum of the list's weights above the cut
-    const auto list_above = [&]() {
-      uint64_t sum = 0;
-      for (int i = tid; i < size; i += kRowThreads)
-        if (sh.list.keys[i] > cut) sum += weight_of(sh.list.keys[i]);
-      return block_reduce<kRowThreads>(sum, sh.tmp, Sum());
-    };
-    const auto key_at = [&](int i) { return sh.list.keys[i]; };
-    uint64_t above, over = 0;   // over: the bins before the list's
-    if ((uint64_t)set.top_k < finite) {
-      const int at = find_bin(sh.counts, kBins, set.top_k, above, sh);
-      if (at < 0 || !collect(at)) return sample_passes<F32>(a, r, row, top, set, sh);
-      uint64_t more;
-      cut = search_list(size, set.top_k - above, more, sh, [](int) { return true; }, key_at, [](int) { return 1; });
-      ties = set.top_k - above - more;
-      uint64_t sum = tid < at ? sh.bins[tid] : 0;
-      over = block_reduce<kRowThreads>(sum, sh.tmp, Sum());
-      all = over + list_above() + ties * weight_of(cut);
+      if (tid < kBins) {
+        sh.sums[j] += sum;
+        sh.counts[j] += many;
+      }
+      static_assert(kRowThreads == 2 * kBins, "two threads a bin");
+      __syncthreads();
     }
-    if (set.top_p < 1.0f) {
-      uint64_t want = (uint64_t)ceil((double)set.top_p * (double)all);
-      if (want == 0) want = 1;
-      const int at = find_bin(sh.bins, bin, want, above, sh);
-      if (at >= 0) {
-        if (!collect(at)) return sample_passes<F32>(a, r, row, top, set, sh);
-        uint64_t more;
-        cut = search_list(size, want - above, more, sh, [](int) { return true; }, key_at,
-                          [&](int i) { return weight_of(sh.list.keys[i]); });
-        const uint64_t w = weight_of(cut);
-        ties = w ? (want - above - more + w - 1) / w : 1;
-        all = above;   // its bins
-      } else if (bin < kBins) {   // among top-k's list
-        const uint64_t high = over + list_above();
-        if (want > high) {
-          const uint64_t w = weight_of(cut), some = w ? (want - high + w - 1) / w : 1;
-          ties = some < ties ? some : ties;
-        } else {
-          uint64_t more;
-          const uint32_t least = cut;
-          cut = search_list(size, want - over, more, sh, [&](int i) { return sh.list.keys[i] > least; }, key_at,
-                            [&](int i) { return weight_of(sh.list.keys[i]); });
-          const uint64_t w = weight_of(cut);
-          ties = w ? (want - over - more + w - 1) / w : 1;
+    uint64_t over = 0;   // top-k: the bins before the list's
+#pragma unroll 1
+    for (int stage = kTopK; stage <= kPlace; ++stage) {
+      int at = -1;            // the bin to look into
+      uint64_t want = 0, above = 0;
+      uint32_t floor = 0;     // of the keys searched
+      if (stage == kTopK) {
+        if (!counting) continue;
+        want = set.top_k;
+      } else if (stage == kTopP) {
+        if (!(set.top_p < 1.0f)) continue;
+        want = (uint64_t)ceil((double)set.top_p * (double)all);
+        if (want == 0) want = 1;
+      } else if (stage == kMinP) {
+        if (!(set.at_least > 0.0)) continue;
+        // the lowest key with a weight that is enough, as weights rise with
+        // keys: near where the logarithm puts it, or found by halves
+        const double max = value_of(top), per = 1.0 / (double)set.heat;
+        const uint32_t guess = key_of((float)(max + (double)set.heat * log(set.at_least)));
+        uint32_t no = kNoKey, yes = top;
+#pragma unroll 1
+        for (int turn = 0; yes - no > 1; ++turn) {
+          // 64 keys about the guess, then one
+          const bool many = turn == 0 && guess > kNoKey + 64 && guess < 0xFFFFFF00u;
+          const uint32_t key = many ? guess - 32 + (uint32_t)lane : no + (yes - no) / 2;
+          const uint64_t enough = __ballot(key >= top || exp64(((double)value_of(key) - max) * per) >= set.at_least);
+          if (many) {
+            if (enough && !(enough & 1)) {
+              yes = guess - 32 + (uint32_t)(__ffsll((unsigned long long)enough) - 1);
+              no = yes - 1;
+            }
+          } else if (enough) {
+            yes = key;
+          } else {
+            no = key;
+          }
         }
-      } else {
-        return sample_passes<F32>(a, r, row, top, set, sh);
-      }
-    }
-    if (set.at_least > 0.0) {
-      // the lowest key with a weight that is enough: weights rise with keys
-      const double max = value_of(top), per = 1.0 / (double)set.heat;
-      uint32_t no = kNoKey, yes = top;
-      while (yes - no > 1) {
-        const uint32_t mid = no + (yes - no) / 2;
-        if (exp64(((double)value_of(mid) - max) * per) >= set.at_least)
-          yes = mid;
-        else
-          no = mid;
-      }
-      if (yes > cut) {
-        const int at = bin_of(split(value_of(yes), sc));
-        if (at >= kBins || !collect(at)) return sample_passes<F32>(a, r, row, top, set, sh);
+        if (yes <= cut) continue;
         cut = yes;
         ties = ~0ull;
+        at = bin_of(split(value_of(yes), sc));
+        if (at >= kBins) {
+          passes = true;
+          break;
+        }
+      } else {
+        if (bin == kBins) continue;
+        // of equal ones at the cut the first by index
+        uint32_t same = 0;
+        for (int i = lane; i < size; i += 64) same += sh.list.keys[i] == cut;
+        if (ties >= wave_sum(same)) continue;
+        want = ties;
       }
-    }
-    if (bin < kBins) {
-      // of equal ones at the cut the first by index
-      uint64_t same = 0;
-      for (int i = tid; i < size; i += kRowThreads) same += sh.list.keys[i] == cut;
-      same = block_reduce<kRowThreads>(same, sh.tmp, Sum());
-      if (ties < same) {
-        uint64_t more;
-        last = search_list(size, ties, more, sh, [&](int i) { return sh.list.keys[i] == cut; },
-                           [&](int i) { return ~sh.list.places[i]; }, [](int) { return 1; });
+      if (stage <= kTopP) {
+        // the first bin with which the sum reaches `want`, and the sum before it
+        const uint64_t *bins = stage == kTopK ? sh.counts : sh.sums;
+        at = 0;
+#pragma unroll 1
+        for (int j = 0; j < kBins; j += 64) at += __popcll(__ballot(bins[j + lane] < want));
+        above = at ? bins[at - 1] : 0;
+        if (at >= bin) {
+          if (bin == kBins) {
+            passes = true;
+            break;
+          }
+          // among top-k's list
+          at = bin;
+          uint64_t w = 0;
+          for (int i = lane; i < size; i += 64)
+            if (sh.list.keys[i] == cut) w = sh.list.weights[i];
+          w = wave_max(w);
+          const uint64_t high = all - ties * w;
+          if (want > high) {
+            const uint64_t some = w ? (want - high + w - 1) / w : 1;
+            ties = some < ties ? some : ties;
+            continue;
+          }
+          above = over;
+          floor = cut;
+        }
+      }
+      if (stage < kPlace && at != bin) {
+        // the logits of that bin, from the parts that have some
+        __syncthreads();
+        if (tid == 0) sh.list_size = 0;
+        uint64_t wanted[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int own = at - 8 * by[h];
+          const bool in = by[h] < 64 && own >= 0;
+          const uint64_t *sums = part_sums + (int64_t)(in ? lane + 64 * h : 0) * kBins + (in ? own : 0);
+          const uint64_t up_to = *sums, before = *(in && own ? sums - 1 : sums);
+          wanted[h] = __ballot(in && (own ? up_to != before : up_to != 0));
+        }
+        __syncthreads();
+#pragma unroll 1
+        while (wanted[0] | wanted[1]) {
+          const int h = wanted[0] ? 0 : 1, l = __ffsll((unsigned long long)wanted[h]) - 1, p = l + 64 * h;
+          wanted[h] &= wanted[h] - 1;
+          const int late = __shfl(h ? by[1] : by[0], l), own = at - 8 * late;
+          Scale ps = sc;
+          ps.power = sc.power - late;
+          const int from = p * kPart, to = min(n, from + kPart);
+          uint32_t some = 0;   // of this thread's 16
+          if (to - from == kPart) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float eight[8];
+              logits<F32, 8>(row, from + (i * kRowThreads + tid) * 8, eight);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[8 * i + e] = eight[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) some |= (uint32_t)(bin_of(split(v[e], ps)) == own) << e;
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < 16; ++e) {
+              const int i = from + (e / 8 * kRowThreads + tid) * 8 + e % 8;
+              if (i < to) some |= (uint32_t)(bin_of(split(logit<F32>(row, i), ps)) == own) << e;
+            }
+          }
+          static_assert(kPart == 16 * kRowThreads, "16 logits of a part to a thread");
+#pragma unroll 1
+          for (; some; some &= some - 1) {
+            const int e = __ffs((int)some) - 1, i = from + (e / 8 * kRowThreads + tid) * 8 + e % 8;
+            const uint32_t to = atomicAdd(&sh.list_size, 1u);
+            if (to >= (uint32_t)kList) break;
+            const float l = logit<F32>(row, i);
+            sh.list.keys[to] = key_of(l);
+            sh.list.places[to] = (uint32_t)i;
+            sh.list.weights[to] = weight_of(l);
+          }
+        }
+        __syncthreads();
+        if (sh.list_size > (uint32_t)kList) {
+          passes = true;
+          break;
+        }
+        size = (int)sh.list_size;
+        bin = at;
+      }
+      if (stage == kMinP) continue;
+      // The value at which the sum over falling values (keys, or complements
+      // of the indices at the cut), of 1 or of weights, of the list reaches
+      // `want`, and the sum above it; if it never does, the lowest.
+      const auto value = [&](int i) {
+        const uint32_t key = sh.list.keys[i];
+        return stage == kPlace ? (key == cut ? ~sh.list.places[i] : 0) : key > floor ? key : 0;   // 0: none
+      };
+      uint32_t found = 0;
+      uint64_t more = 0, w = 0, sum = 0;   // w: the weight found; sum: of the weights above it
+      want -= above;
+      if (size <= 64) {
+        // a lane an entry, each against all
+        const uint32_t mine = lane < size ? value(lane) : 0;
+        const uint64_t weight = lane < size ? sh.list.weights[lane] : 0, add = stage == kTopP ? weight : 1;
+        uint64_t higher = 0;
+#pragma unroll 1
+        for (int j = 0; j < size; ++j) {
+          const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)mine, j);
+          higher += other > mine ? lane_value(add, j) : 0;
+        }
+        found = ~wave_max(mine && higher < want ? ~mine : 0);
+        const int l = __ffsll((unsigned long long)__ballot(mine == found)) - 1;
+        more = lane_value(higher, l);
+        w = lane_value(weight, l);
+        if (stage == kTopK) sum = wave_sum(mine > found ? weight : 0);
+      } else {
+        // eight bits at a time, from the highest that differs
+        uint32_t low = 0xFFFFFFFFu, high = 0;
+        for (int i = lane; i < size; i += 64) {
+          const uint32_t v = value(i);
+          if (v && v < low) low = v;
+          if (v > high) high = v;
+        }
+        high = wave_max(high);
+        low = ~wave_max(~low);
+        found = low;
+        int shift = low < high ? 32 - __clz((int)(low ^ high)) : 0;   // bits from here up are alike
+        if (low < high) found = shift < 32 ? high >> shift << shift : 0;
+#pragma unroll 1
+        while (shift > 0) {
+          const int bits = shift < 8 ? shift : 8, next = shift - bits;
+          __syncthreads();
+          if (tid < 256) sh.digits[tid] = 0;
+          __syncthreads();
+          for (int i = tid; i < size; i += kRowThreads) {
+            const uint32_t v = value(i);
+            if (v && (shift == 32 || v >> shift == found >> shift))
+              atomicAdd(&sh.digits[(v >> next) & ((1u << bits) - 1)],
+                        (unsigned long long)(stage == kTopP ? sh.list.weights[i] : 1));
+          }
+          __syncthreads();
+          // every wave, from the highest down
+          uint64_t so_far = more;
+          int d = -1;
+#pragma unroll 1
+          for (int j = (1 << bits) - 1; j >= 0 && d < 0; j -= 64) {
+            const uint64_t here = j >= lane ? sh.digits[j - lane] : 0, up = so_far + wave_scan(here);
+            const uint64_t there = __ballot(up >= want);
+            if (there) {
+              const int l = __ffsll((unsigned long long)there) - 1;
+              d = j - l;
+              more = lane_value(up - here, l);
+            }
+            so_far = lane_value(up, 63);
+          }
+          if (d < 0) {
+            found = low;
+            break;
+          }
+          found |= (uint32_t)d << next;
+          shift = next;
+        }
+        for (int i = lane; i < size; i += 64) {
+          const uint32_t v = value(i);
+          if (v == found) w = sh.list.weights[i];
+          if (v > found) sum += sh.list.weights[i];
+        }
+        w = wave_max(w);
+        sum = wave_sum(sum);
+      }
+      if (stage == kPlace) {
+        last = found;
+      } else {
+        cut = found;
+        if (stage == kTopK) {
+          ties = want - more;
+          over = at ? sh.sums[at - 1] : 0;
+          all = over + sum + ties * w;
+        } else {
+          ties = w ? (want - more + w - 1) / w : 1;
+        }
       }
     }
   }
-  // what is kept of each part
-  __syncthreads();
-  if (tid < kMaxParts) sh.kept[tid] = tid < parts && bin == kBins ? shifted(sh.heads[tid].sum, behind(tid)) : 0;
-  __syncthreads();
+  if (passes) {
+    sample_passes<F32>(a, r, row, top, set, sh);
+    return;
+  }
+  // what is kept of each part: a part's sum before the bin, and what the list has
   if (bin < kBins) {
-    for (int i = tid; i < parts * kBins; i += kRowThreads) {
-      const int p = i / kBins, by = behind(p);
-      if (by < 64 && i % kBins + 8 * by < bin && part_counts[i])
-        atomicAdd(&sh.kept[p], (unsigned long long)shifted(part_sums[i], by));
-    }
-    for (int i = tid; i < size; i += kRowThreads) {
-      const uint32_t key = sh.list.keys[i], place = sh.list.places[i];
-      if (key > cut || (key == cut && ~place >= last)) atomicAdd(&sh.kept[place / kPart], (unsigned long long)weight_of(key));
+    uint64_t before[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int own = bin - 8 * by[h];
+      const bool in = by[h] < 64 && own > 0;
+      before[h] = part_sums[(int64_t)(in ? lane + 64 * h : 0) * kBins + (in ? own - 1 : 0)];
+      before[h] = in ? before[h] >> by[h] : 0;
     }
     __syncthreads();
+    if (tid < 64) {
+      sh.kept[lane] = before[0];
+      sh.kept[lane + 64] = before[1];
+    }
+    __syncthreads();
+    for (int i = tid; i < size; i += kRowThreads) {
+      const uint32_t key = sh.list.keys[i], place = sh.list.places[i];
+      if (key > cut || (key == cut && ~place >= last)) atomicAdd(&sh.kept[place / kPart], (unsigned long long)sh.list.weights[i]);
+    }
+    __syncthreads();
+    whole[0] = sh.kept[lane];
+    whole[1] = sh.kept[lane + 64];
   }
-  const uint64_t mine = tid < parts ? sh.kept[tid] : 0;
-  const uint64_t before = block_before(mine, sh.tmp);
-  if (tid == parts - 1) sh.above = before + mine;
-  __syncthreads();
-  all = sh.above;
+  // the part in which the sum passes the target
+  uint64_t up[2], start = 0;
+  up[0] = wave_scan(whole[0]);
+  up[1] = parts > 64 ? lane_value(up[0], 63) + wave_scan(whole[1]) : 0;
+  all = lane_value(parts > 64 ? up[1] : up[0], 63);
   uint64_t target = (uint64_t)floor(set.u * (double)all);
   if (target >= all) target = all - 1;
-  __syncthreads();
-  if (tid < parts && before <= target && before + mine > target) {
-    sh.found = tid;
-    sh.above = before;
-  }
-  __syncthreads();
-  const int part = sh.found, from = part * kPart, to = min(n, from + kPart), first = from + 8 * tid;
-  const uint64_t start = sh.above;
-  float v[8];
-  if (first + 8 <= to) {
-    logits<F32, 8>(row, first, v);
-  } else {
-    for (int e = 0; e < 8; ++e) v[e] = first + e < to ? logit<F32>(row, first + e) : -INFINITY;
-  }
-  uint64_t w[8], sum = 0;
-  int final = -1;   // the last that is kept
+  const int h = parts > 64 && lane_value(up[0], 63) <= target ? 1 : 0;
+  const int l = __ffsll((unsigned long long)__ballot(up[h] > target)) - 1, part = l + 64 * h;
+  start = lane_value(up[h] - whole[h], l);
+  __syncthreads();   // (the table, where no list was made)
+  // its logits, 16 in a row to a thread
+  const int from = part * kPart, to = min(n, from + kPart), first = from + 16 * tid;
+  float v[16];
+  if (to - from == kPart) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t key = key_of(v[e]);
-    w[e] = key > cut || (key == cut && ~(uint32_t)(first + e) >= last) ? weight_of(key) : 0;
-    sum += w[e];
-    if (w[e]) final = first + e;
-  }
-  uint64_t at = start + block_before(sum, sh.tmp);
-  int pick = -1;
+    for (int i = 0; i < 16; i += 8) {
+      float eight[8];
+      logits<F32, 8>(row, first + i, eight);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if (at <= target && at + w[e] > target) pick = first + e;
-    at += w[e];
-  }
-  // (the parts' sums are rounded at another place than the row's weights: a
-  // target in the last unit of one is the last token kept)
-  const uint64_t chosen = block_reduce<kRowThreads>((uint64_t)(pick >= 0 ? 1u : 0u) << 32 | (uint32_t)(pick >= 0 ? pick : final + 1),
-                                                    sh.tmp, Larger());
-  const int id = chosen >> 32 ? (int)(uint32_t)chosen : (int)(uint32_t)chosen - 1;
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (id == first + e) {
-      a.ids[r] = id;
-      if (a.logprobs) {
-        const double x = fma((double)v[e], sc.per, -sc.power);
-        a.logprobs[r] = (float)(x * 0.69314718055994530942 - log(ldexp((double)all, -a.unit)));
-      }
+      for (int e = 0; e < 8; ++e) v[i + e] = eight[e];
     }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = logit<F32>(row, min(first + e, n - 1));
+  }
+  // their weights' sum
+  uint64_t sum = 0;
+  int final = -1;   // the last that is kept
+  const auto kept = [&](float x, int place) {
+    const uint32_t key = key_of(x);
+    return place < to && key > kNoKey && (key > cut || (key == cut && ~(uint32_t)place >= last));
+  };
+#pragma unroll 1
+  for (int i = 0; i < 16; i += 4) {
+    float four[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) four[e] = i == 0 ? v[e] : i == 4 ? v[4 + e] : i == 8 ? v[8 + e] : v[12 + e];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t w = weight_of(four[e]);
+      const bool k = kept(four[e], first + i + e) && w;
+      sum += k ? w : 0;
+      final = k ? first + i + e : final;
+    }
+  }
+  // the thread in which the sum passes the target; where rounding at other
+  // places (of the parts' sums, of the weights) leaves none, the last kept
+  uint64_t at = wave_scan(sum);
+  __syncthreads();
+  if (lane == 63) sh.tmp[tid >> 6] = at;
+  if (tid == 0) sh.found = -1;
+  __syncthreads();
+  at += start - sum;
+#pragma unroll 1
+  for (int w = 0; w < tid >> 6; ++w) at += sh.tmp[w];
+  const bool mine = at <= target && at + sum > target;
+  if (mine) sh.found = first;
+  __syncthreads();
+  const bool none = sh.found < 0;
+  if (none) {
+    const uint64_t end = wave_max((uint32_t)(final + 1));
+    if (lane == 0) sh.tmp[tid >> 6] = end;
+    __syncthreads();
+    for (int w = 0; w < kRowThreads / 64; ++w) final = max(final, (int)sh.tmp[w] - 1);
+    __syncthreads();
+  }
+  if (none ? tid == 0 : mine) {
+    int id = final;
+    if (!none)
+#pragma unroll 1
+      for (int e = 0; e < 16; ++e) {
+        const float x = logit<F32>(row, min(first + e, n - 1));
+        const uint64_t w = kept(x, first + e) ? weight_of(x) : 0;
+        if (w) id = first + e;
+        at += w;
+        if (at > target) break;
+      }
+    a.ids[r] = id;
+    if (a.logprobs) {
+      const double x = fma((double)logit<F32>(row, id), sc.per, -sc.power);
+      a.logprobs[r] = (float)(x * 0.69314718055994530942 - log(ldexp((double)all, -a.unit)));
+    }
+  }
 }
 
 }  // namespace
@@ -817,6 +1004,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
 hipError_t launch_sample(const SampleArgs &a, hipStream_t s) {
   const int64_t items = (int64_t)a.rows * a.parts;
   const unsigned groups = (unsigned)(items < kSampleGroups ? items : kSampleGroups);
+  static_assert(sizeof(Shared) <= 160 * 1024, "one workgroup's LDS");
   if (a.f32) {
     hipLaunchKernelGGL(sample_parts_kernel<true>, dim3(groups), dim3(kPartThreads), 0, s, a);
     hipLaunchKernelGGL(sample_rows_kernel<true>, dim3((unsigned)a.rows), dim3(kRowThreads), sizeof(Shared), s, a);

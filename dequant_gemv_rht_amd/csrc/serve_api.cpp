@@ -234,10 +234,12 @@ wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vo
   a.logits = logits;
   a.ldl = ldl;
   a.u = u;
-  a.temperature = temperature;
-  a.top_k = top_k;
-  a.top_p = top_p;
-  a.min_p = min_p;
+  a.given = (temperature ? wq::kGivenHeat : 0) | (top_k ? wq::kGivenTopK : 0) | (top_p ? wq::kGivenTopP : 0) |
+            (min_p ? wq::kGivenMinP : 0);
+  a.temperature = temperature ? temperature : u;
+  a.top_k = top_k ? top_k : reinterpret_cast<const int32_t *>(u);
+  a.top_p = top_p ? top_p : u;
+  a.min_p = min_p ? min_p : u;
   a.ids = ids;
   a.logprobs = logprobs;
   a.rows = (int32_t)rows;

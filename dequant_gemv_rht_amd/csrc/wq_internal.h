@@ -257,7 +257,7 @@ hipError_t launch_lora(const LoraArgs &a, const LoraPlan &p, hipStream_t s);
 
 constexpr int kSamplePart = 8192;   // logits of a row that a workgroup takes at once
 constexpr int kSampleBins = 256;
-constexpr int64_t kSampleGroups = 2048;
+constexpr int64_t kSampleGroups = 640;
 constexpr int32_t kFarPart = INT32_MIN;
 struct SamplePart {
   uint64_t best;                // largest key, complement of its first index
@@ -265,6 +265,7 @@ struct SamplePart {
   int32_t power;                // kFarPart: weights not summed
   uint32_t finite;
 };
+constexpr uint32_t kGivenHeat = 1, kGivenTopK = 2, kGivenTopP = 4, kGivenMinP = 8;
 struct SampleArgs {
   const void *logits;
   int64_t ldl;
@@ -274,8 +275,9 @@ struct SampleArgs {
   float *logprobs;
   int32_t rows, vocab, f32, parts;
   int32_t unit;                 // weights are counted in 2^-unit
+  uint32_t given;               // kGiven...: settings that the caller gave; the others point at any array
   SamplePart *heads;            // [rows][parts]
-  uint64_t *sums;               // [rows][parts][kSampleBins]
+  uint64_t *sums;               // [rows][parts][kSampleBins], up to and with each bin
   uint32_t *counts;
 };
 size_t sample_workspace(int64_t rows, int64_t vocab, size_t *sums_at, size_t *counts_at);
