@@ -175,22 +175,38 @@ struct Sum {
 
 // ---------------------------------------------------------------- parts
 
+// the largest of v over a wave, in every lane
+__device__ __forceinline__ float wave_max_f32(float v) {
+  v = fmaxf(v, dpp<kQuadXor1>(v));
+  v = fmaxf(v, dpp<kQuadXor2>(v));
+  v = fmaxf(v, dpp<kRowHalfMirror>(v));
+  v = fmaxf(v, dpp<kRowMirror>(v));
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+
+// The next part's logits and settings are on their way while this one's are
+// counted, the bins of one part are summed up by one wave while the others go
+// on: two sets of bins, two barriers a part.
 template <bool F32>
 __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a) {
   constexpr int V = F32 ? 4 : 8;   // logits in 16 bytes
+  constexpr int kWaves = kPartThreads / 64;
   __shared__ double table[kTable];
-  __shared__ unsigned long long sums[kBins];
-  __shared__ uint32_t counts[kBins];
-  __shared__ uint64_t tmp[kPartThreads / 64];
-  __shared__ uint32_t tmp_counts[kBins / 64];
-  const int tid = threadIdx.x;
-  for (int j = tid; j < kTable; j += kPartThreads) table[j] = table_entry(j);
+  struct Bins {
+    alignas(16) unsigned long long sums[kBins];
+    alignas(16) uint32_t counts[kBins];
+    unsigned long long sum;
+    uint32_t finite, where;
+  };
+  __shared__ Bins both[2];
+  __shared__ float tops[2][kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int items = a.rows * a.parts;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    const int r = item / a.parts, part = item - r * a.parts, from = part * kPart;
+  const auto fetch = [&](int item, float (&v)[kEach], Settings &s) {
+    const int r = item / a.parts, from = (item - r * a.parts) * kPart;
     const void *row = F32 ? (const void *)(static_cast<const float *>(a.logits) + r * a.ldl)
                           : (const void *)(static_cast<const uint16_t *>(a.logits) + r * a.ldl);
-    float v[kEach];
     if (from + kPart <= a.vocab) {
 #pragma unroll
       for (int i = 0; i < kEach / V; ++i) {
@@ -199,102 +215,143 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
 #pragma unroll
         for (int e = 0; e < V; ++e) v[V * i + e] = some[e];
       }
-    } else {
+    } else {   // (a lambda of its own would join the loads of the two)
+#pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int at = from + (i / V * kPartThreads + tid) * V + i % V;
-        v[i] = at < a.vocab ? logit<F32>(row, at) : -INFINITY;
+        v[i] = logit<F32>(row, min(at, a.vocab - 1));
+        v[i] = at < a.vocab ? v[i] : -INFINITY;
       }
     }
-    const Settings s = settings(a, r);
-    if (s.cuts && tid < kBins) {
-      sums[tid] = 0;
-      counts[tid] = 0;
-    }
+    s = settings(a, r);
+  };
+  float v[kEach], next[kEach];
+  Settings s, next_s;
+  if ((int)blockIdx.x < items) fetch(blockIdx.x, v, s);
+  for (int j = tid; j < kTable; j += kPartThreads) table[j] = table_entry(j);
+  for (int j = tid; j < 2 * kBins; j += kPartThreads) {
+    both[j / kBins].sums[j % kBins] = 0;
+    both[j / kBins].counts[j % kBins] = 0;
+  }
+  if (tid < 2) {
+    both[tid].sum = 0;
+    both[tid].finite = 0;
+    both[tid].where = 0xFFFFFFFFu;
+  }
+  int turn = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x, ++turn) {
+    Bins &sh = both[turn & 1];
     float top = -INFINITY;
-    int where = 0, finite = 0;
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int at = from + (i / V * kPartThreads + tid) * V + i % V;
-      where = v[i] > top ? at : where;
-      top = v[i] > top ? v[i] : top;
-      finite += v[i] > -INFINITY;
-    }
-    const uint64_t best =
-        block_reduce<kPartThreads>((uint64_t)key_of(top) << 32 | (uint32_t)~where, tmp, Larger());   // and the bins are cleared
-    SamplePart head;
-    head.best = best;
-    head.sum = 0;
-    head.power = kFarPart;   // no bins
-    head.finite = 0;
-    if (!s.greedy && (uint32_t)(best >> 32) > kNoKey) {
-      Scale sc;
-      sc.per = 1.4426950408889634074 / (double)s.heat;
-      sc.unit = a.unit;
-      const double most = (double)value_of((uint32_t)(best >> 32)) * sc.per;
-      const bool near = fabs(most) < kFar;
-      sc.power = floor(most);
-      uint64_t sum = 0;
-      if (near) {
-        // eight at a time: a table entry of one waits behind the sums of none
-#pragma unroll
-        for (int i = 0; i < kEach; i += 8) {
-          Split p[8];
-          uint64_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = split(v[i + e], sc);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = counted(p[e], sc, table);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum += w[e];
-          if (!s.cuts) continue;
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (bin_of(p[e]) < kBins) {
-              atomicAdd(&sums[bin_of(p[e])], (unsigned long long)w[e]);
-              if (s.top_k < a.vocab) atomicAdd(&counts[bin_of(p[e])], 1u);
-            }
-        }
-        head.power = (int32_t)sc.power;
-      }
-      head.sum = block_reduce<kPartThreads>(sum, tmp, Sum());
-      head.finite = (uint32_t)block_reduce<kPartThreads>((uint64_t)finite, tmp, Sum());
-      if (near && s.cuts) {
-        // sums up to and with each bin
-        uint64_t up = tid < kBins ? sums[tid] : 0;
-        uint32_t many = tid < kBins ? counts[tid] : 0;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-          const uint64_t o = __shfl_up(up, d);
-          const uint32_t c = __shfl_up(many, d);
-          if ((tid & 63) >= d) {
-            up += o;
-            many += c;
-          }
-        }
-        __syncthreads();
-        if ((tid & 63) == 63 && tid < kBins) {
-          tmp[tid >> 6] = up;
-          tmp_counts[tid >> 6] = many;
-        }
-        __syncthreads();
-        if (tid < kBins) {
-          for (int w = 0; w < tid >> 6; ++w) {
-            up += tmp[w];
-            many += tmp_counts[w];
-          }
-          a.sums[(int64_t)item * kBins + tid] = up;
-          a.counts[(int64_t)item * kBins + tid] = many;
-        }
-      }
-    }
-    if (tid == 0) a.heads[item] = head;
+    for (int i = 0; i < kEach; ++i) top = fmaxf(top, v[i]);   // (not NaN)
+    const float high = wave_max_f32(top);
+    if (lane == 0) tops[turn & 1][wave] = high;
     __syncthreads();
+    float most = tops[turn & 1][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) most = fmaxf(most, tops[turn & 1][w]);
+    if (top == most) {   // the first of them
+#pragma unroll
+      for (int i = kEach - 1; i >= 0; --i)
+        if (v[i] == most) top = __builtin_bit_cast(float, (i / V * kPartThreads + tid) * V + i % V);
+      atomicMin(&sh.where, __builtin_bit_cast(uint32_t, top));
+    }
+    Scale sc;
+    sc.per = 1.4426950408889634074 / (double)s.heat;
+    sc.unit = a.unit;
+    const double power = (double)most * sc.per;
+    const bool near = !s.greedy && most > -INFINITY && fabs(power) < kFar;
+    sc.power = floor(power);
+    if (item + (int)gridDim.x < items) fetch(item + gridDim.x, next, next_s);
+    if (near) {
+      uint64_t sum = 0;
+      const bool counts = s.top_k < a.vocab;
+      // eight at a time: a table entry of one waits behind the sums of none
+#pragma unroll
+      for (int i = 0; i < kEach; i += 8) {
+        Split p[8];
+        uint64_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p[e] = split(v[i + e], sc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = counted(p[e], sc, table);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += w[e];
+        if (!s.cuts) continue;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (bin_of(p[e]) < kBins) {
+            atomicAdd(&sh.sums[bin_of(p[e])], (unsigned long long)w[e]);
+            if (counts) atomicAdd(&sh.counts[bin_of(p[e])], 1u);
+          }
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+      if (lane == 0) atomicAdd(&sh.sum, (unsigned long long)sum);
+    }
+    if (!s.greedy && s.top_k < a.vocab) {
+      uint32_t finite = 0;   // of the wave
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) finite += __popcll(__ballot(v[i] > -INFINITY));
+      if (lane == 0) atomicAdd(&sh.finite, finite);
+    }
+    __syncthreads();
+    if (wave == turn % kWaves) {
+      if (lane == 0) {
+        const int r = item / a.parts;
+        SamplePart head;
+        head.best = (uint64_t)key_of(most) << 32 | (uint32_t)~((item - r * a.parts) * kPart + sh.where);
+        head.sum = sh.sum;
+        head.power = near ? (int32_t)sc.power : kFarPart;   // far: no bins
+        head.finite = sh.finite;
+        a.heads[item] = head;
+        sh.sum = 0;
+        sh.finite = 0;
+        sh.where = 0xFFFFFFFFu;
+      }
+      if (near && s.cuts) {
+        // sums up to and with each bin, four a lane
+        uint64_t up[4];
+        uint32_t many[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          up[e] = sh.sums[4 * lane + e] + (e ? up[e - 1] : 0);
+          many[e] = sh.counts[4 * lane + e] + (e ? many[e - 1] : 0);
+          sh.sums[4 * lane + e] = 0;
+          sh.counts[4 * lane + e] = 0;
+        }
+        static_assert(kBins == 256, "four a lane");
+        uint64_t all = up[3];
+        uint32_t all_many = many[3];
+#pragma unroll 1
+        for (int d = 1; d < 64; d <<= 1) {
+          const uint64_t o = __shfl_up(all, d);
+          const uint32_t c = __shfl_up(all_many, d);
+          if (lane >= d) {
+            all += o;
+            all_many += c;
+          }
+        }
+        all -= up[3];
+        all_many -= many[3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          a.sums[(int64_t)item * kBins + 4 * lane + e] = all + up[e];
+          a.counts[(int64_t)item * kBins + 4 * lane + e] = all_many + many[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) v[i] = next[i];
+    s = next_s;
   }
 }
 
 // ---------------------------------------------------------------- rows
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 1024;
+constexpr int kMine = kPart / kRowThreads;   // logits of a part to a thread
+static_assert(kMine == 8, "");
 constexpr int kList = 8192;                  // logits of a cut's bin, at most
 
 // the sum of v over the threads before this one
@@ -314,18 +371,19 @@ __device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t *tmp) {
 }
 
 constexpr int kSlowBins = 2048;
-constexpr int kTurn = 4 * kRowThreads;       // logits of one turn of the passes
-constexpr int kTurns = (1 << 20) / kTurn;
+constexpr int kTurn = 4 * kRowThreads;       // logits that a pass takes side by side
+constexpr int kTurns = kMaxParts;
 
 struct Shared {
   double table[kTable];
   uint64_t tmp[kRowThreads / 64];
-  uint64_t sums[kBins], counts[kBins];       // the row's, up to and with each bin
+  unsigned long long sums[kBins], counts[kBins];   // the row's, up to and with each bin
   unsigned long long digits[256];            // of a search in a long list
   unsigned long long kept[kMaxParts];        // of each part
   uint64_t above;
+  unsigned long long found_weight, found_sum;
   int32_t found;
-  uint32_t list_size;
+  uint32_t list_size, low, high;
   union {
     struct {
       uint64_t weights[kList];
@@ -355,17 +413,23 @@ __device__ __forceinline__ double weight(uint32_t key, const Far &s) {
 
 __device__ __forceinline__ uint64_t counted(double w, const Far &s) { return (uint64_t)rint(w * s.unit); }
 
-// f(key) for every logit of [from, to), from a multiple of 4
+// f(key) for every logit of [from, to)
 template <bool F32, typename F>
 __device__ __forceinline__ void each_key(const void *row, int from, int to, F f) {
-  int i = from + 4 * (int)threadIdx.x;
-  for (; i + 4 <= to; i += kTurn) {
-    float v[4];
-    logits<F32, 4>(row, i, v);
+  constexpr int kAtOnce = 4;
+  int i = from;
+#pragma unroll 1
+  for (; i + kAtOnce * kTurn <= to; i += kAtOnce * kTurn) {
+    float v[kAtOnce][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) f(key_of(v[e]));
+    for (int j = 0; j < kAtOnce; ++j) logits<F32, 4>(row, i + j * kTurn + 4 * (int)threadIdx.x, v[j]);
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(key_of(v[j][e]));
   }
-  for (int e = i; e < to && e < i + 4; ++e) f(key_of(logit<F32>(row, e)));
+#pragma unroll 1
+  for (i += (int)threadIdx.x; i < to; i += kRowThreads) f(key_of(logit<F32>(row, i)));
 }
 
 // The key at which the sum over falling keys, of counts or of weights, of
@@ -386,21 +450,14 @@ __device__ uint32_t search_row(const void *row, int n, const Far &s, uint32_t fl
       if (add) atomicAdd(&sh.slow.bins[(key >> next) & ((1u << bits) - 1)], (unsigned long long)add);
     });
     __syncthreads();
-    // from the highest down, four bins a thread
-    const int d = (1 << bits) - 1 - 4 * (int)threadIdx.x;
-    uint64_t here = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) here += d >= e ? sh.slow.bins[d - e] : 0;
-    uint64_t before = above + block_before(here, sh.tmp);
-    if (before < want && before + here >= want)
-      for (int e = 0; e < 4 && d >= e; ++e) {
-        const uint64_t one = sh.slow.bins[d - e];
-        if (before < want && before + one >= want) {
-          sh.found = d - e;
-          sh.above = before;
-        }
-        before += one;
-      }
+    // from the highest down, two bins a thread
+    const int d = (1 << bits) - 1 - 2 * (int)threadIdx.x;
+    const uint64_t one = d >= 0 ? sh.slow.bins[d] : 0, two = d > 0 ? sh.slow.bins[d - 1] : 0;
+    const uint64_t before = above + block_before(one + two, sh.tmp);
+    if (before < want && before + one + two >= want) {
+      sh.found = before + one >= want ? d : d - 1;
+      sh.above = before + one >= want ? before : before + one;
+    }
     __syncthreads();
     prefix |= (uint32_t)sh.found << next;
     above = sh.above;
@@ -447,16 +504,16 @@ __device__ __forceinline__ void sample_passes(const SampleArgs &a, int64_t r, co
       ties = (want - above + w - 1) / w;
     }
   }
-  // sums of each turn, in the order of the index
+  // sums of each part
   const double cut_weight = weight(cut, s);
   const uint64_t tie = cut_weight >= set.at_least ? counted(cut_weight, s) : 0;
-  const int turns = (n + kTurn - 1) / kTurn;
+  const int turns = (n + kPart - 1) / kPart;
   for (int t = tid; t < turns; t += kRowThreads) sh.slow.sums[t] = sh.slow.ties[t] = 0;
   __syncthreads();
   for (int t = 0; t < turns; ++t) {
     uint64_t sum = 0;
     uint32_t same = 0;
-    each_key<F32>(row, t * kTurn, min(n, (t + 1) * kTurn), [&](uint32_t key) {
+    each_key<F32>(row, t * kPart, min(n, (t + 1) * kPart), [&](uint32_t key) {
       same += key == cut;
       if (key > cut) {
         const double w = weight(key, s);
@@ -492,40 +549,38 @@ __device__ __forceinline__ void sample_passes(const SampleArgs &a, int64_t r, co
     before += here;
     seen += kept;
   }
-  // the turn's logits, four in a row to a thread
-  const int first = t * kTurn + 4 * tid;
-  uint32_t key[4];
+  // the part's logits, some in a row to a thread
+  const int first = t * kPart + kMine * tid;
   uint64_t same = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    key[e] = first + e < n ? key_of(logit<F32>(row, first + e)) : 0;
-    same += key[e] == cut && cut;
-  }
-  uint64_t rank = seen + block_before(same, sh.tmp);
-  uint64_t w[4], mine = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    w[e] = 0;
-    if (key[e] > cut) {
-      const double v = weight(key[e], s);
-      if (v >= set.at_least) w[e] = counted(v, s);
-    } else if (key[e] == cut && cut) {
-      if (rank < ties) w[e] = tie;
-      ++rank;
+#pragma unroll 1
+  for (int e = 0; e < kMine; ++e) same += first + e < n && cut && key_of(logit<F32>(row, first + e)) == cut;
+  const uint64_t rank = seen + block_before(same, sh.tmp);
+  const auto weight_at = [&](uint32_t key, uint64_t &place) -> uint64_t {
+    if (key > cut) {
+      const double v = weight(key, s);
+      return v >= set.at_least ? counted(v, s) : 0;
     }
-    mine += w[e];
-  }
+    return key == cut && cut && place++ < ties ? tie : 0;
+  };
+  uint64_t mine = 0, place = rank;
+#pragma unroll 1
+  for (int e = 0; e < kMine && first + e < n; ++e) mine += weight_at(key_of(logit<F32>(row, first + e)), place);
   uint64_t sum = before + block_before(mine, sh.tmp);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (sum <= target && sum + w[e] > target) {
-      a.ids[r] = first + e;
-      if (a.logprobs) {
-        const double z = key[e] == s.top ? 0.0 : ((double)value_of(key[e]) - s.max) * s.per;
-        a.logprobs[r] = (float)(z - log((double)all / s.unit));
+  if (sum <= target && sum + mine > target) {
+    place = rank;
+#pragma unroll 1
+    for (int e = 0; e < kMine; ++e) {
+      const uint32_t key = key_of(logit<F32>(row, first + e));
+      sum += weight_at(key, place);
+      if (sum > target) {
+        a.ids[r] = first + e;
+        if (a.logprobs) {
+          const double z = key == s.top ? 0.0 : ((double)value_of(key) - s.max) * s.per;
+          a.logprobs[r] = (float)(z - log((double)all / s.unit));
+        }
+        break;
       }
     }
-    sum += w[e];
   }
 }
 
@@ -564,6 +619,21 @@ __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
 }
 
+// kMine logits of a thread, from `first` on; where fewer are left, those up to
+// the row's end: the first of them is at the place returned, and those before
+// `first` are another thread's.
+template <bool F32>
+__device__ __forceinline__ int fetch(const void *row, int first, int n, float (&v)[kMine]) {
+  const int place = max(min(first, n - kMine), 0);
+  if (n >= kMine) {
+    logits<F32, kMine>(row, place, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kMine; ++e) v[e] = e < n ? logit<F32>(row, min(e, n - 1)) : NAN;
+  }
+  return place;
+}
+
 // In turn: what top-k leaves, what top-p leaves of that, what min-p leaves of
 // that, and which of equal logits at the cut.
 enum Stage { kTopK, kTopP, kMinP, kPlace };
@@ -593,8 +663,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     }
     return;
   }
-#pragma unroll 1
-  for (int j = tid; j < kTable; j += kRowThreads) sh.table[j] = table_entry(j);
+  sh.table[tid] = table_entry(tid);
+  static_assert(kTable == kRowThreads, "an entry a thread");
+  if (tid < kBins) sh.sums[tid] = sh.counts[tid] = 0;
+  __syncthreads();
   Scale sc;
   sc.per = 1.4426950408889634074 / (double)set.heat;
   sc.unit = a.unit;
@@ -623,11 +695,11 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   if (!passes && set.cuts) {
     const uint32_t finite = wave_sum((lane < parts ? head[0].finite : 0) + (lane + 64 < parts ? head[1].finite : 0));
     const bool counting = (uint32_t)set.top_k < finite;
-    // the row's bins: a thread one bin, of every other part
+    // the row's bins: a thread one bin of some parts
     {
       const int j = tid & (kBins - 1);
       uint64_t sum = 0, many = 0;
-#pragma unroll 4
+#pragma unroll 5
       for (int p = tid / kBins; p < parts; p += kRowThreads / kBins) {
         const int late = __shfl(p < 64 ? by[0] : by[1], p & 63), own = j - 8 * late;   // p is the wave's
         const int64_t i = (int64_t)p * kBins + max(own, 0);
@@ -636,16 +708,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         sum += late < 64 && own >= 0 ? w >> late : 0;
         many += late < 64 && own >= 0 ? c : 0;
       }
-      if (tid >= kBins) {
-        sh.sums[j] = sum;
-        sh.counts[j] = many;
-      }
-      __syncthreads();
-      if (tid < kBins) {
-        sh.sums[j] += sum;
-        sh.counts[j] += many;
-      }
-      static_assert(kRowThreads == 2 * kBins, "two threads a bin");
+      atomicAdd(&sh.sums[j], (unsigned long long)sum);
+      atomicAdd(&sh.counts[j], (unsigned long long)many);
+      static_assert(kRowThreads % kBins == 0, "threads of a bin");
       __syncthreads();
     }
     uint64_t over = 0;   // top-k: the bins before the list's
@@ -696,14 +761,20 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
       } else {
         if (bin == kBins) continue;
         // of equal ones at the cut the first by index
+        __syncthreads();
+        if (tid == 0) sh.list_size = 0;   // (size has it)
+        __syncthreads();
         uint32_t same = 0;
-        for (int i = lane; i < size; i += 64) same += sh.list.keys[i] == cut;
-        if (ties >= wave_sum(same)) continue;
+        for (int i = tid; i < size; i += kRowThreads) same += sh.list.keys[i] == cut;
+        same = wave_sum(same);
+        if (lane == 0 && same) atomicAdd(&sh.list_size, same);
+        __syncthreads();
+        if (ties >= sh.list_size) continue;
         want = ties;
       }
       if (stage <= kTopP) {
         // the first bin with which the sum reaches `want`, and the sum before it
-        const uint64_t *bins = stage == kTopK ? sh.counts : sh.sums;
+        const unsigned long long *bins = stage == kTopK ? sh.counts : sh.sums;
         at = 0;
 #pragma unroll 1
         for (int j = 0; j < kBins; j += 64) at += __popcll(__ballot(bins[j + lane] < want));
@@ -715,11 +786,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
           }
           // among top-k's list
           at = bin;
-          uint64_t w = 0;
-          for (int i = lane; i < size; i += 64)
-            if (sh.list.keys[i] == cut) w = sh.list.weights[i];
-          w = wave_max(w);
-          const uint64_t high = all - ties * w;
+          const uint64_t w = weight_of(value_of(cut)), high = all - ties * w;
           if (want > high) {
             const uint64_t some = w ? (want - high + w - 1) / w : 1;
             ties = some < ties ? some : ties;
@@ -743,45 +810,90 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
           wanted[h] = __ballot(in && (own ? up_to != before : up_to != 0));
         }
         __syncthreads();
+        // The bin's logits are those from `from_value` up to `to_value`, whose
+        // keys are the lowest of the bin and of the next higher: near where
+        // the logarithm puts them (64 keys at once), or by halves.
+        float from_value = 0.0f, to_value = 0.0f;
+#pragma unroll 1
+        for (int edge = 0; edge < 2; ++edge) {
+          const uint32_t guess = key_of((float)(((double)(8 - at + edge) * 0.125 - 1.0 / 2048.0 + sc.power) / sc.per));
+          uint32_t no = kNoKey, yes = top + 1;
+#pragma unroll 1
+          for (int turn = 0; yes - no > 1; ++turn) {
+            const bool many = turn == 0 && guess > kNoKey + 64 && guess <= top;
+            const uint32_t key = many ? guess - 32 + (uint32_t)lane : no + (yes - no) / 2;
+            const uint64_t there = __ballot(key > top || bin_of(split(value_of(key), sc)) <= at - edge);
+            if (many) {
+              if (there && !(there & 1)) {
+                yes = guess - 32 + (uint32_t)(__ffsll((unsigned long long)there) - 1);
+                no = yes - 1;
+              }
+            } else if (there) {
+              yes = key;
+            } else {
+              no = key;
+            }
+          }
+          from_value = edge ? from_value : value_of(yes);
+          to_value = yes > top ? INFINITY : value_of(yes);   // above the largest: nothing is that high
+        }
 #pragma unroll 1
         while (wanted[0] | wanted[1]) {
-          const int h = wanted[0] ? 0 : 1, l = __ffsll((unsigned long long)wanted[h]) - 1, p = l + 64 * h;
-          wanted[h] &= wanted[h] - 1;
-          const int late = __shfl(h ? by[1] : by[0], l), own = at - 8 * late;
-          Scale ps = sc;
-          ps.power = sc.power - late;
-          const int from = p * kPart, to = min(n, from + kPart);
-          uint32_t some = 0;   // of this thread's 16
-          if (to - from == kPart) {
-            float v[16];
+          // four parts asked for at once
+          int which[4];
+          float four[4][kMine];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float eight[8];
-              logits<F32, 8>(row, from + (i * kRowThreads + tid) * 8, eight);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[8 * i + e] = eight[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) some |= (uint32_t)(bin_of(split(v[e], ps)) == own) << e;
-          } else {
-#pragma unroll 1
-            for (int e = 0; e < 16; ++e) {
-              const int i = from + (e / 8 * kRowThreads + tid) * 8 + e % 8;
-              if (i < to) some |= (uint32_t)(bin_of(split(logit<F32>(row, i), ps)) == own) << e;
-            }
+          for (int j = 0; j < 4; ++j) {
+            const bool low = wanted[0] != 0;
+            const uint64_t left = low ? wanted[0] : wanted[1];
+            which[j] = left ? __ffsll((unsigned long long)left) - 1 + (low ? 0 : 64) : -1;
+            wanted[0] &= wanted[0] - (low ? 1 : 0);
+            wanted[1] &= wanted[1] - (low || !left ? 0 : 1);
+            fetch<F32>(row, max(which[j], 0) * kPart + kMine * tid, n, four[j]);
           }
-          static_assert(kPart == 16 * kRowThreads, "16 logits of a part to a thread");
 #pragma unroll 1
-          for (; some; some &= some - 1) {
-            const int e = __ffs((int)some) - 1, i = from + (e / 8 * kRowThreads + tid) * 8 + e % 8;
-            const uint32_t to = atomicAdd(&sh.list_size, 1u);
-            if (to >= (uint32_t)kList) break;
-            const float l = logit<F32>(row, i);
-            sh.list.keys[to] = key_of(l);
-            sh.list.places[to] = (uint32_t)i;
-            sh.list.weights[to] = weight_of(l);
+          for (int j = 0; j < 4; ++j) {
+            const int p = j < 2 ? (j ? which[1] : which[0]) : j == 2 ? which[2] : which[3];
+            if (p < 0) break;
+            const int first = p * kPart + kMine * tid, from = max(min(first, n - kMine), 0);
+            float v[kMine];
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) v[e] = j < 2 ? (j ? four[1][e] : four[0][e]) : j == 2 ? four[2][e] : four[3][e];
+            if ((p + 1) * kPart > n) {
+#pragma unroll
+              for (int e = 0; e < kMine; ++e) v[e] = from + e >= first ? v[e] : NAN;   // another thread's
+            }
+            uint64_t in[kMine];   // lanes
+            uint32_t many = 0;
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+              in[e] = __ballot(v[e] >= from_value && v[e] < to_value);
+              many += (uint32_t)__popcll(in[e]);
+            }
+            if (!many) continue;
+            uint32_t to = 0;
+            if (lane == 0) to = atomicAdd(&sh.list_size, many);
+            to = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
+#pragma unroll
+            for (int e = 0; e < kMine; ++e) {
+              if (!in[e]) continue;
+              const uint32_t i = to + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[e] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[e], 0));
+              if ((in[e] >> lane & 1) && i < (uint32_t)kList) {
+                // (the key later)
+                sh.list.keys[i] = __builtin_bit_cast(uint32_t, v[e]);
+                sh.list.places[i] = (uint32_t)(from + e);
+              }
+              to += (uint32_t)__popcll(in[e]);
+            }
           }
         }
+        __syncthreads();
+        if (sh.list_size <= (uint32_t)kList)
+          for (int i = tid; i < (int)sh.list_size; i += kRowThreads) {
+            const float l = __builtin_bit_cast(float, sh.list.keys[i]);
+            sh.list.keys[i] = key_of(l);
+            sh.list.weights[i] = weight_of(l);
+          }
         __syncthreads();
         if (sh.list_size > (uint32_t)kList) {
           passes = true;
@@ -818,58 +930,77 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         if (stage == kTopK) sum = wave_sum(mine > found ? weight : 0);
       } else {
         // eight bits at a time, from the highest that differs
+        __syncthreads();
+        if (tid == 0) {
+          sh.low = 0xFFFFFFFFu;
+          sh.high = 0;
+          sh.found_weight = sh.found_sum = 0;
+        }
+        __syncthreads();
         uint32_t low = 0xFFFFFFFFu, high = 0;
-        for (int i = lane; i < size; i += 64) {
+        for (int i = tid; i < size; i += kRowThreads) {
           const uint32_t v = value(i);
           if (v && v < low) low = v;
           if (v > high) high = v;
         }
         high = wave_max(high);
         low = ~wave_max(~low);
+        if (lane == 0) {
+          atomicMax(&sh.high, high);
+          atomicMin(&sh.low, low);
+        }
+        __syncthreads();
+        high = sh.high;
+        low = sh.low;
         found = low;
         int shift = low < high ? 32 - __clz((int)(low ^ high)) : 0;   // bits from here up are alike
         if (low < high) found = shift < 32 ? high >> shift << shift : 0;
 #pragma unroll 1
         while (shift > 0) {
-          const int bits = shift < 8 ? shift : 8, next = shift - bits;
-          __syncthreads();
+          const int bits = shift < 8 ? shift : 8, next = shift - bits, end = (1 << bits) - 1;
           if (tid < 256) sh.digits[tid] = 0;
           __syncthreads();
           for (int i = tid; i < size; i += kRowThreads) {
             const uint32_t v = value(i);
             if (v && (shift == 32 || v >> shift == found >> shift))
-              atomicAdd(&sh.digits[(v >> next) & ((1u << bits) - 1)],
+              atomicAdd(&sh.digits[end - ((v >> next) & end)],   // from the highest on
                         (unsigned long long)(stage == kTopP ? sh.list.weights[i] : 1));
           }
           __syncthreads();
-          // every wave, from the highest down
-          uint64_t so_far = more;
-          int d = -1;
-#pragma unroll 1
-          for (int j = (1 << bits) - 1; j >= 0 && d < 0; j -= 64) {
-            const uint64_t here = j >= lane ? sh.digits[j - lane] : 0, up = so_far + wave_scan(here);
-            const uint64_t there = __ballot(up >= want);
-            if (there) {
-              const int l = __ffsll((unsigned long long)there) - 1;
-              d = j - l;
-              more = lane_value(up - here, l);
-            }
-            so_far = lane_value(up, 63);
-          }
-          if (d < 0) {
+          // every wave: four digits a lane
+          uint64_t up[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up[e] = sh.digits[4 * lane + e] + (e ? up[e - 1] : 0);
+          const uint64_t before = more + wave_scan(up[3]) - up[3];
+          const uint64_t there = __ballot(before + up[3] >= want);
+          __syncthreads();
+          if (!there) {
             found = low;
             break;
           }
-          found |= (uint32_t)d << next;
+          const int l = __ffsll((unsigned long long)there) - 1;
+          int e = 0;
+          uint64_t higher = before;
+#pragma unroll
+          for (int f = 0; f < 3; ++f)
+            if (before + up[f] < want) {
+              e = f + 1;
+              higher = before + up[f];
+            }
+          more = lane_value(higher, l);
+          found |= (uint32_t)(end - (4 * l + __builtin_amdgcn_readlane(e, l))) << next;
           shift = next;
         }
-        for (int i = lane; i < size; i += 64) {
+        for (int i = tid; i < size; i += kRowThreads) {
           const uint32_t v = value(i);
-          if (v == found) w = sh.list.weights[i];
+          if (v == found) sh.found_weight = sh.list.weights[i];
           if (v > found) sum += sh.list.weights[i];
         }
-        w = wave_max(w);
         sum = wave_sum(sum);
+        if (lane == 0 && sum) atomicAdd(&sh.found_sum, (unsigned long long)sum);
+        __syncthreads();
+        w = sh.found_weight;
+        sum = sh.found_sum;
       }
       if (stage == kPlace) {
         last = found;
@@ -924,43 +1055,31 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   const int l = __ffsll((unsigned long long)__ballot(up[h] > target)) - 1, part = l + 64 * h;
   start = lane_value(up[h] - whole[h], l);
   __syncthreads();   // (the table, where no list was made)
-  // its logits, 16 in a row to a thread
-  const int from = part * kPart, to = min(n, from + kPart), first = from + 16 * tid;
-  float v[16];
-  if (to - from == kPart) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 8) {
-      float eight[8];
-      logits<F32, 8>(row, first + i, eight);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i + e] = eight[e];
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = logit<F32>(row, min(first + e, n - 1));
-  }
+  // its logits, some in a row to a thread
+  const int first = part * kPart + kMine * tid, to = min(n, (part + 1) * kPart);
+  float v[kMine];
+  const int from = fetch<F32>(row, first, n, v);
+  const auto taken = [&](float x, int place) {
+    const uint32_t key = key_of(x);
+    return key > kNoKey && (key > cut || (key == cut && ~(uint32_t)place >= last));
+  };
   // their weights' sum
   uint64_t sum = 0;
   int final = -1;   // the last that is kept
-  const auto kept = [&](float x, int place) {
-    const uint32_t key = key_of(x);
-    return place < to && key > kNoKey && (key > cut || (key == cut && ~(uint32_t)place >= last));
-  };
 #pragma unroll 1
-  for (int i = 0; i < 16; i += 4) {
-    float four[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) four[e] = i == 0 ? v[e] : i == 4 ? v[4 + e] : i == 8 ? v[8 + e] : v[12 + e];
+  for (int i = 0; i < kMine; i += 4) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint64_t w = weight_of(four[e]);
-      const bool k = kept(four[e], first + i + e) && w;
+      const float x = i ? v[4 + e] : v[e];
+      const uint64_t w = weight_of(x);
+      const bool k = from + i + e >= first && from + i + e < to && taken(x, from + i + e) && w;
       sum += k ? w : 0;
-      final = k ? first + i + e : final;
+      final = k ? from + i + e : final;
     }
   }
-  // the thread in which the sum passes the target; where rounding at other
-  // places (of the parts' sums, of the weights) leaves none, the last kept
+  // the wave and the thread in which the sum passes the target; where
+  // rounding at other places (of the parts' sums, of the weights) leaves none,
+  // the last kept
   uint64_t at = wave_scan(sum);
   __syncthreads();
   if (lane == 63) sh.tmp[tid >> 6] = at;
@@ -969,33 +1088,31 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   at += start - sum;
 #pragma unroll 1
   for (int w = 0; w < tid >> 6; ++w) at += sh.tmp[w];
-  const bool mine = at <= target && at + sum > target;
-  if (mine) sh.found = first;
+  const uint64_t owner = __ballot(at <= target && at + sum > target);
+  if (owner && lane == 0) sh.found = 0;
   __syncthreads();
   const bool none = sh.found < 0;
+  int id = -1;
   if (none) {
     const uint64_t end = wave_max((uint32_t)(final + 1));
     if (lane == 0) sh.tmp[tid >> 6] = end;
     __syncthreads();
-    for (int w = 0; w < kRowThreads / 64; ++w) final = max(final, (int)sh.tmp[w] - 1);
-    __syncthreads();
+    for (int w = 0; w < kRowThreads / 64; ++w) id = max(id, (int)sh.tmp[w] - 1);
+    if (tid) return;
+  } else {
+    if (!owner) return;
+    // the thread's logits, one to a lane
+    const int o = __ffsll((unsigned long long)owner) - 1, place = __builtin_amdgcn_readlane(first, o) + lane;
+    const float x = logit<F32>(row, min(place, n - 1));
+    const uint64_t w = lane < kMine && place < to && taken(x, place) ? weight_of(x) : 0, up = lane_value(at, o) + wave_scan(w);
+    const uint64_t passed = __ballot(up > target);
+    id = __builtin_amdgcn_readlane(place, __ffsll((unsigned long long)passed) - 1);
+    if (lane) return;
   }
-  if (none ? tid == 0 : mine) {
-    int id = final;
-    if (!none)
-#pragma unroll 1
-      for (int e = 0; e < 16; ++e) {
-        const float x = logit<F32>(row, min(first + e, n - 1));
-        const uint64_t w = kept(x, first + e) ? weight_of(x) : 0;
-        if (w) id = first + e;
-        at += w;
-        if (at > target) break;
-      }
-    a.ids[r] = id;
-    if (a.logprobs) {
-      const double x = fma((double)logit<F32>(row, id), sc.per, -sc.power);
-      a.logprobs[r] = (float)(x * 0.69314718055994530942 - log(ldexp((double)all, -a.unit)));
-    }
+  a.ids[r] = id;
+  if (a.logprobs) {
+    const double x = fma((double)logit<F32>(row, id), sc.per, -sc.power);
+    a.logprobs[r] = (float)(x * 0.69314718055994530942 - log(ldexp((double)all, -a.unit)));
   }
 }
 
