@@ -257,7 +257,7 @@ hipError_t launch_lora(const LoraArgs &a, const LoraPlan &p, hipStream_t s);
 
 constexpr int kSamplePart = 8192;   // logits of a row that a workgroup takes at once
 constexpr int kSampleBins = 256;
-constexpr int64_t kSampleGroups = 640;
+constexpr int64_t kSampleGroups = 512;
 constexpr int32_t kFarPart = INT32_MIN;
 struct SamplePart {
   uint64_t best;                // largest key, complement of its first index
