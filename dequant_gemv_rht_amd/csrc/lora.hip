@@ -183,69 +183,156 @@ __global__ __launch_bounds__(kLoraThreads) void lora_inner_kernel(LoraArgs g) {
   });
 }
 
-// 16 neighbours of a row, at any alignment
+// A lane's 16 outputs of a row in one step of the outer product, 16 bytes
+// side by side; vector v's first is 4 V v + V q past the step's.
 template <typename T>
 struct Run {
-  T v[16];
+  static constexpr int V = 16 / sizeof(T), N = 16 / V;   // of a vector; vectors
+  T v[N][V];
 };
 
-template <typename T>
+// FULL: all 64 outputs of the step are there.  The last step of a linear may
+// lack some and goes one by one; it has code of its own, a branch for each
+// vector would keep the loads apart.
+template <bool FULL, typename T>
 __device__ __forceinline__ Run<T> load_run(const T *row, int n, int end) {
+  constexpr int V = Run<T>::V;
   Run<T> r;
-  if (n + 16 <= end) {
-    __builtin_memcpy(&r, row + n, sizeof r);
+  if constexpr (FULL) {
+#pragma unroll
+    for (int i = 0; i < Run<T>::N; ++i) __builtin_memcpy(r.v[i], row + n + 4 * V * i, 16);   // at any alignment
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) r.v[i] = n + i < end ? row[n + i] : (T)0.0f;
+    for (int i = 0; i < 16; ++i) r.v[i / V][i % V] = row[min(n + 4 * V * (i / V) + i % V, end - 1)];
   }
   return r;
 }
 
-template <typename T>
+template <bool FULL, typename T>
 __device__ __forceinline__ void store_run(T *row, int n, int end, const Run<T> &r) {
-  if (n + 16 <= end) {
-    __builtin_memcpy(row + n, &r, sizeof r);
+  constexpr int V = Run<T>::V;
+  if constexpr (FULL) {
+#pragma unroll
+    for (int i = 0; i < Run<T>::N; ++i) __builtin_memcpy(row + n + 4 * V * i, r.v[i], 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (n + i < end) row[n + i] = r.v[i];
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void copy_rows(const LoraDesc &L, const int32_t *list, int rows, int n0, int n1) {
-  if (L.y == L.base) return;
-  for (int r = 0; r < rows; ++r) {
-    const T *base = static_cast<const T *>(L.base) + list[r] * L.ldb;
-    T *y = static_cast<T *>(L.y) + list[r] * L.ldy;
-    for (int n = n0 + (int)threadIdx.x; n < n1; n += kLoraThreads) y[n] = base[n];
-  }
-}
-
-// B's part of 64 outputs from n on: instruction j's output row r is output
-// n + 16 (r / 4) + 4 j + r % 4, so that a lane ends up with 16 neighbours.
-template <int KK, bool PACK>
-__device__ __forceinline__ void load_b(const LoraDesc &L, int32_t id, int n, half8_t (&b)[4][KK]) {
-  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int at = min(n + 16 * (c >> 2) + 4 * j + (c & 3), L.n - 1);
-    const _Float16 *bp = reinterpret_cast<const _Float16 *>(L.b) + ((int64_t)id * L.n + at) * L.rank;
-#pragma unroll
-    for (int k = 0; k < KK; ++k) {
-      const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
-      b[j][k] = rank < L.rank ? *reinterpret_cast<const half8_t *>(bp + rank) : zero8();
+    for (int i = 0; i < 16; ++i) {
+      const int at = n + 4 * V * (i / V) + i % V;
+      if (at < end) row[at] = r.v[i / V][i % V];
     }
   }
 }
 
-// The outputs of one group: T base's and y's type.  KK: 32-wide steps over
-// the ranks; PACK (ranks up to 16): both parts of t in one step.
+// B's part of the 64 outputs from n on: instruction j's output row 4 q + i is
+// the output that is element 4 j + i of lane q's run.  Outputs past the last
+// repeat it and are not stored; ranks past the last repeat the last eight and
+// meet zeros in t.
+template <bool FULL, typename T, int KK, bool PACK>
+__device__ __forceinline__ void load_b(const LoraDesc &L, int32_t id, int n, half8_t (&b)[4][KK]) {
+  constexpr int V = Run<T>::V;
+  const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    int at = n + 4 * V * (4 * j / V) + V * (c >> 2) + 4 * j % V + (c & 3);
+    if (!FULL) at = min(at, L.n - 1);
+    const _Float16 *bp = reinterpret_cast<const _Float16 *>(L.b) + ((int64_t)id * L.n + at) * L.rank;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
+      b[j][k] = *reinterpret_cast<const half8_t *>(bp + min(rank, L.rank - 8));
+    }
+  }
+}
+
+// t of 16 rows (lane: row c, ranks 8 q ..) as two fp16 parts under a power of
+// two of its row: its largest in [2^13, 2^14), infinities as they are.
+template <int KK, bool PACK>
+__device__ __forceinline__ int load_parts(const LoraArgs &g, const LoraDesc &L, int32_t row,
+                                          half8_t (&parts)[KK][PACK ? 1 : 2]) {
+  const int q = (threadIdx.x & 63) >> 4, splits = (L.k / 32 + g.steps - 1) / g.steps;
+  float v[KK][8], most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < KK; ++k) {
+    const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
+    const bool has = rank < L.rank;
+    const float *t = L.t + (int64_t)row * L.rank + (has ? rank : 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
+    for (int s0 = 0; s0 < splits; s0 += 4) {   // four splits asked for at once
+      float4_t lo[4], hi[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float4_t *at = reinterpret_cast<const float4_t *>(t + (int64_t)min(s0 + s, splits - 1) * g.m * L.rank);
+        lo[s] = at[0];
+        hi[s] = at[1];
+      }
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const bool adds = has && s0 + s < splits;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[k][e] += adds ? lo[s][e] : 0.0f;
+          v[k][4 + e] += adds ? hi[s][e] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[k][e]));
+  }
+  most = fmaxf(most, __shfl_xor(most, 16));
+  most = fmaxf(most, __shfl_xor(most, 32));
+  const int power = most > 0.0f && most <= 3.4028234e38f ? 14 - __builtin_amdgcn_frexp_expf(most) : 0;
+#pragma unroll
+  for (int k = 0; k < KK; ++k) {
+    half8_t hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = ldexpf(v[k][e], power);
+      hi[e] = (_Float16)x;
+      const float rest = x - (float)hi[e];
+      lo[e] = (_Float16)(rest - rest == 0.0f ? rest : 0.0f);
+    }
+    if (PACK) {
+      parts[k][0] = q < 2 ? hi : lo;
+    } else {
+      parts[k][0] = hi;
+      parts[k][1] = lo;
+    }
+  }
+  return -power;
+}
+
+template <typename T, int KK, bool PACK>
+__device__ __forceinline__ void add_product(Run<T> &out, const half8_t (&b)[4][KK], const half8_t (&parts)[KK][PACK ? 1 : 2],
+                                            int power) {
+  constexpr int V = Run<T>::V;
+  float4_t acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < KK; ++k)
+#pragma unroll
+    for (int p = 0; p < (PACK ? 1 : 2); ++p)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j][k], parts[k][p], acc[j], 0, 0, 0);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      T &o = out.v[4 * j / V][4 * j % V + e];
+      o = (T)((float)o + ldexpf(acc[j][e], power));
+    }
+}
+
+// The outputs [n0, n1) of one group: T base's and y's type.  KK: 32-wide
+// steps over the ranks; PACK (ranks up to 16): both parts of t in one.
 template <typename T, int KK, bool PACK, int CT>
 __device__ __forceinline__ void outer_group(const LoraArgs &g, const LoraDesc &L, const int32_t *list,
-                                            half8_t (*parts)[KK][PACK ? 1 : 2][64], int32_t (*powers)[16], int32_t id, int rows,
+                                            half8_t (*shared)[KK][PACK ? 1 : 2][64], int32_t (*powers)[16], int32_t id, int rows,
                                             int n0, int n1) {
+  constexpr int V = Run<T>::V;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
+  const int full = n1 < L.n ? n1 : L.n & ~63, end = L.n, own = V * q;   // the lane's first output of a step
   int n = n0 + 64 * wave;
   const T *base[CT];
   T *y[CT];
@@ -255,98 +342,66 @@ __device__ __forceinline__ void outer_group(const LoraArgs &g, const LoraDesc &L
     base[t] = static_cast<const T *>(L.base) + row * L.ldb;
     y[t] = static_cast<T *>(L.y) + row * L.ldy;
   }
-  // B and base do not wait for t
+  if (id < 0) {
+    if (L.y == L.base) return;
+    for (; n < n1; n += 64 * kWaves)
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        if (16 * t + c >= rows) continue;
+        if (n < full)
+          store_run<true>(y[t], n + own, end, load_run<true>(base[t], n + own, end));
+        else
+          store_run<false>(y[t], n + own, end, load_run<false>(base[t], n + own, end));
+      }
+    return;
+  }
+  // B and base do not wait for t; tiles past the group's last repeat its last row
   half8_t b[4][KK];
   Run<T> out[CT];
   const auto load = [&](int at) {
-    load_b<KK, PACK>(L, id, at, b);
+    load_b<true, T, KK, PACK>(L, id, at, b);
 #pragma unroll
-    for (int t = 0; t < CT; ++t)
-      if (16 * t < rows) out[t] = load_run(base[t], at + 16 * q, at + 16 * q < n1 ? L.n : 0);
+    for (int t = 0; t < CT; ++t) out[t] = load_run<true>(base[t], at + own, end);
   };
-  if (n < n1) load(n);
+  if (n < full) load(n);
   // wave w makes the parts of the group's rows 16 w .. 16 w + 15
-  if (16 * wave < rows && wave < CT) {
-    const int32_t row = list[min(16 * wave + c, rows - 1)];
-    const int splits = (L.k / 32 + g.steps - 1) / g.steps;
-    float v[KK][8], most = 0.0f;
+  if (wave < CT && 16 * wave < rows) {
+    half8_t parts[KK][PACK ? 1 : 2];
+    const int power = load_parts<KK, PACK>(g, L, list[min(16 * wave + c, rows - 1)], parts);
+    if (q == 0) powers[wave][c] = power;
 #pragma unroll
-    for (int k = 0; k < KK; ++k) {
-      const int rank = PACK ? 8 * (q & 1) : 32 * k + 8 * q;
-      const bool has = rank < L.rank;
-      const float *t = L.t + (int64_t)row * L.rank + (has ? rank : 0);
+    for (int k = 0; k < KK; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] = 0.0f;
-      for (int s0 = 0; s0 < splits; s0 += 4) {   // four splits asked for at once
-        float4_t lo[4], hi[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float4_t *at = reinterpret_cast<const float4_t *>(t + (int64_t)min(s0 + s, splits - 1) * g.m * L.rank);
-          lo[s] = at[0];
-          hi[s] = at[1];
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const bool adds = has && s0 + s < splits;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[k][e] += adds ? lo[s][e] : 0.0f;
-            v[k][4 + e] += adds ? hi[s][e] : 0.0f;
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(v[k][e]));
-    }
-    most = fmaxf(most, __shfl_xor(most, 16));
-    most = fmaxf(most, __shfl_xor(most, 32));
-    // the row's largest into [2^13, 2^14); infinities as they are
-    const int power = most > 0.0f && most <= 3.4028234e38f ? 14 - __builtin_amdgcn_frexp_expf(most) : 0;
-    if (q == 0) powers[wave][c] = -power;
-#pragma unroll
-    for (int k = 0; k < KK; ++k) {
-      half8_t hi, lo;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float x = ldexpf(v[k][e], power);
-        hi[e] = (_Float16)x;
-        const float rest = x - (float)hi[e];
-        lo[e] = (_Float16)(rest - rest == 0.0f ? rest : 0.0f);
-      }
-      if (PACK) {
-        parts[wave][k][0][lane] = q < 2 ? hi : lo;
-      } else {
-        parts[wave][k][0][lane] = hi;
-        parts[wave][k][1][lane] = lo;
-      }
-    }
+      for (int p = 0; p < (PACK ? 1 : 2); ++p) shared[wave][k][p][lane] = parts[k][p];
   }
   __syncthreads();
-  for (; n < n1;) {
-    const int mine = n + 16 * q, end = mine < n1 ? L.n : 0;
+  const auto add = [&](int t) {
+    half8_t parts[KK][PACK ? 1 : 2];
+#pragma unroll
+    for (int k = 0; k < KK; ++k)
+#pragma unroll
+      for (int p = 0; p < (PACK ? 1 : 2); ++p) parts[k][p] = shared[t][k][p][lane];
+    add_product<T, KK, PACK>(out[t], b, parts, powers[t][c]);
+  };
+  while (n < full) {
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       if (16 * t >= rows) break;
-      float4_t acc[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int k = 0; k < KK; ++k)
-#pragma unroll
-        for (int p = 0; p < (PACK ? 1 : 2); ++p) {
-          const half8_t part = parts[t][k][p][lane];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[j][k], part, acc[j], 0, 0, 0);
-        }
-      const int power = powers[t][c];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[t].v[4 * j + e] = (T)((float)out[t].v[4 * j + e] + ldexpf(acc[j][e], power));
-      if (16 * t + c < rows) store_run(y[t], mine, end, out[t]);
+      add(t);
+      if (16 * t + c < rows) store_run<true>(y[t], n + own, end, out[t]);
     }
     n += 64 * kWaves;
-    if (n < n1) load(n);
+    if (n < full) load(n);
+  }
+  if (n < n1) {
+    load_b<false, T, KK, PACK>(L, id, n, b);
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+      if (16 * t >= rows) break;
+      out[t] = load_run<false>(base[t], n + own, end);
+      add(t);
+      if (16 * t + c < rows) store_run<false>(y[t], n + own, end, out[t]);
+    }
   }
 }
 
@@ -361,16 +416,10 @@ __global__ __launch_bounds__(kLoraThreads) void lora_outer_kernel(LoraArgs g) {
   if (n0 >= L.n) return;
   const int n1 = min(n0 + g.chunk, L.n);
   for_groups<WHOLE, CT>(g, L.count, list, masks, [&](int32_t id, int rows) {
-    if (id < 0) {
-      if (L.f32)
-        copy_rows<float>(L, list, rows, n0, n1);
-      else
-        copy_rows<_Float16>(L, list, rows, n0, n1);
-    } else if (L.f32) {
+    if (L.f32)
       outer_group<float, KK, PACK, CT>(g, L, list, parts, powers, id, rows, n0, n1);
-    } else {
+    else
       outer_group<_Float16, KK, PACK, CT>(g, L, list, parts, powers, id, rows, n0, n1);
-    }
   });
 }
 
