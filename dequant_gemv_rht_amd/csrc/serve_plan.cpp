@@ -6,7 +6,8 @@ namespace wq {
 
 namespace {
 
-constexpr int64_t kWork = 2048;   // workgroups that K and the outputs are cut for
+constexpr int64_t kWork = 2048;   // workgroups that K and the outputs of up to kWholeRows rows are cut for
+constexpr int64_t kLongWork = 768, kLongSplits = 4;
 
 // the smallest multiple of `unit` in which `pieces`, cut, make at most kWork
 // workgroups for each `tiles`, and at most `most` of the longest piece
@@ -23,6 +24,13 @@ int64_t cut(int32_t count, const wq_adapters *w, int64_t wq_adapters::*length, i
   return (piece + unit - 1) / unit * unit;
 }
 
+// splits of K in a long call, for three workgroups a CU (their LDS fits): 4001
+// rows, three projections, rank 64: 30 us with one, 27 with two
+int32_t splits_for(int64_t tiles) {
+  const int64_t s = kLongWork / tiles;
+  return (int32_t)(s < 1 ? 1 : s > kLongSplits ? kLongSplits : s);
+}
+
 }  // namespace
 
 LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
@@ -37,7 +45,13 @@ LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
     k = w[i].k > k ? w[i].k : k;
     p.rank = w[i].rank > p.rank ? w[i].rank : p.rank;
   }
-  const int64_t piece = p.whole ? cut(count, w, &wq_adapters::k, m, 128, kLoraSplits) : k;
+  int64_t piece;
+  if (p.whole) {
+    piece = cut(count, w, &wq_adapters::k, m, 128, kLoraSplits);
+  } else {
+    const int64_t splits = splits_for(p.inner_tiles * count);
+    piece = ((k + splits - 1) / splits + 255) / 256 * 256;
+  }
   p.steps = (int32_t)(piece / 32);
   p.splits = (int32_t)((k + piece - 1) / piece);
   p.chunk = (int32_t)cut(count, w, &wq_adapters::n, p.outer_tiles, 256, INT32_MAX);
@@ -46,8 +60,11 @@ LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
 }
 
 size_t lora_workspace(const wq_adapters &w, int64_t m) {
-  const int64_t rows = (m <= kWholeRows ? m : kWholeRows) * kLoraSplits;
-  const size_t bytes = (size_t)(rows > m ? rows : m) * (size_t)w.rank * sizeof(float);
+  // a bound of splits * m that grows with m: in a long call splits is at most
+  // kLongSplits, and at most kLongWork over a 32nd of m
+  const int64_t whole = (m <= kWholeRows ? m : kWholeRows) * kLoraSplits;
+  const int64_t most = kLongSplits * m, filled = m + 32 * kLongWork, longer = most < filled ? most : filled;
+  const size_t bytes = (size_t)(m <= kWholeRows || whole > longer ? whole : longer) * (size_t)w.rank * sizeof(float);
   return (bytes + 255) / 256 * 256;
 }
 
