@@ -16,7 +16,7 @@
 // sum of what is kept; the part in which the sum passes u times all of it is
 // read again, token by token.  Rows for which that does not do (a cut below
 // the bins, more logits in its bin than fit in LDS, logits beyond 2^13 powers
-// of two) are searched in as many passes as it takes.
+// of two, temperatures near infinity) are searched in as many passes as it takes.
 //
 // The second launch runs once through its code, most of which then comes from
 // the L2 line by line: loops there stay rolled, each piece of work has one
@@ -114,40 +114,49 @@ __device__ __forceinline__ Settings settings(const SampleArgs &a, int64_t r) {
   return s;
 }
 
-// Weights by powers of two: x = l log2(e) / T - power, w = 2^x.  x is split
-// at 1024ths: a table of 2^(j / 1024), and 2^g = 1 + e, |g| <= 2^-11, where e
-// in fp32 is 2^-35 of w off.
+// Weights by powers of two: x = l log2(e) / T - power, w = 2^x.  One fp64
+// multiply-add leaves x in 2^-40s in the low bits of its result, from which
+// whole powers, 1024ths (a table of 2^(j / 1024)) and the rest g are cut;
+// 2^g = 1 + e, g < 2^-10, where e in fp32 is 2^-34 of w off.
 struct Scale {
   double per;                  // log2(e) / T
   double power;                // a whole number
   int unit;
+  double shift;                // 1.5 2^12 - power: 2^-40s are its last bit
+  float lowest;                // logits below it count as it: x about -1000
 };
 
+constexpr uint32_t kShiftHigh = 0x40B80000u;   // the upper half of 1.5 2^12
+
+__device__ __forceinline__ Scale scale(double per, double power, int unit) {
+  const double lowest = (power - 1000.0) / per;
+  return {per, power, unit, 6144.0 - power, (float)(lowest > -3.4e38 ? lowest : -3.4e38)};
+}
+
+// What scale() is for: x of the largest logit, and of -infinity's stand-in, in
+// the range of the low bits.
+__device__ __forceinline__ bool near(double per, double most) { return fabs(most) < kFar && per > 1e-30; }
+
 struct Split {
-  double x;
-  int i;                       // 1024 x, rounded
-  float g;                     // x - i / 1024
+  uint32_t hi, lo;
 };
 
 __device__ __forceinline__ Split split(float l, const Scale &s) {
-  constexpr double kMagic = 6755399441055744.0;   // 1.5 2^52: adding it rounds to whole numbers
-  Split p;
-  p.x = fmax(fma((double)l, s.per, -s.power), -1000.0);   // NaN and -infinity count as nothing too
-  const double q = fma(p.x, 1024.0, kMagic);
-  p.i = (int)(uint32_t)__builtin_bit_cast(uint64_t, q);
-  p.g = (float)fma(q - kMagic, -1.0 / 1024.0, p.x);
-  return p;
+  const uint64_t q = __builtin_bit_cast(uint64_t, fma((double)fmaxf(l, s.lowest), s.per, s.shift));   // (not NaN)
+  return {(uint32_t)(q >> 32), (uint32_t)q};
 }
 
 __device__ __forceinline__ uint64_t counted(const Split &p, const Scale &s, const double *table) {
-  const float t = p.g * 0.69314718f, e = t * fmaf(t, fmaf(t, 0.16666667f, 0.5f), 1.0f);
-  const double w = table[p.i & (kTable - 1)];
-  const double c = ldexp(fma(w, (double)e, w), (p.i >> 10) + s.unit) + 4503599627370496.0;   // 2^52: whole numbers
+  constexpr float kLn2 = 6.3041364e-13f;   // ln 2 / 2^40
+  const float g = (float)(p.lo & 0x3FFFFFFFu), e = g * fmaf(g, fmaf(g, kLn2 * kLn2 * kLn2 / 6.0f, kLn2 * kLn2 / 2.0f), kLn2);
+  const double w = table[__builtin_amdgcn_alignbit(p.hi, p.lo, 30) & (kTable - 1)];
+  const int power = ((int)(p.hi - kShiftHigh) >> 8) + s.unit;
+  const double c = ldexp(fma(w, (double)e, w), power) + 4503599627370496.0;   // 2^52: whole numbers
   return __builtin_bit_cast(uint64_t, c) - 0x4330000000000000ull;
 }
 
-// 0: the largest (x from 7 / 8 on); eighths of a power of two
-__device__ __forceinline__ int bin_of(const Split &p) { return 8 - (p.i >> 7); }
+// Eighths of a power of two: 0 and 1 are the largest's
+__device__ __forceinline__ int bin_of(const Split &p) { return 8 - ((int)(p.hi - kShiftHigh) >> 5); }
 
 __device__ __forceinline__ double table_entry(int j) { return exp64((double)j * (0.69314718055994530942 / kTable)); }
 
@@ -256,14 +265,11 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
         if (v[i] == most) top = __builtin_bit_cast(float, (i / V * kPartThreads + tid) * V + i % V);
       atomicMin(&sh.where, __builtin_bit_cast(uint32_t, top));
     }
-    Scale sc;
-    sc.per = 1.4426950408889634074 / (double)s.heat;
-    sc.unit = a.unit;
-    const double power = (double)most * sc.per;
-    const bool near = !s.greedy && most > -INFINITY && fabs(power) < kFar;
-    sc.power = floor(power);
+    const double per = 1.4426950408889634074 / (double)s.heat, power = (double)most * per;
+    const bool counts_in = !s.greedy && most > -INFINITY && near(per, power);
+    const Scale sc = scale(per, floor(power), a.unit);
     if (item + (int)gridDim.x < items) fetch(item + gridDim.x, next, next_s);
-    if (near) {
+    if (counts_in) {
       uint64_t sum = 0;
       const bool counts = s.top_k < a.vocab;
       // eight at a time: a table entry of one waits behind the sums of none
@@ -302,14 +308,14 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
         SamplePart head;
         head.best = (uint64_t)key_of(most) << 32 | (uint32_t)~((item - r * a.parts) * kPart + sh.where);
         head.sum = sh.sum;
-        head.power = near ? (int32_t)sc.power : kFarPart;   // far: no bins
+        head.power = counts_in ? (int32_t)sc.power : kFarPart;   // no bins
         head.finite = sh.finite;
         a.heads[item] = head;
         sh.sum = 0;
         sh.finite = 0;
         sh.where = 0xFFFFFFFFu;
       }
-      if (near && s.cuts) {
+      if (counts_in && s.cuts) {
         // sums up to and with each bin, four a lane
         uint64_t up[4];
         uint32_t many[4];
@@ -667,14 +673,11 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   static_assert(kTable == kRowThreads, "an entry a thread");
   if (tid < kBins) sh.sums[tid] = sh.counts[tid] = 0;
   __syncthreads();
-  Scale sc;
-  sc.per = 1.4426950408889634074 / (double)set.heat;
-  sc.unit = a.unit;
-  const double most = (double)value_of(top) * sc.per;
-  sc.power = floor(most);
+  const double per = 1.4426950408889634074 / (double)set.heat, most = (double)value_of(top) * per;
+  const Scale sc = scale(per, floor(most), a.unit);
   // as the first launch counted it: borders of equal weights are exact
   const auto weight_of = [&](float l) { return counted(split(l, sc), sc, sh.table); };
-  bool passes = !(fabs(most) < kFar);
+  bool passes = !near(per, most);
 
   // what is kept: keys above `cut`, and of those at it the ones whose index's
   // complement is `last` or more; all of the bins before `bin` and, in the
@@ -816,7 +819,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         float from_value = 0.0f, to_value = 0.0f;
 #pragma unroll 1
         for (int edge = 0; edge < 2; ++edge) {
-          const uint32_t guess = key_of((float)(((double)(8 - at + edge) * 0.125 - 1.0 / 2048.0 + sc.power) / sc.per));
+          const uint32_t guess = key_of((float)(((double)(8 - at + edge) * 0.125 + sc.power) / sc.per));
           uint32_t no = kNoKey, yes = top + 1;
 #pragma unroll 1
           for (int turn = 0; yes - no > 1; ++turn) {
