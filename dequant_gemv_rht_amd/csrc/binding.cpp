@@ -378,6 +378,14 @@ PyObject *tuple_of(at::Tensor *t, Py_ssize_t n) {
   return r.release();
 }
 
+// the n elements of a new vector from `from` on (a view without the dispatcher's cost)
+at::Tensor part_of(const at::Tensor &whole, int64_t from, int64_t n) {
+  auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+  impl->set_sizes_contiguous(at::IntArrayRef(&n, 1));
+  impl->set_storage_offset(from);
+  return at::Tensor(std::move(impl));
+}
+
 // kv_slots(page_size, pages, table, lens, new_tokens, free_pages, used, tokens, out): out None or six tensors
 PyObject *kv_slots(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -407,8 +415,14 @@ PyObject *kv_slots(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!given) throw python_error();
     TORCH_CHECK_VALUE(PyTuple_GET_SIZE(given.get()) == 6, "out must be six tensors");
   }
+  int64_t total = 0, from[6];
   for (int i = 0; i < 6; ++i) {
-    out[i] = given ? tensor(PyTuple_GET_ITEM(given.get(), i), names[i]) : p.make({sizes[i]}, at::kInt);
+    from[i] = total;
+    total += (sizes[i] + 3) / 4 * 4;
+  }
+  const at::Tensor whole = given ? at::Tensor() : p.make({total}, at::kInt);   // new outputs share one allocation
+  for (int i = 0; i < 6; ++i) {
+    out[i] = given ? tensor(PyTuple_GET_ITEM(given.get(), i), names[i]) : part_of(whole, from[i], sizes[i]);
     po[i] = static_cast<int32_t *>(vec(p, out[i], at::kInt, sizes[i], names[i]));
   }
   const wq_status st = slots_fn((int32_t)page_size, pages, static_cast<int32_t *>(table.data_ptr()),

@@ -19,26 +19,44 @@ constexpr int kSlotThreads = 256;
 constexpr int kItems = 4;                    // sequences, and rows, of a thread
 constexpr int kRows = kSlotThreads * kItems;
 
-// exclusive sums of v over the workgroup's threads, and the total
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sums, int64_t &total) {
+constexpr int kWaves = kSlotThreads / 64;
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
+}
+
+// f over the lanes up to this one: within rows of 16 lanes, then the row
+// before's last to rows 1 and 3, then lane 31's to rows 2 and 3
+template <typename F>
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t none, F f) {
+  v = f(v, moved<0x111, 0xF>(v, none));
+  v = f(v, moved<0x112, 0xF>(v, none));
+  v = f(v, moved<0x114, 0xF>(v, none));
+  v = f(v, moved<0x118, 0xF>(v, none));
+  v = f(v, moved<0x142, 0xA>(v, none));
+  return f(v, moved<0x143, 0xC>(v, none));
+}
+
+// Sums that stop at `most` (so that they stay in 32 bits), over the threads
+// before this one and over all, on top of `so_far`.  Every call has a `sums`
+// of its own until the next barrier but one.
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t most, uint32_t *sums, uint32_t &so_far) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t up = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(up, d);
-    if (lane >= d) up += o;
-  }
-  __syncthreads();   // the last use of sums is over
+  const auto add = [&](uint32_t a, uint32_t b) { return min(a + b, most); };
+  const uint32_t up = wave_scan(v, 0, add);
   if (lane == 63) sums[wave] = up;
   __syncthreads();
-  int64_t before = up - v;
-  total = 0;
+  uint32_t before = so_far, all = so_far;
 #pragma unroll
-  for (int w = 0; w < kSlotThreads / 64; ++w) {
-    if (w < wave) before += sums[w];
-    total += sums[w];
+  for (int w = 0; w < kWaves; ++w) {
+    const uint32_t s = sums[w];
+    if (w < wave) before = add(before, s);
+    all = add(all, s);
   }
-  return before;
+  so_far = all;
+  const uint32_t left = moved<0x138, 0xF>(up, 0);   // the lane before's
+  return add(before, lane ? left : 0);
 }
 
 struct Record {
@@ -49,16 +67,21 @@ struct Record {
 };
 
 __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotsArgs a) {
-  __shared__ int64_t sums[kSlotThreads / 64];
+  __shared__ uint32_t sums[4][kWaves];
   __shared__ Record rec[kRows];
-  __shared__ int32_t mark[kRows], tops[kSlotThreads / 64];
+  __shared__ alignas(16) int32_t mark[kRows];
+  __shared__ int32_t tops[kWaves];
   const int tid = threadIdx.x;
-  const int64_t row0 = (int64_t)blockIdx.x * kRows, row1 = row0 + kRows < a.tokens ? row0 + kRows : a.tokens;
+  const uint32_t row0 = blockIdx.x * kRows, row1 = min(row0 + kRows, (uint32_t)a.tokens);
   const int32_t used = *a.used, mask = (1 << a.page_shift) - 1;
-  const int64_t room = used >= 0 && used <= a.free_count ? a.free_count - used : 0;
-  for (int i = tid; i < kRows; i += kSlotThreads) mark[i] = -1;
+  const uint32_t room = used >= 0 && used <= a.free_count ? a.free_count - used : 0;
+#pragma unroll
+  for (int e = 0; e < kItems; ++e) mark[tid * kItems + e] = -1;
 
-  int64_t rows = 0, need_sum = 0, taken = 0;   // before the turn; pages given out
+  // before the turn: rows, up to one more than the step has, and pages (each
+  // page counted has a row, or there would be no room for it)
+  uint32_t rows = 0, asked = 0, taken = 0;
+  const uint32_t most = (uint32_t)a.tokens + 1;
   const int turns = (a.seqs + kRows - 1) / kRows;
   // turn t's sequences are written by workgroup t % gridDim, used_out by the
   // last turn's; a workgroup stops after its last such turn once the rows are
@@ -69,35 +92,35 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotsArgs a) {
     if (rows >= row1 && t > until) break;
     const bool writes = t % grid == group;
     int32_t len[kItems], add[kItems];
-    int64_t mine = 0;
+    uint32_t mine = 0;
 #pragma unroll
     for (int e = 0; e < kItems; ++e) {
-      const int64_t s = (int64_t)t * kRows + tid * kItems + e;
+      const int s = t * kRows + tid * kItems + e;
       len[e] = s < a.seqs ? a.lens[s] : 0;
       add[e] = s < a.seqs ? a.new_tokens[s] : 0;
-      if (add[e] < 0) add[e] = 0;
-      mine += add[e];
     }
-    int64_t total;
-    int64_t begin = rows + block_scan(mine, sums, total);
-    rows += total;
+#pragma unroll
+    for (int e = 0; e < kItems; ++e) {
+      if (add[e] < 0) add[e] = 0;
+      mine = min(mine + (uint32_t)add[e], most);
+    }
+    uint32_t begin = block_scan(mine, most, sums[2 * (t & 1)], rows);
     int32_t need[kItems], held[kItems];
     bool fits[kItems];
-    int64_t at = begin, pages = 0;
+    uint32_t at = begin, pages = 0;
 #pragma unroll
     for (int e = 0; e < kItems; ++e) {
       const int64_t l = len[e] > 0 ? len[e] : 0, to = l + add[e];
-      at += add[e];
+      at = min(at + (uint32_t)add[e], most);
       held[e] = (int32_t)((l + mask) >> a.page_shift);
-      fits[e] = at <= a.tokens && to <= ((int64_t)a.table_pages << a.page_shift);
+      fits[e] = at < most && to <= ((int64_t)a.table_pages << a.page_shift);
       need[e] = fits[e] ? (int32_t)((to + mask) >> a.page_shift) - held[e] : 0;
       pages += need[e];
     }
-    int64_t place = need_sum + block_scan(pages, sums, total);
-    need_sum += total;
+    uint32_t place = block_scan(pages, 0x7FFFFFFFu, sums[2 * (t & 1) + 1], asked);
 #pragma unroll
     for (int e = 0; e < kItems; ++e) {
-      const int64_t s = (int64_t)t * kRows + tid * kItems + e;
+      const int s = t * kRows + tid * kItems + e;
       const bool served = fits[e] && (need[e] == 0 || place + need[e] <= room);
       if (s < a.seqs) {
         if (served && need[e]) taken = place + need[e];
@@ -106,31 +129,28 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotsArgs a) {
           a.last[s] = served && add[e] ? (int32_t)(begin + add[e] - 1) : -1;
         }
         // its first row here, if it has one
-        const int64_t first = begin > row0 ? begin : row0;
-        if (add[e] && first < row1 && begin + add[e] > row0) {
+        const uint32_t first = max(begin, row0);
+        if (add[e] && first < row1 && min(begin + (uint32_t)add[e], most) > row0) {
           const int i = (int)(first - row0);
           mark[i] = i;
-          rec[i] = {served ? (int32_t)s : -1, (int32_t)((len[e] > 0 ? len[e] : 0) - begin), held[e],
-                    served ? (int32_t)(used + place) : 0};
+          rec[i] = {served ? s : -1, (int32_t)((uint32_t)(len[e] > 0 ? len[e] : 0) - begin), held[e],
+                    served ? (int32_t)((uint32_t)used + place) : 0};
         }
       }
-      begin += add[e];
+      begin = min(begin + (uint32_t)add[e], most);
       place += need[e];
     }
   }
   // what the last served sequence took: places only grow
   if ((turns ? turns - 1 : 0) % grid == group) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int64_t o = __shfl_xor(taken, d);
-      taken = o > taken ? o : taken;
-    }
+    const uint32_t top = wave_scan(taken, 0, [](uint32_t x, uint32_t y) { return max(x, y); });
     __syncthreads();
-    if ((tid & 63) == 0) sums[tid >> 6] = taken;
+    if ((tid & 63) == 63) sums[0][tid >> 6] = top;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kSlotThreads / 64; ++w) taken = sums[w] > taken ? sums[w] : taken;
-      *a.used_out = (int32_t)(used + taken);
+      taken = sums[0][0];
+      for (int w = 1; w < kWaves; ++w) taken = max(taken, sums[0][w]);
+      *a.used_out = (int32_t)((uint32_t)used + taken);
     }
   }
   __syncthreads();
@@ -142,27 +162,23 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotsArgs a) {
     top = m > top ? m : top;
     r[e] = top;
   }
-  int32_t up = top;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int32_t o = __shfl_up(up, d);
-    if ((tid & 63) >= d && o > up) up = o;
-  }
-  if ((tid & 63) == 63) tops[tid >> 6] = up;
-  int32_t before = __shfl_up(up, 1);
-  if ((tid & 63) == 0) before = -1;
+  const auto later = [](uint32_t x, uint32_t y) { return (uint32_t)max((int32_t)x, (int32_t)y); };
+  const uint32_t up = wave_scan((uint32_t)top, 0xFFFFFFFFu, later);
+  if ((tid & 63) == 63) tops[tid >> 6] = (int32_t)up;
+  const int32_t left = (int32_t)moved<0x138, 0xF>(up, 0xFFFFFFFFu);
+  int32_t before = tid & 63 ? left : -1;
   __syncthreads();
-  for (int w = 0; w < tid >> 6; ++w) before = tops[w] > before ? tops[w] : before;
+  for (int w = 0; w < tid >> 6; ++w) before = max(before, tops[w]);
 #pragma unroll
   for (int e = 0; e < kItems; ++e) {
-    const int64_t row = row0 + tid * kItems + e;
+    const uint32_t row = row0 + tid * kItems + e;
     if (row >= row1) break;
     const int32_t i = r[e] > before ? r[e] : before;
     int32_t slot = -1, pos = -1, seq = -1;
     if (i >= 0 && row < rows && rec[i].seq >= 0) {
       const Record c = rec[i];
       seq = c.seq;
-      pos = (int32_t)(row + c.shift);
+      pos = (int32_t)(row + (uint32_t)c.shift);
       const int32_t index = pos >> a.page_shift;
       int32_t *entry = a.table + seq * a.ld_table + index;
       int32_t page;
