@@ -12,6 +12,7 @@
 #include "wq_internal.h"
 
 namespace wq {
+using namespace dev;
 
 namespace {
 
@@ -21,30 +22,13 @@ constexpr int kRows = kSlotThreads * kItems;
 
 constexpr int kWaves = kSlotThreads / 64;
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xF, false);
-}
-
-// f over the lanes up to this one: within rows of 16 lanes, then the row
-// before's last to rows 1 and 3, then lane 31's to rows 2 and 3
-template <typename F>
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t none, F f) {
-  v = f(v, moved<0x111, 0xF>(v, none));
-  v = f(v, moved<0x112, 0xF>(v, none));
-  v = f(v, moved<0x114, 0xF>(v, none));
-  v = f(v, moved<0x118, 0xF>(v, none));
-  v = f(v, moved<0x142, 0xA>(v, none));
-  return f(v, moved<0x143, 0xC>(v, none));
-}
-
 // Sums that stop at `most` (so that they stay in 32 bits), over the threads
 // before this one and over all, on top of `so_far`.  Every call has a `sums`
 // of its own until the next barrier but one.
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t most, uint32_t *sums, uint32_t &so_far) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const auto add = [&](uint32_t a, uint32_t b) { return min(a + b, most); };
-  const uint32_t up = wave_scan(v, 0, add);
+  const uint32_t up = wave_scan(v, 0u, add);
   if (lane == 63) sums[wave] = up;
   __syncthreads();
   uint32_t before = so_far, all = so_far;
@@ -55,8 +39,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t most, uint32
     all = add(all, s);
   }
   so_far = all;
-  const uint32_t left = moved<0x138, 0xF>(up, 0);   // the lane before's
-  return add(before, lane ? left : 0);
+  return add(before, lane_before(up, 0));
 }
 
 struct Record {
@@ -143,7 +126,7 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotsArgs a) {
   }
   // what the last served sequence took: places only grow
   if ((turns ? turns - 1 : 0) % grid == group) {
-    const uint32_t top = wave_scan(taken, 0, [](uint32_t x, uint32_t y) { return max(x, y); });
+    const uint32_t top = wave_scan(taken, 0u, [](uint32_t x, uint32_t y) { return max(x, y); });
     __syncthreads();
     if ((tid & 63) == 63) sums[0][tid >> 6] = top;
     __syncthreads();
@@ -165,8 +148,7 @@ __global__ __launch_bounds__(kSlotThreads) void kv_slots_kernel(SlotsArgs a) {
   const auto later = [](uint32_t x, uint32_t y) { return (uint32_t)max((int32_t)x, (int32_t)y); };
   const uint32_t up = wave_scan((uint32_t)top, 0xFFFFFFFFu, later);
   if ((tid & 63) == 63) tops[tid >> 6] = (int32_t)up;
-  const int32_t left = (int32_t)moved<0x138, 0xF>(up, 0xFFFFFFFFu);
-  int32_t before = tid & 63 ? left : -1;
+  int32_t before = (int32_t)lane_before(up, 0xFFFFFFFFu);
   __syncthreads();
   for (int w = 0; w < tid >> 6; ++w) before = max(before, tops[w]);
 #pragma unroll

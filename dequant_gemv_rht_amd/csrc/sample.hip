@@ -160,19 +160,6 @@ __device__ __forceinline__ int bin_of(const Split &p) { return 8 - ((int)(p.hi -
 
 __device__ __forceinline__ double table_entry(int j) { return exp64((double)j * (0.69314718055994530942 / kTable)); }
 
-template <int THREADS, typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, T *tmp, F f) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = f(v, __shfl_xor(v, d));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
-  __syncthreads();
-  T r = tmp[0];
-#pragma unroll
-  for (int w = 1; w < THREADS / 64; ++w) r = f(r, tmp[w]);
-  return r;
-}
-
 struct Larger {
   template <typename T>
   __device__ T operator()(T a, T b) const { return a > b ? a : b; }
@@ -181,6 +168,12 @@ struct Sum {
   template <typename T>
   __device__ T operator()(T a, T b) const { return a + b; }
 };
+
+// over a wave, in every lane
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) { return lane_value(wave_scan(v, (T)0, Sum()), 63); }
+template <typename T>
+__device__ __forceinline__ T wave_max(T v) { return lane_value(wave_scan(v, (T)0, Larger()), 63); }
 
 // ---------------------------------------------------------------- parts
 
@@ -291,8 +284,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
             if (counts) atomicAdd(&sh.counts[bin_of(p[e])], 1u);
           }
       }
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+      sum = wave_sum(sum);
       if (lane == 0) atomicAdd(&sh.sum, (unsigned long long)sum);
     }
     if (!s.greedy && s.top_k < a.vocab) {
@@ -327,17 +319,8 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
           sh.counts[4 * lane + e] = 0;
         }
         static_assert(kBins == 256, "four a lane");
-        uint64_t all = up[3];
-        uint32_t all_many = many[3];
-#pragma unroll 1
-        for (int d = 1; d < 64; d <<= 1) {
-          const uint64_t o = __shfl_up(all, d);
-          const uint32_t c = __shfl_up(all_many, d);
-          if (lane >= d) {
-            all += o;
-            all_many += c;
-          }
-        }
+        uint64_t all = wave_scan(up[3], (uint64_t)0, Sum());
+        uint32_t all_many = wave_scan(many[3], 0u, Sum());
         all -= up[3];
         all_many -= many[3];
 #pragma unroll
@@ -360,20 +343,27 @@ constexpr int kMine = kPart / kRowThreads;   // logits of a part to a thread
 static_assert(kMine == 8, "");
 constexpr int kList = 8192;                  // logits of a cut's bin, at most
 
-// the sum of v over the threads before this one
+// the sum of v over the threads before this one, and over all
 __device__ __forceinline__ uint64_t block_before(uint64_t v, uint64_t *tmp) {
-  uint64_t up = v;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = __shfl_up(up, d);
-    if ((int)(threadIdx.x & 63) >= d) up += o;
-  }
+  const uint64_t up = wave_scan(v, (uint64_t)0, Sum());
   __syncthreads();
   if ((threadIdx.x & 63) == 63) tmp[threadIdx.x >> 6] = up;
   __syncthreads();
   uint64_t before = up - v;
+#pragma unroll 1
   for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) before += tmp[w];
   return before;
+}
+
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *tmp) {
+  const uint64_t sum = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  uint64_t all = 0;
+#pragma unroll 1
+  for (int w = 0; w < kRowThreads / 64; ++w) all += tmp[w];
+  return all;
 }
 
 constexpr int kSlowBins = 2048;
@@ -495,7 +485,7 @@ __device__ __forceinline__ void sample_passes(const SampleArgs &a, int64_t r, co
     each_key<F32>(row, 0, n, [&](uint32_t key) {
       if (key > cut) sum += counted(weight(key, s), s);
     });
-    const uint64_t over = block_reduce<kRowThreads>(sum, sh.tmp, Sum());
+    const uint64_t over = block_sum(sum, sh.tmp);
     const uint64_t tie = counted(weight(cut, s), s), all = over + ties * tie;
     // kept are those before which less than p * all lies
     uint64_t want = (uint64_t)ceil((double)set.top_p * (double)all);
@@ -526,11 +516,8 @@ __device__ __forceinline__ void sample_passes(const SampleArgs &a, int64_t r, co
         if (w >= set.at_least) sum += counted(w, s);
       }
     });
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      sum += __shfl_xor(sum, d);
-      same += __shfl_xor(same, d);
-    }
+    sum = wave_sum(sum);
+    same = wave_sum(same);
     if ((tid & 63) == 0) {
       if (sum) atomicAdd(&sh.slow.sums[t], (unsigned long long)sum);
       if (same) atomicAdd(&sh.slow.ties[t], same);
@@ -591,39 +578,6 @@ __device__ __forceinline__ void sample_passes(const SampleArgs &a, int64_t r, co
 }
 
 // ---- by the parts' bins
-
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll 1
-  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-
-template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
-#pragma unroll 1
-  for (int d = 32; d; d >>= 1) {
-    const T o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
-}
-
-// the sum of v over the lanes up to this one
-__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll 1
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
-  return v;
-}
-
-__device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane) {
-  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
-         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
-}
 
 // kMine logits of a thread, from `first` on; where fewer are left, those up to
 // the row's end: the first of them is at the place returned, and those before
@@ -974,7 +928,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
           uint64_t up[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) up[e] = sh.digits[4 * lane + e] + (e ? up[e - 1] : 0);
-          const uint64_t before = more + wave_scan(up[3]) - up[3];
+          const uint64_t before = more + wave_scan(up[3], (uint64_t)0, Sum()) - up[3];
           const uint64_t there = __ballot(before + up[3] >= want);
           __syncthreads();
           if (!there) {
@@ -1049,8 +1003,8 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   }
   // the part in which the sum passes the target
   uint64_t up[2], start = 0;
-  up[0] = wave_scan(whole[0]);
-  up[1] = parts > 64 ? lane_value(up[0], 63) + wave_scan(whole[1]) : 0;
+  up[0] = wave_scan(whole[0], (uint64_t)0, Sum());
+  up[1] = parts > 64 ? lane_value(up[0], 63) + wave_scan(whole[1], (uint64_t)0, Sum()) : 0;
   all = lane_value(parts > 64 ? up[1] : up[0], 63);
   uint64_t target = (uint64_t)floor(set.u * (double)all);
   if (target >= all) target = all - 1;
@@ -1083,7 +1037,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   // the wave and the thread in which the sum passes the target; where
   // rounding at other places (of the parts' sums, of the weights) leaves none,
   // the last kept
-  uint64_t at = wave_scan(sum);
+  uint64_t at = wave_scan(sum, (uint64_t)0, Sum());
   __syncthreads();
   if (lane == 63) sh.tmp[tid >> 6] = at;
   if (tid == 0) sh.found = -1;
@@ -1107,7 +1061,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     // the thread's logits, one to a lane
     const int o = __ffsll((unsigned long long)owner) - 1, place = __builtin_amdgcn_readlane(first, o) + lane;
     const float x = logit<F32>(row, min(place, n - 1));
-    const uint64_t w = lane < kMine && place < to && taken(x, place) ? weight_of(x) : 0, up = lane_value(at, o) + wave_scan(w);
+    const uint64_t w = lane < kMine && place < to && taken(x, place) ? weight_of(x) : 0, up = lane_value(at, o) + wave_scan(w, (uint64_t)0, Sum());
     const uint64_t passed = __ballot(up > target);
     id = __builtin_amdgcn_readlane(place, __ffsll((unsigned long long)passed) - 1);
     if (lane) return;
