@@ -820,27 +820,22 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
 #pragma unroll
               for (int e = 0; e < kMine; ++e) v[e] = from + e >= first ? v[e] : NAN;   // another thread's
             }
-            uint64_t in[kMine];   // lanes
-            uint32_t many = 0;
+            uint32_t some = 0;
 #pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-              in[e] = __ballot(v[e] >= from_value && v[e] < to_value);
-              many += (uint32_t)__popcll(in[e]);
-            }
-            if (!many) continue;
-            uint32_t to = 0;
-            if (lane == 0) to = atomicAdd(&sh.list_size, many);
-            to = (uint32_t)__builtin_amdgcn_readfirstlane((int)to);
-#pragma unroll
-            for (int e = 0; e < kMine; ++e) {
-              if (!in[e]) continue;
-              const uint32_t i = to + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[e] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[e], 0));
-              if ((in[e] >> lane & 1) && i < (uint32_t)kList) {
-                // (the key later)
-                sh.list.keys[i] = __builtin_bit_cast(uint32_t, v[e]);
-                sh.list.places[i] = (uint32_t)(from + e);
+            for (int e = 0; e < kMine; ++e) some |= v[e] >= from_value && v[e] < to_value ? 1u << e : 0;
+            // one of each lane at a time (rarely more than a few)
+#pragma unroll 1
+            for (uint64_t lanes; (lanes = __ballot(some)) != 0; some &= some - 1) {
+              const int place = from + __ffs((int)some) - 1;
+              const float l = logit<F32>(row, some ? place : 0);
+              uint32_t to = 0;
+              if (lane == 0) to = atomicAdd(&sh.list_size, (uint32_t)__popcll(lanes));
+              const uint32_t i = (uint32_t)__builtin_amdgcn_readfirstlane((int)to) +
+                                 __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
+              if (some && i < (uint32_t)kList) {
+                sh.list.keys[i] = __builtin_bit_cast(uint32_t, l);   // (the key later)
+                sh.list.places[i] = (uint32_t)place;
               }
-              to += (uint32_t)__popcll(in[e]);
             }
           }
         }
