@@ -10,11 +10,26 @@
 //          its row
 // Bound by the bytes of the adapters (decode) or of x, base and y (prompts).
 // So every adapter is read once for the rows that share it: a workgroup takes
-// a group, up to 64 rows of one adapter (16 where a call has no more rows),
-// gathered by their ids.  Up to kWholeRows rows one workgroup stands for each
-// row: it looks through all ids, and goes on if it is the first of its group.
-// Above, a workgroup stands for 64 rows in succession and takes their groups
-// in turn.
+// a group, rows of one adapter, gathered by their ids.  Up to kWholeRows rows
+// one workgroup stands for each row: it looks through all ids, and goes on if
+// it is the first of its group (16 rows).  Above, a workgroup stands for 32
+// (inner) or 64 (outer) rows in succession and takes their groups in turn.
+//
+// Measured: 128 rows with an adapter each, seven projections, rank 32: inner
+// 43 us for 218 MB (5.1 TB/s), outer 57 us for 268 MB (4.7); plain reads of
+// that size reach 6.4.  64 rows of 28 adapters, two projections, rank 16: 5.1
+// and 13.5 us (27 MB), where starting 1664 workgroups, 28 of 64 of which find
+// a group, takes about 5.  4001 rows of three requests, three projections,
+// rank 64: 26 and 43 us (124 MB).  One row: 4.2 and 4.6 us.
+//
+// What mattered: loads with no branch between them (a branch for each vector,
+// or two paths that the compiler joins, keeps them apart or cuts them into
+// words: 45 and 75 us for the outer kernel of the 4001 rows), x and A through
+// LDS in rows of 512 bytes (straight into the matrix layout, 64 bytes of 16
+// rows at a time: 54 us for the 218 MB), 16-byte LDS accesses (the union
+// aligned to 16).  Not kept: waves that go their own way over a compact list
+// of groups (61 to 75 us), a second set of registers for the next step (three
+// instead of five waves a SIMD: 71 to 83 us).
 //
 // The matrix instruction's columns are rows of x; a group's last row fills
 // the columns it leaves, which are not stored.

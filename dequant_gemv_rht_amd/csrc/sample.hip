@@ -18,10 +18,16 @@
 // the bins, more logits in its bin than fit in LDS, logits beyond 2^13 powers
 // of two, temperatures near infinity) are searched in as many passes as it takes.
 //
-// The second launch runs once through its code, most of which then comes from
-// the L2 line by line: loops there stay rolled, each piece of work has one
-// place, and what a wave can find out alone every wave does, without waiting
-// for the others.
+// The first launch is bound by vector instructions, 33 for each 64 logits,
+// six of them in fp64 or converting to and from it, and by LDS atomics where
+// there are cuts: 66 us for 256 rows of 151936 (156 MB; a plain read 24), of
+// which the sums in bins take a third; 7 us for one row.  The second runs
+// once through its code, most of which then comes from the L2 line by line
+// (92 KB of unrolled code took 49 us for one row where 45 KB take 30): loops
+// there stay rolled, each piece of work has one place, and what a wave can
+// find out alone every wave does, without waiting for the others.  45 us for
+// 64 rows, 50 for 256: the row with the most open top-p, whose cut's bin holds
+// thousands of logits in all parts, which one CU reads again.
 #include "wq_internal.h"
 
 namespace wq {

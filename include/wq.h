@@ -511,11 +511,12 @@ typedef struct wq_adapters {
  * for rows r = 0 .. m - 1 of every linear i.  A row whose id is outside
  * [0, count) gets base[i][r].  x is what the linear was given, not rotated.
  * Sums are fp32; A x enters the second product as two fp16 parts under a
- * power of two of its row (22 bits), and y is rounded once.  Rows with one
- * adapter share its weights wherever they stand, up to 256 rows; above, up
- * to 64 of them in each 64 rows in succession, so rows of one request should
- * then stand together.  An infinity or a NaN in a row of x or base reaches
- * that row of y only.  Results do not depend on timing.
+ * power of two of its row (22 bits), and y is rounded once.  Up to 256 rows,
+ * rows with one adapter share its weights, 16 at a time, wherever they stand;
+ * above, those among 32 (A) or 64 (B) rows in succession do, so rows of one
+ * request should then stand together.  An infinity or a NaN in a row of x or
+ * base reaches that row of y only; weights of adapters that no row names are
+ * not met.  Results do not depend on timing.
  *   w          host array [count] of descriptors
  *   x          fp16 [m][ldx[i]]
  *   ids        device int32 [m], one for all linears
@@ -558,12 +559,17 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
  *   logprobs out: device fp32 [rows], or NULL; -infinity for such a row
  *   workspace  device scratch of wq_sample_workspace bytes; no
  *            initialisation needed
- * Sums of w are whole multiples of 2^-44 or less of the largest (for vocab
- * up to 2^18; twice that for each doubling), added exactly in 64 bits: the
- * same inputs give the same token, whatever the timing.  rows 0 does
- * nothing.  Errors (before anything is launched): WQ_E_ARG, WQ_E_ALIGN (int32
- * and fp32 arrays other than logits need 4-byte alignment), WQ_E_UNSUPPORTED
- * (vocab above 2^20, rows above 2^20), WQ_E_WORKSPACE; WQ_E_HIP. */
+ * Weights are counted in 2^-44 of a power of two near the largest (2^-43 for
+ * vocab above 2^18, 2^-42 above 2^19), each within 2^-34 of itself, and added
+ * as whole numbers in 64 bits: the same inputs give the same token, whatever
+ * the timing and whatever the other rows are.  Two launches; a row with a cut
+ * further than 2^31 below its largest w, with logits beyond 2^13 T, or with
+ * more than 8192 logits within an eighth of a power of two of w around the
+ * cut takes several passes over its logits (about 0.1 ms more).  rows 0 does
+ * nothing.  Errors (before anything is launched): WQ_E_ARG (also an output
+ * that overlaps another array), WQ_E_ALIGN (int32 and fp32 arrays other than
+ * logits need 4-byte alignment), WQ_E_UNSUPPORTED (vocab above 2^20, rows
+ * above 2^20), WQ_E_WORKSPACE; WQ_E_HIP. */
 size_t wq_sample_workspace(int64_t rows, int64_t vocab);
 wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vocab, int64_t ldl, const float *u,
                     const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
