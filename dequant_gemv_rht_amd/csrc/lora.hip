@@ -10,10 +10,13 @@
 //          its row
 // Bound by the bytes of the adapters (decode) or of x, base and y (prompts).
 // So every adapter is read once for the rows that share it: a workgroup takes
-// a group, rows of one adapter, gathered by their ids.  Up to kWholeRows rows
-// one workgroup stands for each row: it looks through all ids, and goes on if
-// it is the first of its group (16 rows).  Above, a workgroup stands for 32
-// (inner) or 64 (outer) rows in succession and takes their groups in turn.
+// a group, rows of one adapter, gathered by their ids.  Of few rows, or up to
+// kWholeRows with many adapters, one workgroup stands for each row: it looks
+// through all ids, and goes on if it is the first of its group (16 rows).
+// Otherwise a workgroup stands for 32 (inner) or 64 (outer) rows in succession
+// and takes their groups in turn, or every slots-th of them: where there are
+// few rows, several workgroups share them in case every row has an adapter of
+// its own.  (The host knows how many adapters there are, not the rows' ids.)
 //
 // Measured: 128 rows with an adapter each, seven projections, rank 32: inner
 // 43 us for 218 MB (5.1 TB/s), outer 57 us for 268 MB (4.7); plain reads of
@@ -59,7 +62,7 @@ __device__ __forceinline__ uint64_t below(int n) { return n >= 64 ? ~0ull : (1ul
 // Runs f(id, rows in list) for the workgroup's groups, of at most 16 CT rows;
 // id -1: no adapter.
 template <bool WHOLE, int CT, typename F>
-__device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, int32_t *list, uint64_t *masks, F f) {
+__device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, int32_t *list, uint64_t *masks, int slot, F f) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
   const auto known = [&](int32_t id) { return id >= 0 && id < adapters ? id : -1; };
   if (WHOLE) {
@@ -86,16 +89,27 @@ __device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, 
     const bool live = lane < 16 * CT && row < g.m;
     const int32_t mine = live ? known(g.ids[row]) : -1;
     uint64_t left = __ballot(live);
-    while (left) {
+    for (int i = 0; left; ++i) {
       const int32_t id = __shfl(mine, __ffsll((unsigned long long)left) - 1);
       const uint64_t same = __ballot(live && mine == id) & left;
       left &= ~same;
+      if (i % g.slots != slot) continue;   // another workgroup's
       __syncthreads();   // the last group's list is no longer needed
       if (wave == 0 && (same >> lane & 1)) list[__popcll(same & below(lane))] = (int32_t)row;
       __syncthreads();
       f(id, __popcll(same));
     }
   }
+}
+
+// The linear that piece `i` of a launch is of, and which of its pieces it is
+__device__ __forceinline__ int linear_of(const LoraArgs &g, const uint32_t *to, uint32_t &i) {
+  int l = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxBatch - 1; ++k) l += k + 1 < g.count && i >= to[k];
+  l = __builtin_amdgcn_readfirstlane(l);
+  i -= l ? to[l - 1] : 0;
+  return l;
 }
 
 constexpr int kStage = 256;            // channels staged in LDS at once
@@ -115,13 +129,14 @@ __global__ __launch_bounds__(kLoraThreads) void lora_inner_kernel(LoraArgs g) {
     _Float16 rows[kRanks + kRows][kStageLd];
     float sums[kWaves][16][kSumLd];
   } lds;
-  const int part = (int)blockIdx.z / g.count;
-  const LoraDesc L = g.lin[blockIdx.z - part * g.count];
-  const int r0 = part * kRanks, k0 = (int)blockIdx.y * g.steps * 32, k1 = min(L.k, k0 + g.steps * 32);
-  if (r0 >= L.rank || k0 >= k1) return;
+  uint32_t split = blockIdx.y;
+  const LoraDesc L = g.lin[linear_of(g, g.splits_to, split)];
+  const int slot = (int)blockIdx.z % g.slots, r0 = (int)blockIdx.z / g.slots * kRanks;   // first rank
+  const int k0 = (int)split * g.steps * 32, k1 = min(L.k, k0 + g.steps * 32);
+  if (r0 >= L.rank) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int row = tid >> 5, at = 8 * (tid & 31);   // a thread's rows row + 8 i and its 8 channels
-  for_groups<WHOLE, CT>(g, L.count, list, masks, [&](int32_t id, int rows) {
+  for_groups<WHOLE, CT>(g, L.count, list, masks, slot, [&](int32_t id, int rows) {
     if (id < 0) return;
     // ranks and rows past the last repeat it and are not stored; channels
     // past the last are zeros
@@ -177,7 +192,7 @@ __global__ __launch_bounds__(kLoraThreads) void lora_inner_kernel(LoraArgs g) {
       }
     }
     const float scale = L.scales ? L.scales[id] : 1.0f;
-    float *out = L.t + (int64_t)blockIdx.y * g.m * L.rank + r0;
+    float *out = L.t + (int64_t)split * g.m * L.rank + r0;
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
       if (16 * t >= rows) break;
@@ -426,11 +441,10 @@ __global__ __launch_bounds__(kLoraThreads) void lora_outer_kernel(LoraArgs g) {
   __shared__ uint64_t masks[kWaves];
   __shared__ alignas(16) half8_t parts[CT][KK][PACK ? 1 : 2][64];
   __shared__ int32_t powers[CT][16];
-  const LoraDesc L = g.lin[blockIdx.z];
-  const int n0 = (int)blockIdx.y * g.chunk;
-  if (n0 >= L.n) return;
-  const int n1 = min(n0 + g.chunk, L.n);
-  for_groups<WHOLE, CT>(g, L.count, list, masks, [&](int32_t id, int rows) {
+  uint32_t chunk = blockIdx.y;
+  const LoraDesc L = g.lin[linear_of(g, g.chunks_to, chunk)];
+  const int n0 = (int)chunk * g.chunk, n1 = min(n0 + g.chunk, L.n);
+  for_groups<WHOLE, CT>(g, L.count, list, masks, (int)blockIdx.z, [&](int32_t id, int rows) {
     if (L.f32)
       outer_group<float, KK, PACK, CT>(g, L, list, parts, powers, id, rows, n0, n1);
     else
@@ -443,8 +457,8 @@ template <bool WHOLE, int CI, int CO>
 hipError_t launch(const LoraArgs &a, const LoraPlan &p, hipStream_t s) {
   const auto inner = [&](auto kernel, int tiles) {
     const unsigned parts = (unsigned)((p.rank + 16 * tiles - 1) / (16 * tiles));
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.inner_tiles, (unsigned)p.splits, parts * (unsigned)a.count), dim3(kLoraThreads),
-                       0, s, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.inner_tiles, (unsigned)p.splits, parts * (unsigned)p.slots),
+                       dim3(kLoraThreads), 0, s, a);
   };
   if (p.rank <= 16)
     inner(lora_inner_kernel<WHOLE, 1, CI>, 1);
@@ -453,7 +467,8 @@ hipError_t launch(const LoraArgs &a, const LoraPlan &p, hipStream_t s) {
   else
     inner(lora_inner_kernel<WHOLE, 4, CI>, 4);
   const auto outer = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.outer_tiles, (unsigned)p.chunks, (unsigned)a.count), dim3(kLoraThreads), 0, s, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)p.outer_tiles, (unsigned)p.chunks, (unsigned)p.slots), dim3(kLoraThreads), 0, s,
+                       a);
   };
   if (p.rank <= 16)
     outer(lora_outer_kernel<WHOLE, 1, true, CO>);

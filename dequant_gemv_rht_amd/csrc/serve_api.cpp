@@ -184,6 +184,9 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   a.m = (int32_t)m;
   const wq::LoraPlan plan = wq::lora_plan(count, w, m);
   a.steps = plan.steps;
+  a.slots = plan.slots;
+  memcpy(a.splits_to, plan.splits_to, sizeof a.splits_to);
+  memcpy(a.chunks_to, plan.chunks_to, sizeof a.chunks_to);
   a.chunk = plan.chunk;
   return hip_status(wq::launch_lora(a, plan, (hipStream_t)stream), who);
 }

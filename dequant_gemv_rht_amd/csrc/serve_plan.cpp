@@ -6,18 +6,28 @@ namespace wq {
 
 namespace {
 
-constexpr int64_t kWork = 2048;   // workgroups that K and the outputs of up to kWholeRows rows are cut for
-constexpr int64_t kLongWork = 768, kLongSplits = 4;
+constexpr int64_t kLongWork = 768, kLongSplits = 4, kBlockWork = 2048;
+constexpr int64_t kFewAdapters = 8, kShared = 4096, kMostSlots = 16;
 
-// the smallest multiple of `unit` in which `pieces`, cut, make at most kWork
-// workgroups for each `tiles`, and at most `most` of the longest piece
-int64_t cut(int32_t count, const wq_adapters *w, int64_t wq_adapters::*length, int64_t tiles, int64_t unit, int64_t most) {
+// Workgroups that K and the outputs are cut for where one stands for each row:
+// most of them find no group, so they are few, but eight of a row at least,
+// one group's work being divided by that.  Projections 2560 to 4096, 1024 and
+// 1024, rank 16, a call in us:
+//              64 rows, 32 adapters  256 rows, 32 adapters
+//   1024 all            10.9                  21.4
+//   2048 all            13.7                  17.7
+int64_t work(int64_t rows) { return rows <= 128 ? 1024 : 8 * rows; }
+
+// the smallest multiple of `unit` in which the linears' lengths, cut, make at
+// most `work` workgroups for `tiles`, and at most `most` of the longest
+int64_t cut(int32_t count, const wq_adapters *w, int64_t wq_adapters::*length, int64_t tiles, int64_t unit, int64_t work,
+            int64_t most) {
   int64_t sum = 0, longest = 0;
   for (int32_t i = 0; i < count; ++i) {
     sum += w[i].*length;
     longest = w[i].*length > longest ? w[i].*length : longest;
   }
-  int64_t piece = (sum * tiles + kWork - 1) / kWork;
+  int64_t piece = (sum * tiles + work - 1) / work;
   if (piece > longest) piece = longest;
   const int64_t least = (longest + most - 1) / most;
   if (piece < least) piece = least;
@@ -31,37 +41,59 @@ int32_t splits_for(int64_t tiles) {
   return (int32_t)(s < 1 ? 1 : s > kLongSplits ? kLongSplits : s);
 }
 
+// Workgroups that share the groups of some rows in succession.  Every row may
+// have an adapter of its own: one workgroup takes 205 us for 257 rows of the
+// projections above with 256 adapters, fifteen 71 (32 adapters: 119 and 42, in
+// runs 35 and 18; one adapter: 11 both).  With more rows the blocks are enough:
+// 4001 rows 67 us both; twice as many at 512 rows 122 us instead of 102.
+int32_t slots_for(int64_t rows, int32_t adapters) {
+  int64_t s = kShared / rows;
+  s = s < 1 ? 1 : s > kMostSlots ? kMostSlots : s;
+  return (int32_t)(s > adapters + 1 ? adapters + 1 : s);
+}
+
 }  // namespace
 
 LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
-  LoraPlan p;
-  p.whole = m <= kWholeRows;
+  LoraPlan p = {};
+  int32_t adapters = 0;
+  for (int32_t i = 0; i < count; ++i) adapters = w[i].count > adapters ? w[i].count : adapters;
+  // A workgroup for each row or for rows in succession: the projections above,
+  // rows with ids in any order, a call in us:
+  //   rows, adapters  32, 8  64, 1  64, 16  128, 4  128, 16  256, 8  256, 16
+  //   each row          9.6   11.7    10.9    15.6     14.0    18.9     19.2
+  //   in succession    10.2   10.8    12.8    10.1     17.3    15.8     27.7
+  p.whole = m <= 32 || (m <= kWholeRows && adapters > kFewAdapters);
   p.inner_tiles = p.whole ? m : (m + 31) / 32;
   p.outer_tiles = p.whole ? m : (m + 63) / 64;
-  int64_t n = 0, k = 0;
-  p.rank = 0;
+  int64_t k = 0;
   for (int32_t i = 0; i < count; ++i) {
-    n = w[i].n > n ? w[i].n : n;
     k = w[i].k > k ? w[i].k : k;
     p.rank = w[i].rank > p.rank ? w[i].rank : p.rank;
   }
   int64_t piece;
   if (p.whole) {
-    piece = cut(count, w, &wq_adapters::k, m, 128, kLoraSplits);
+    piece = cut(count, w, &wq_adapters::k, m, 128, work(m), kLoraSplits);
+    p.slots = 1;
   } else {
     const int64_t splits = splits_for(p.inner_tiles * count);
     piece = ((k + splits - 1) / splits + 255) / 256 * 256;
+    p.slots = slots_for(m, adapters);
   }
   p.steps = (int32_t)(piece / 32);
-  p.splits = (int32_t)((k + piece - 1) / piece);
-  p.chunk = (int32_t)cut(count, w, &wq_adapters::n, p.outer_tiles, 256, INT32_MAX);
-  p.chunks = (n + p.chunk - 1) / p.chunk;
+  p.chunk = (int32_t)cut(count, w, &wq_adapters::n, p.outer_tiles, 256, p.whole ? work(m) : kBlockWork, INT32_MAX);
+  for (int32_t i = 0; i < count; ++i) {
+    p.splits += (uint32_t)((w[i].k + piece - 1) / piece);
+    p.chunks += (uint32_t)((w[i].n + p.chunk - 1) / p.chunk);
+    p.splits_to[i] = p.splits;
+    p.chunks_to[i] = p.chunks;
+  }
   return p;
 }
 
 size_t lora_workspace(const wq_adapters &w, int64_t m) {
-  // a bound of splits * m that grows with m: in a long call splits is at most
-  // kLongSplits, and at most kLongWork over a 32nd of m
+  // a bound of splits * m that grows with m: where workgroups stand for rows in
+  // succession, splits is at most kLongSplits, and at most kLongWork over a 32nd of m
   const int64_t whole = (m <= kWholeRows ? m : kWholeRows) * kLoraSplits;
   const int64_t most = kLongSplits * m, filled = m + 32 * kLongWork, longer = most < filled ? most : filled;
   const size_t bytes = (size_t)(m <= kWholeRows || whole > longer ? whole : longer) * (size_t)w.rank * sizeof(float);

@@ -243,13 +243,17 @@ struct LoraArgs {
   const int32_t *ids;
   int32_t count, m;
   int32_t steps, chunk;         // 32s of K of a workgroup (first kernel); outputs, a multiple of 256 (second)
+  int32_t slots;                // workgroups that share the groups of some rows in succession
+  uint32_t splits_to[kMaxBatch], chunks_to[kMaxBatch];   // pieces of K, of the outputs, of linears 0 .. i together
 };
 constexpr int kWholeRows = 256; // rows whose groups are gathered from all of the call
 constexpr int kLoraSplits = 8;  // at most
 struct LoraPlan {
   bool whole;                   // a workgroup for each row, or for rows in succession
-  int64_t inner_tiles, outer_tiles, chunks;
-  int32_t splits, steps, chunk, rank;   // the largest rank
+  int64_t inner_tiles, outer_tiles;
+  int32_t steps, chunk, slots, rank;    // the largest rank
+  uint32_t splits, chunks;      // of all linears
+  uint32_t splits_to[kMaxBatch], chunks_to[kMaxBatch];
 };
 LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m);
 size_t lora_workspace(const wq_adapters &w, int64_t m);   // of one linear

@@ -511,10 +511,10 @@ typedef struct wq_adapters {
  * for rows r = 0 .. m - 1 of every linear i.  A row whose id is outside
  * [0, count) gets base[i][r].  x is what the linear was given, not rotated.
  * Sums are fp32; A x enters the second product as two fp16 parts under a
- * power of two of its row (22 bits), and y is rounded once.  Up to 256 rows,
- * rows with one adapter share its weights, 16 at a time, wherever they stand;
- * above, those among 32 (A) or 64 (B) rows in succession do, so rows of one
- * request should then stand together.  An infinity or a NaN in a row of x or
+ * power of two of its row (22 bits), and y is rounded once.  Up to 32 rows,
+ * or 256 with more than 8 adapters, rows with one adapter share its weights,
+ * 16 at a time, wherever they stand; above, those among 32 (A) or 64 (B) rows
+ * in succession do, so rows of one request should then stand together.  An infinity or a NaN in a row of x or
  * base reaches that row of y only; weights of adapters that no row names are
  * not met.  Results do not depend on timing.
  *   w          host array [count] of descriptors

@@ -104,12 +104,20 @@ int main() {
         for (int64_t m = 1; m < 1 << 20; m += 1 + m / 4) {
           const wq::LoraPlan p = wq::lora_plan(count, w, m);
           const size_t ws = wq::lora_workspace(w[0], m);
-          expect(p.steps > 0 && (int64_t)p.steps * 32 * p.splits >= k && (int64_t)p.steps * 32 * (p.splits - 1) < k, "K", k, m);
-          expect(p.steps % 4 == 0, "whole 128s", k, m);
-          expect(p.chunk > 0 && p.chunk % 256 == 0 && p.chunk * p.chunks >= n + 100 * (count - 1), "outputs", n, m);
-          expect((size_t)p.splits * m * w[0].rank * sizeof(float) <= ws && ws >= before, "workspace", p.splits, m);
+          expect(p.steps > 0 && p.steps % 4 == 0 && p.chunk > 0 && p.chunk % 256 == 0, "whole 128s", k, m);
+          uint32_t splits = 0, chunks = 0;
+          for (int i = 0; i < count; ++i) {
+            const int64_t of_k = p.splits_to[i] - splits, of_n = p.chunks_to[i] - chunks;
+            expect(of_k * p.steps * 32 >= k && (of_k - 1) * p.steps * 32 < k, "K", k, m);
+            expect(of_n * p.chunk >= w[i].n && (of_n - 1) * p.chunk < w[i].n, "outputs", n, m);
+            expect((size_t)of_k * m * w[i].rank * sizeof(float) <= wq::lora_workspace(w[i], m), "workspace", of_k, m);
+            splits = p.splits_to[i];
+            chunks = p.chunks_to[i];
+          }
+          expect(splits == p.splits && chunks == p.chunks && ws >= before, "sums", p.splits, m);
           expect(p.rank == 8 * count, "rank", p.rank, count);
-          expect(p.inner_tiles * p.splits * count * 8 <= wq::kMaxGroups256 * (int64_t)64 && p.splits <= 65535 && p.chunks <= 65535,
+          expect(p.inner_tiles * p.splits * p.slots * 2 <= wq::kMaxGroups256 && p.splits <= 65535 && p.chunks <= 65535 &&
+                     p.outer_tiles * p.chunks * p.slots <= wq::kMaxGroups256 && p.slots >= 1 && (p.slots == 1 || !p.whole),
                  "launch", p.inner_tiles, p.chunks);
           before = ws;
         }

@@ -68,6 +68,19 @@ def test_against_oracle(m, count, rank, k, n, kind, f32):
     assert np.array_equal(y.cpu().numpy()[out], base[out])   # bit for bit
 
 
+@pytest.mark.parametrize("kind", ["each", "runs", "some"])
+@pytest.mark.parametrize("count", [8, 9, 40])
+@pytest.mark.parametrize("m", [31, 32, 33, 129, 256, 257, 1025])
+def test_few_and_many_adapters(m, count, kind):
+    """Rows on both sides of where the groups are made in another way."""
+    rng = np.random.default_rng(m * 100 + count)
+    a, b, x, base = make(rng, count, 72, 384, 70, m)
+    ids = ids_of(kind, rng, m, count).astype(np.int32)
+    say("lora", m, count, kind)
+    (y,) = dq.wq_lora([dev(a)], [dev(b)], [dev(x)], dev(ids), [dev(base)])
+    check(y, *O.lora(a, b, x, ids, base), False, "y")
+
+
 def test_several_linears_strides_and_in_place():
     rng = np.random.default_rng(5)
     m, count = 37, 4
