@@ -17,20 +17,28 @@ wq_status hip_status(hipError_t e, const char *who) {
   return e == hipSuccess ? WQ_OK : set_error(WQ_E_HIP, "%s: %s", who, hipGetErrorString(e));
 }
 
-// bytes [begin, end) of an array; empty ones overlap nothing
+// bytes [begin, end) of an array; empty ones overlap nothing.  Of rows, their
+// distance and their own bytes.
 struct Range {
-  uintptr_t begin, end;
+  uintptr_t begin, end, pitch, width;
 };
 
-Range range(const void *p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes}; }
+Range range(const void *p, int64_t bytes) { return {(uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes, 0, 0}; }
 
 // rows of `cols` elements, `ld` apart
 Range rows(const void *p, int64_t n, int64_t ld, int64_t cols, int size) {
-  return range(p, n && cols ? ((n - 1) * ld + cols) * size : 0);
+  Range r = range(p, n && cols ? ((n - 1) * ld + cols) * size : 0);
+  r.pitch = (uintptr_t)ld * size;
+  r.width = (uintptr_t)cols * size;
+  return r;
 }
 
 bool overlap(const Range &a, const Range &b) {
-  return a.begin != a.end && b.begin != b.end && a.begin < b.end && b.begin < a.end;
+  if (a.begin == a.end || b.begin == b.end || a.begin >= b.end || b.begin >= a.end) return false;
+  if (!a.pitch || a.pitch != b.pitch) return true;
+  // rows at one distance: other columns of one wider array
+  const uintptr_t off = a.begin <= b.begin ? (b.begin - a.begin) % a.pitch : (a.pitch - (a.begin - b.begin) % a.pitch) % a.pitch;
+  return off < a.width || off + b.width > a.pitch;
 }
 
 wq_status check_adapters(int32_t count, const wq_adapters *w, int64_t m, const char *who) {
@@ -48,6 +56,8 @@ wq_status check_adapters(int32_t count, const wq_adapters *w, int64_t m, const c
     if (w[i].k % 128) return set_error(WQ_E_ARG, "%s: k[%d]=%lld is not a multiple of 128", who, i, (long long)w[i].k);
     if (w[i].n >= 1 << 30 || w[i].k >= 1 << 27)
       return set_error(WQ_E_UNSUPPORTED, "%s: n[%d] of 2^30 or k of 2^27 or more", who, i);
+    if ((int64_t)w[i].count * w[i].rank > INT64_MAX / 8 / (w[i].k > w[i].n ? w[i].k : w[i].n))
+      return set_error(WQ_E_UNSUPPORTED, "%s: adapters[%d] past the address range", who, i);
   }
   return WQ_OK;
 }
@@ -137,7 +147,7 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   if (!aligned(ids, 4)) return set_error(WQ_E_ALIGN, "%s: ids must be 4-byte aligned", who);
   wq::LoraArgs a;
   memset(&a, 0, sizeof a);
-  Range in[3 * WQ_MAX_BATCH + 1], out[WQ_MAX_BATCH];
+  Range in[5 * WQ_MAX_BATCH + 1], out[WQ_MAX_BATCH];
   int ins = 0;
   in[ins++] = range(ids, 4 * m);
   size_t need = 0;
@@ -158,6 +168,8 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
     in[ins++] = rows(x[i], m, ldx[i], w[i].k, 2);
     in[ins++] = range(w[i].scales, w[i].scales ? 4 * (int64_t)w[i].count : 0);
     in[ins++] = rows(base[i], m, ldb[i], w[i].n, size);
+    in[ins++] = range(w[i].a, (int64_t)w[i].count * w[i].rank * w[i].k * 2);
+    in[ins++] = range(w[i].b, (int64_t)w[i].count * w[i].rank * w[i].n * 2);
     out[i] = rows(y[i], m, ldy[i], w[i].n, size);
     a.lin[i] = {w[i].a, w[i].b, w[i].scales, x[i], base[i], y[i], nullptr, ldx[i], ldb[i], ldy[i],
                 (int32_t)w[i].n, (int32_t)w[i].k, w[i].count, w[i].rank, dtype[i] == WQ_F32};
@@ -165,7 +177,7 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   }
   for (int i = 0; i < count; ++i) {
     for (int j = 0; j < ins; ++j) {
-      const bool in_place = j == 3 * i + 3 && y[i] == base[i] && ldy[i] == ldb[i];
+      const bool in_place = j == 5 * i + 3 && y[i] == base[i] && ldy[i] == ldb[i];
       if (!in_place && overlap(out[i], in[j])) return set_error(WQ_E_ARG, "%s: y[%d] overlaps an input", who, i);
     }
     for (int j = 0; j < i; ++j)
@@ -174,6 +186,11 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   if (workspace_bytes < need || !workspace)
     return set_error(WQ_E_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given", who, need, workspace_bytes);
   if (!aligned(workspace, 16)) return set_error(WQ_E_ALIGN, "%s: workspace must be 16-byte aligned", who);
+  const Range scratch = range(workspace, (int64_t)need);
+  for (int j = 0; j < ins; ++j)
+    if (overlap(scratch, in[j])) return set_error(WQ_E_ARG, "%s: the workspace overlaps an input", who);
+  for (int i = 0; i < count; ++i)
+    if (overlap(scratch, out[i])) return set_error(WQ_E_ARG, "%s: the workspace overlaps y[%d]", who, i);
   char *at = static_cast<char *>(workspace);
   for (int i = 0; i < count; ++i) {
     a.lin[i].t = reinterpret_cast<float *>(at);
@@ -232,6 +249,11 @@ wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vo
     for (const Range &r : in)
       if (overlap(o, r)) return set_error(WQ_E_ARG, "%s: an output overlaps an input", who);
   if (overlap(out[0], out[1])) return set_error(WQ_E_ARG, "%s: outputs overlap", who);
+  const Range scratch = range(workspace, (int64_t)need);
+  for (const Range &r : in)
+    if (overlap(scratch, r)) return set_error(WQ_E_ARG, "%s: the workspace overlaps an input", who);
+  if (overlap(scratch, out[0]) || overlap(scratch, out[1]))
+    return set_error(WQ_E_ARG, "%s: the workspace overlaps an output", who);
   wq::SampleArgs a;
   memset(&a, 0, sizeof a);
   a.logits = logits;

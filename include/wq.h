@@ -521,12 +521,14 @@ typedef struct wq_adapters {
  *   x          fp16 [m][ldx[i]]
  *   ids        device int32 [m], one for all linears
  *   base, y    fp16 or fp32 (dtype[i]) [m][ldb[i]], [m][ldy[i]]; y[i] may
- *              equal base[i] when ldy == ldb, and overlaps no other array;
+ *              equal base[i] when ldy == ldb, and overlaps no other array
+ *              (columns of one wider array, of one row stride, do not);
  *              ldb and ldy at least n, of any alignment
- *   workspace  device scratch of wq_lora_workspace bytes (A x of every row)
+ *   workspace  device scratch of wq_lora_workspace bytes (A x of every row),
+ *              apart from every other array
  * m 0 does nothing.  Errors (before anything is launched): WQ_E_ARG,
  * WQ_E_ALIGN (also ldx not a multiple of 8; ids need 4-byte alignment),
- * WQ_E_UNSUPPORTED (rank or k as above, m of 2^24 or more, n of 2^30 or
+ * WQ_E_UNSUPPORTED (rank or k as above, m of 2^24, n of 2^30, k of 2^27 or
  * more), WQ_E_WORKSPACE; WQ_E_HIP. */
 size_t wq_lora_workspace(int32_t count, const wq_adapters *w, int64_t m);
 wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x, const int64_t *ldx, int64_t m,
@@ -557,8 +559,8 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
  *   ids      out: device int32 [rows]; -1 for a row in which nothing can
  *            be drawn
  *   logprobs out: device fp32 [rows], or NULL; -infinity for such a row
- *   workspace  device scratch of wq_sample_workspace bytes; no
- *            initialisation needed
+ *   workspace  device scratch of wq_sample_workspace bytes, apart from
+ *            every other array; no initialisation needed
  * Weights are counted in 2^-44 of a power of two near the largest (2^-43 for
  * vocab above 2^18, 2^-42 above 2^19), each within 2^-34 of itself, and added
  * as whole numbers in 64 bits: the same inputs give the same token, whatever

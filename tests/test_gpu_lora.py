@@ -109,6 +109,29 @@ def test_several_linears_strides_and_in_place():
         assert torch.equal(buf, before)   # nothing beside the rows was written
 
 
+@pytest.mark.parametrize("m", [3, 50, 300])
+def test_columns_of_one_wide_array_in_place(m):
+    rng = np.random.default_rng(m)
+    count, k, widths = 5, 256, (96, 32, 32)
+    ids = ids_of("some", rng, m, count).astype(np.int32)
+    wide = torch.full((m, sum(widths) + 8), 5.0, dtype=torch.float16, device="cuda")
+    parts, a, b, want, at = [], [], [], [], 0
+    x = None
+    for n in widths:
+        A, B, X, base = make(rng, count, 16, k, n, m)
+        x = X if x is None else x
+        view = wide[:, at:at + n]
+        view.copy_(dev(base))
+        parts.append(view), a.append(dev(A)), b.append(dev(B))
+        want.append(O.lora(A, B, x, ids, base))
+        at += n
+    xs = [dev(x)] * 3
+    ys = dq.wq_lora(a, b, xs, dev(ids), parts, out=parts)
+    for y, w in zip(ys, want):
+        check(y, *w, False, "y")
+    assert (wide[:, at:] == 5.0).all()
+
+
 @pytest.mark.parametrize("m,kind", [(5, "each"), (40, "some"), (300, "runs")])
 @pytest.mark.parametrize("x_scale", [1e-6, 60.0, 3000.0])
 def test_magnitudes(m, kind, x_scale):

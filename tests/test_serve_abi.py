@@ -113,6 +113,21 @@ def test_bad_lora(lib, kw, status, text):
     said(lib, lora(lib, **kw), status, text)
 
 
+@pytest.mark.parametrize("kw,status,text", [
+    (dict(y=P(0)), A, "overlaps an input"), (dict(y=P(1) + 16), A, "overlaps an input"),      # a, b
+    (dict(ws=P(6)), A, "workspace overlaps y[0]"), (dict(ws=P(5) + 16), A, "workspace overlaps an input"),
+    (dict(ws=P(0)), A, "workspace overlaps an input"), (dict(ws=P(3)), A, "workspace overlaps an input"),
+    (dict(w=adapters(count=2 ** 31 - 1, rank=128, k=1 << 26)), U, "address range"),
+    # columns of one wide array: a column in common, another row stride, the next row's first column
+    (dict(count=2, y=[P(6), P(6) + 112], ldy=128), A, "overlap"), (dict(count=2, y=[P(6), P(6) + 128], ldy=[128, 136]), A, "overlap"),
+    (dict(count=2, y=[P(6), P(6) + 144], ldy=128), A, "overlap"), (dict(count=2, y=[P(6) + 144, P(6)], ldy=128), A, "overlap"),
+    (dict(count=2, y=[P(6), P(6) + 128], ldy=128, ws=None), W, "workspace"),                  # none: goes on to the next check
+    (dict(count=2, y=[P(6) + 256 + 128, P(6)], ldy=128, ws=None), W, "workspace"),
+])
+def test_lora_arrays_apart(lib, kw, status, text):
+    said(lib, lora(lib, **kw), status, text)
+
+
 def test_lora_workspace(lib):
     assert lib.wq_lora_workspace(1, adapters(), 0) == 0
     sizes = [lib.wq_lora_workspace(1, adapters(), m) for m in (0, 1, 2, 16, 17, 64, 256, 257, 1000, 5000, (1 << 24) - 1)]
@@ -139,6 +154,11 @@ SAMPLE = dict(logits=P(0), dtype=2, rows=4, vocab=1000, ldl=1000, u=P(1), temper
 ])
 def test_bad_sample(lib, kw, status, text):
     said(lib, lib.wq_sample(*{**SAMPLE, **kw}.values(), None), status, text)
+
+
+@pytest.mark.parametrize("ws,text", [(P(0), "an input"), (P(4), "an input"), (P(6), "an output"), (P(7), "an output")])
+def test_sample_workspace_apart(lib, ws, text):
+    said(lib, lib.wq_sample(*{**SAMPLE, "ws": ws}.values(), None), A, "workspace overlaps " + text)
 
 
 def test_sample_workspace(lib):
