@@ -19,11 +19,11 @@
 // its own.  (The host knows how many adapters there are, not the rows' ids.)
 //
 // Measured: 128 rows with an adapter each, seven projections, rank 32: inner
-// 43 us for 218 MB (5.1 TB/s), outer 57 us for 268 MB (4.7); plain reads of
-// that size reach 6.4.  64 rows of 28 adapters, two projections, rank 16: 5.1
-// and 13.5 us (27 MB), where starting 1664 workgroups, 28 of 64 of which find
-// a group, takes about 5.  4001 rows of three requests, three projections,
-// rank 64: 26 and 43 us (124 MB).  One row: 4.2 and 4.6 us.
+// 42 us for 218 MB (5.2 TB/s), outer 58 us for 268 MB (4.6); plain reads of
+// that size reach 6.4.  64 rows of 28 adapters, two projections, rank 16: 5.6
+// and 11.0 us (27 MB), of which starting 900 and 1024 workgroups, 28 of 64 of
+// which find a group, is about half.  4001 rows of three requests, three
+// projections, rank 64: 28 and 42 us (124 MB).  One row: 4.6 and 5.0 us.
 //
 // What mattered: loads with no branch between them (a branch for each vector,
 // or two paths that the compiler joins, keeps them apart or cuts them into
