@@ -23,7 +23,8 @@
 // that size reach 6.4.  64 rows of 28 adapters, two projections, rank 16: 5.6
 // and 11.0 us (27 MB), of which starting 900 and 1024 workgroups, 28 of 64 of
 // which find a group, is about half.  4001 rows of three requests, three
-// projections, rank 64: 28 and 42 us (124 MB).  One row: 4.6 and 5.0 us.
+// projections, rank 64: a call of 59 us (124 MB; with the rows' pieces spread
+// over all XCDs, and twice as many of the outputs, 67).  One row: 4.6 and 5.0 us.
 //
 // What mattered: loads with no branch between them (a branch for each vector,
 // or two paths that the compiler joins, keeps them apart or cuts them into
@@ -47,6 +48,7 @@ typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
+constexpr int kXcds = 8;
 constexpr int kLoraThreads = 64 * kWaves;
 static_assert(kWholeRows == kLoraThreads, "a thread looks at one id");
 
@@ -62,8 +64,8 @@ __device__ __forceinline__ uint64_t below(int n) { return n >= 64 ? ~0ull : (1ul
 // Runs f(id, rows in list) for the workgroup's groups, of at most 16 CT rows;
 // id -1: no adapter.
 template <bool WHOLE, int CT, typename F>
-__device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, int32_t *list, uint64_t *masks, int slot, F f) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = blockIdx.x;
+__device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, int32_t *list, uint64_t *masks, int b, int slot, F f) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const auto known = [&](int32_t id) { return id >= 0 && id < adapters ? id : -1; };
   if (WHOLE) {
     const int32_t id = known(g.ids[b]);
@@ -102,6 +104,21 @@ __device__ __forceinline__ void for_groups(const LoraArgs &g, int32_t adapters, 
   }
 }
 
+// Which rows, which piece of K or of the outputs, and what else of it a
+// workgroup takes.  NEAR: the pieces of some rows follow each other on one
+// XCD (workgroups go to the eight in turn), whose L2 then has x or t.
+struct Part {
+  int tile;
+  uint32_t piece;
+  int rest;
+};
+
+template <bool WHOLE>
+__device__ __forceinline__ Part part_of(uint32_t pieces, bool near) {
+  if (WHOLE || !near) return {(int)blockIdx.x, blockIdx.y, (int)blockIdx.z};
+  return {(int)(blockIdx.z * kXcds + blockIdx.x), blockIdx.y % pieces, (int)(blockIdx.y / pieces)};
+}
+
 // The linear that piece `i` of a launch is of, and which of its pieces it is
 __device__ __forceinline__ int linear_of(const LoraArgs &g, const uint32_t *to, uint32_t &i) {
   int l = 0;
@@ -129,14 +146,15 @@ __global__ __launch_bounds__(kLoraThreads) void lora_inner_kernel(LoraArgs g) {
     _Float16 rows[kRanks + kRows][kStageLd];
     float sums[kWaves][16][kSumLd];
   } lds;
-  uint32_t split = blockIdx.y;
+  const Part part = part_of<WHOLE>(g.splits_to[g.count - 1], g.near);
+  uint32_t split = part.piece;
   const LoraDesc L = g.lin[linear_of(g, g.splits_to, split)];
-  const int slot = (int)blockIdx.z % g.slots, r0 = (int)blockIdx.z / g.slots * kRanks;   // first rank
+  const int slot = part.rest % g.slots, r0 = part.rest / g.slots * kRanks;   // first rank
   const int k0 = (int)split * g.steps * 32, k1 = min(L.k, k0 + g.steps * 32);
   if (r0 >= L.rank) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = lane & 15, q = lane >> 4;
   const int row = tid >> 5, at = 8 * (tid & 31);   // a thread's rows row + 8 i and its 8 channels
-  for_groups<WHOLE, CT>(g, L.count, list, masks, slot, [&](int32_t id, int rows) {
+  for_groups<WHOLE, CT>(g, L.count, list, masks, part.tile, slot, [&](int32_t id, int rows) {
     if (id < 0) return;
     // ranks and rows past the last repeat it and are not stored; channels
     // past the last are zeros
@@ -441,10 +459,11 @@ __global__ __launch_bounds__(kLoraThreads) void lora_outer_kernel(LoraArgs g) {
   __shared__ uint64_t masks[kWaves];
   __shared__ alignas(16) half8_t parts[CT][KK][PACK ? 1 : 2][64];
   __shared__ int32_t powers[CT][16];
-  uint32_t chunk = blockIdx.y;
+  const Part part = part_of<WHOLE>(g.chunks_to[g.count - 1], g.near);
+  uint32_t chunk = part.piece;
   const LoraDesc L = g.lin[linear_of(g, g.chunks_to, chunk)];
   const int n0 = (int)chunk * g.chunk, n1 = min(n0 + g.chunk, L.n);
-  for_groups<WHOLE, CT>(g, L.count, list, masks, (int)blockIdx.z, [&](int32_t id, int rows) {
+  for_groups<WHOLE, CT>(g, L.count, list, masks, part.tile, part.rest, [&](int32_t id, int rows) {
     if (L.f32)
       outer_group<float, KK, PACK, CT>(g, L, list, parts, powers, id, rows, n0, n1);
     else
@@ -452,13 +471,18 @@ __global__ __launch_bounds__(kLoraThreads) void lora_outer_kernel(LoraArgs g) {
   });
 }
 
+dim3 grid(int64_t tiles, uint32_t pieces, uint32_t rest, bool near) {
+  if (near) return dim3(kXcds, pieces * rest, (unsigned)((tiles + kXcds - 1) / kXcds));
+  return dim3((unsigned)tiles, pieces, rest);
+}
+
 // CI, CO: sixteens of rows of a group in the inner and the outer kernel
 template <bool WHOLE, int CI, int CO>
 hipError_t launch(const LoraArgs &a, const LoraPlan &p, hipStream_t s) {
   const auto inner = [&](auto kernel, int tiles) {
-    const unsigned parts = (unsigned)((p.rank + 16 * tiles - 1) / (16 * tiles));
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.inner_tiles, (unsigned)p.splits, parts * (unsigned)p.slots),
-                       dim3(kLoraThreads), 0, s, a);
+    const uint32_t parts = (uint32_t)((p.rank + 16 * tiles - 1) / (16 * tiles));
+    hipLaunchKernelGGL(kernel, grid(p.inner_tiles, p.splits, parts * (uint32_t)p.slots, a.near), dim3(kLoraThreads), 0,
+                       s, a);
   };
   if (p.rank <= 16)
     inner(lora_inner_kernel<WHOLE, 1, CI>, 1);
@@ -467,8 +491,7 @@ hipError_t launch(const LoraArgs &a, const LoraPlan &p, hipStream_t s) {
   else
     inner(lora_inner_kernel<WHOLE, 4, CI>, 4);
   const auto outer = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)p.outer_tiles, (unsigned)p.chunks, (unsigned)p.slots), dim3(kLoraThreads), 0, s,
-                       a);
+    hipLaunchKernelGGL(kernel, grid(p.outer_tiles, p.chunks, (uint32_t)p.slots, a.near), dim3(kLoraThreads), 0, s, a);
   };
   if (p.rank <= 16)
     outer(lora_outer_kernel<WHOLE, 1, true, CO>);

@@ -202,6 +202,7 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
   const wq::LoraPlan plan = wq::lora_plan(count, w, m);
   a.steps = plan.steps;
   a.slots = plan.slots;
+  a.near = plan.near;
   memcpy(a.splits_to, plan.splits_to, sizeof a.splits_to);
   memcpy(a.chunks_to, plan.chunks_to, sizeof a.chunks_to);
   a.chunk = plan.chunk;

@@ -6,7 +6,13 @@ namespace wq {
 
 namespace {
 
-constexpr int64_t kLongWork = 768, kLongSplits = 4, kBlockWork = 2048;
+constexpr int64_t kLongWork = 768, kLongSplits = 4, kNearRows = 2048, kMostNearRows = 1 << 20;
+
+// Workgroups that the outputs of rows in succession are cut for, about four a
+// CU: 4001 rows of the projections below, rank 64, 62 us a call, with twice as
+// many 67 (9728 outputs from 1100 rows 44 and 51; half as many 9728 from 2700
+// rows 85 instead of 77).
+constexpr int64_t kBlockWork = 1024;
 constexpr int64_t kFewAdapters = 8, kShared = 4096, kMostSlots = 16;
 
 // Workgroups that K and the outputs are cut for where one stands for each row:
@@ -79,6 +85,12 @@ LoraPlan lora_plan(int32_t count, const wq_adapters *w, int64_t m) {
     const int64_t splits = splits_for(p.inner_tiles * count);
     piece = ((k + splits - 1) / splits + 255) / 256 * 256;
     p.slots = slots_for(m, adapters);
+    // Rows' pieces next to each other on one XCD: of many rows, x, read for
+    // each linear, and t, for each piece of the outputs, come from its L2 then.
+    // The projections above, rank 64, 4001 rows 60 -> 56 us, one linear 4096 to
+    // 2560 41 -> 36; below that many rows the XCDs get uneven shares: 1500 rows
+    // of the one linear 21 -> 25.
+    p.near = m >= kNearRows && m <= kMostNearRows;
   }
   p.steps = (int32_t)(piece / 32);
   p.chunk = (int32_t)cut(count, w, &wq_adapters::n, p.outer_tiles, 256, p.whole ? work(m) : kBlockWork, INT32_MAX);

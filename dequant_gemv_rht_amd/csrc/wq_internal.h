@@ -243,6 +243,7 @@ struct LoraArgs {
   const int32_t *ids;
   int32_t count, m;
   int32_t steps, chunk;         // 32s of K of a workgroup (first kernel); outputs, a multiple of 256 (second)
+  int32_t near;                 // pieces of some rows next to each other on one XCD
   int32_t slots;                // workgroups that share the groups of some rows in succession
   uint32_t splits_to[kMaxBatch], chunks_to[kMaxBatch];   // pieces of K, of the outputs, of linears 0 .. i together
 };
@@ -251,6 +252,7 @@ constexpr int kLoraSplits = 8;  // at most
 struct LoraPlan {
   bool whole;                   // a workgroup for each row, or for rows in succession
   int64_t inner_tiles, outer_tiles;
+  bool near;                    // pieces of some rows next to each other on one XCD
   int32_t steps, chunk, slots, rank;    // the largest rank
   uint32_t splits, chunks;      // of all linears
   uint32_t splits_to[kMaxBatch], chunks_to[kMaxBatch];

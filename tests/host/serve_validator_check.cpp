@@ -119,6 +119,9 @@ int main() {
           expect(p.inner_tiles * p.splits * p.slots * 2 <= wq::kMaxGroups256 && p.splits <= 65535 && p.chunks <= 65535 &&
                      p.outer_tiles * p.chunks * p.slots <= wq::kMaxGroups256 && p.slots >= 1 && (p.slots == 1 || !p.whole),
                  "launch", p.inner_tiles, p.chunks);
+          expect(!p.near || (!p.whole && p.inner_tiles <= 8 * 65535 && p.splits * p.slots * 2 <= 65535 &&
+                             p.chunks * p.slots <= 65535),
+                 "launch by XCD", p.inner_tiles, p.chunks);
           before = ws;
         }
       }

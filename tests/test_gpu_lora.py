@@ -81,6 +81,21 @@ def test_few_and_many_adapters(m, count, kind):
     check(y, *O.lora(a, b, x, ids, base), False, "y")
 
 
+@pytest.mark.parametrize("m,count,rank", [(2047, 3, 16), (2048, 3, 16), (2049, 40, 72), (2500, 300, 128), (4097, 2, 24)])
+def test_many_rows(m, count, rank):
+    rng = np.random.default_rng(m)
+    ids = ids_of("runs" if count < 10 else "some", rng, m, count).astype(np.int32)
+    a, b, xs, bases, want = [], [], [], [], []
+    x = None
+    for n, f32 in ((300, False), (33, True), (512, False)):
+        A, B, X, base = make(rng, count, rank, 256, n, m, f32)
+        x = X if x is None else x
+        a.append(dev(A)), b.append(dev(B)), xs.append(dev(x)), bases.append(dev(base))
+        want.append((O.lora(A, B, x, ids, base), f32))
+    for y, (w, f32) in zip(dq.wq_lora(a, b, xs, dev(ids), bases), want):
+        check(y, *w, f32, "y")
+
+
 def test_several_linears_strides_and_in_place():
     rng = np.random.default_rng(5)
     m, count = 37, 4
