@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
     alignas(16) unsigned long long sums[kBins];
     alignas(16) uint32_t counts[kBins];
     unsigned long long sum;
-    uint32_t finite, where;
+    uint32_t nonzero, where;
   };
   __shared__ Bins both[2];
   __shared__ float tops[2][kWaves];
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
   }
   if (tid < 2) {
     both[tid].sum = 0;
-    both[tid].finite = 0;
+    both[tid].nonzero = 0;
     both[tid].where = 0xFFFFFFFFu;
   }
   int turn = 0;
@@ -270,6 +270,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
     if (item + (int)gridDim.x < items) fetch(item + gridDim.x, next, next_s);
     if (counts_in) {
       uint64_t sum = 0;
+      uint32_t nonzero = 0;   // of the wave
       const bool counts = s.top_k < a.vocab;
       // eight at a time: a table entry of one waits behind the sums of none
 #pragma unroll
@@ -283,6 +284,9 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += w[e];
         if (!s.cuts) continue;
+        if (counts)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) nonzero += __popcll(__ballot(w[e] != 0));
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (bin_of(p[e]) < kBins) {
@@ -291,13 +295,10 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
           }
       }
       sum = wave_sum(sum);
-      if (lane == 0) atomicAdd(&sh.sum, (unsigned long long)sum);
-    }
-    if (!s.greedy && s.top_k < a.vocab) {
-      uint32_t finite = 0;   // of the wave
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) finite += __popcll(__ballot(v[i] > -INFINITY));
-      if (lane == 0) atomicAdd(&sh.finite, finite);
+      if (lane == 0) {
+        atomicAdd(&sh.sum, (unsigned long long)sum);
+        if (counts) atomicAdd(&sh.nonzero, nonzero);
+      }
     }
     __syncthreads();
     if (wave == turn % kWaves) {
@@ -307,10 +308,10 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
         head.best = (uint64_t)key_of(most) << 32 | (uint32_t)~((item - r * a.parts) * kPart + sh.where);
         head.sum = sh.sum;
         head.power = counts_in ? (int32_t)sc.power : kFarPart;   // no bins
-        head.finite = sh.finite;
+        head.nonzero = sh.nonzero;
         a.heads[item] = head;
         sh.sum = 0;
-        sh.finite = 0;
+        sh.nonzero = 0;
         sh.where = 0xFFFFFFFFu;
       }
       if (counts_in && s.cuts) {
@@ -656,8 +657,12 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     all = wave_sum(whole[0] + whole[1]);
   }
   if (!passes && set.cuts) {
-    const uint32_t finite = wave_sum((lane < parts ? head[0].finite : 0) + (lane + 64 < parts ? head[1].finite : 0));
-    const bool counting = (uint32_t)set.top_k < finite;
+    // top-k matters if it leaves out a logit whose weight is not 0: parts so far
+    // below the row's that theirs are have none, the others at most their own
+    uint32_t nonzero = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) nonzero += by[h] < a.unit + 2 ? head[h].nonzero : 0;
+    const bool counting = (uint32_t)set.top_k < wave_sum(nonzero);
     // the row's bins: a thread one bin of some parts
     {
       const int j = tid & (kBins - 1);

@@ -269,7 +269,7 @@ struct SamplePart {
   uint64_t best;                // largest key, complement of its first index
   uint64_t sum;                 // of weights, under `power`
   int32_t power;                // kFarPart: weights not summed
-  uint32_t finite;
+  uint32_t nonzero;             // weights that are not 0, where top-k is asked for
 };
 constexpr uint32_t kGivenHeat = 1, kGivenTopK = 2, kGivenTopP = 4, kGivenMinP = 8;
 struct SampleArgs {

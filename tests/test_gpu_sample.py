@@ -126,6 +126,16 @@ def test_odd_settings():
     check(x, np.full(6, 0.4, np.float32), min_p=np.array([math.nan, -1.0, math.inf, 1e-30, 1 - 2 ** -24, 1.0]))
 
 
+@pytest.mark.parametrize("temperature", [0.02, 0.05, 0.1, 0.15])
+def test_low_temperatures(temperature):
+    """top-k's last tokens far below the largest, some of them of no weight."""
+    rng = np.random.default_rng(6)
+    x = logits_of(rng, 24, 40000, 2.0, False)
+    x[:, 100:112] += rng.uniform(0, 6, (24, 12)).astype(np.float32)
+    for k in (1, 5, 12, 50, 400, 20000):
+        check(x, rng.random(24).astype(np.float32), temperature=temperature, top_k=k, top_p=np.float32([1.0, 0.9] * 12))
+
+
 def test_wide_open():
     """Many tokens within a millionth of each other's chance: the borders need the sums' 64 bits."""
     rng = np.random.default_rng(2)
