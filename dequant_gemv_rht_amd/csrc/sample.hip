@@ -14,9 +14,10 @@
 // finds in which bin a cut lies, fetches that bin's logits alone (from the
 // parts that have any), finds the cut among them, and with it every part's
 // sum of what is kept; the part in which the sum passes u times all of it is
-// read again, token by token.  Rows for which that does not do (a cut below
-// the bins, more logits in its bin than fit in LDS, logits beyond 2^13 powers
-// of two, temperatures near infinity) are searched in as many passes as it takes.
+// read again, token by token.  A cut below the bins lies in one more, of all
+// weights that are left (2^-32 to 2^-45 of the largest).  Rows for which that
+// does not do (more logits in a cut's bin than fit in LDS, logits beyond 2^13
+// powers of two, temperatures near infinity) take several passes over all.
 //
 // The first launch is bound by vector instructions, 33 for each 64 logits,
 // six of them in fp64 or converting to and from it, and by LDS atomics where
@@ -37,6 +38,8 @@ namespace {
 
 constexpr uint32_t kNoKey = 0x007FFFFFu;     // of -infinity
 constexpr int kBins = kSampleBins;
+constexpr int kBelow = kBins;                // all weights below the bins, down to a unit's half
+constexpr int kNoBin = kBins + 1;
 constexpr int kPart = kSamplePart;
 constexpr int kPartThreads = 512;
 constexpr int kEach = kPart / kPartThreads;  // logits of a thread
@@ -645,7 +648,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   // list, the logits of that bin
   uint32_t cut = 0, last = 0;
   uint64_t ties = ~0ull, all = 0, whole[2];   // sum of the weights kept; of a part's
-  int bin = kBins, size = 0, by[2];           // by: how far a part's powers are below the row's (64: too far)
+  int bin = kNoBin, size = 0, by[2];           // by: how far a part's powers are below the row's (64: too far)
   if (!passes) {
     const int power = (int)sc.power;
 #pragma unroll
@@ -721,13 +724,9 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         if (yes <= cut) continue;
         cut = yes;
         ties = ~0ull;
-        at = bin_of(split(value_of(yes), sc));
-        if (at >= kBins) {
-          passes = true;
-          break;
-        }
+        at = min(bin_of(split(value_of(yes), sc)), kBelow);
       } else {
-        if (bin == kBins) continue;
+        if (bin == kNoBin) continue;
         // of equal ones at the cut the first by index
         __syncthreads();
         if (tid == 0) sh.list_size = 0;   // (size has it)
@@ -748,10 +747,6 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         for (int j = 0; j < kBins; j += 64) at += __popcll(__ballot(bins[j + lane] < want));
         above = at ? bins[at - 1] : 0;
         if (at >= bin) {
-          if (bin == kBins) {
-            passes = true;
-            break;
-          }
           // among top-k's list
           at = bin;
           const uint64_t w = weight_of(value_of(cut)), high = all - ties * w;
@@ -772,10 +767,11 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int own = at - 8 * by[h];
-          const bool in = by[h] < 64 && own >= 0;
-          const uint64_t *sums = part_sums + (int64_t)(in ? lane + 64 * h : 0) * kBins + (in ? own : 0);
-          const uint64_t up_to = *sums, before = *(in && own ? sums - 1 : sums);
-          wanted[h] = __ballot(in && (own ? up_to != before : up_to != 0));
+          const bool in = at == kBelow ? by[h] < a.unit + 2 : by[h] < 64 && own >= 0;
+          const uint64_t *sums = part_sums + (int64_t)(in ? lane + 64 * h : 0) * kBins;
+          const uint64_t binned = sums[min(max(own, 0), kBins - 1)], before = sums[max(own - 1, 0)];
+          const uint64_t up_to = at == kBelow ? head[h].sum : binned;
+          wanted[h] = __ballot(in && (own > 0 ? up_to != before : up_to != 0));
         }
         __syncthreads();
         // The bin's logits are those from `from_value` up to `to_value`, whose
@@ -784,13 +780,14 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         float from_value = 0.0f, to_value = 0.0f;
 #pragma unroll 1
         for (int edge = 0; edge < 2; ++edge) {
-          const uint32_t guess = key_of((float)(((double)(8 - at + edge) * 0.125 + sc.power) / sc.per));
+          const int lowest = edge ? at - 1 : at == kBelow ? 8 * (a.unit + 2) : at;   // the bin that starts there
+          const uint32_t guess = key_of((float)(((double)(8 - lowest) * 0.125 + sc.power) / sc.per));
           uint32_t no = kNoKey, yes = top + 1;
 #pragma unroll 1
           for (int turn = 0; yes - no > 1; ++turn) {
             const bool many = turn == 0 && guess > kNoKey + 64 && guess <= top;
             const uint32_t key = many ? guess - 32 + (uint32_t)lane : no + (yes - no) / 2;
-            const uint64_t there = __ballot(key > top || bin_of(split(value_of(key), sc)) <= at - edge);
+            const uint64_t there = __ballot(key > top || bin_of(split(value_of(key), sc)) <= lowest);
             if (many) {
               if (there && !(there & 1)) {
                 yes = guess - 32 + (uint32_t)(__ffsll((unsigned long long)there) - 1);
@@ -866,6 +863,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         bin = at;
       }
       if (stage == kMinP) continue;
+      if (stage < kPlace && at == kBelow && (size == 0 || (stage == kTopK && want - above >= (uint64_t)size))) {
+        over = sh.sums[kBins - 1];   // (all that has a weight)
+        continue;
+      }
       // The value at which the sum over falling values (keys, or complements
       // of the indices at the cut), of 1 or of weights, of the list reaches
       // `want`, and the sum above it; if it never does, the lowest.
@@ -984,7 +985,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     return;
   }
   // what is kept of each part: a part's sum before the bin, and what the list has
-  if (bin < kBins) {
+  if (bin < kNoBin) {
     uint64_t before[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -58,15 +58,13 @@ def lora(a, b, x, ids, base, scales=None):
     return y, off
 
 
-def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
-    """One row -> (id, logprob)."""
+def kept(logits, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row's tokens that can be drawn, by index, and their weights (the largest 1); temperature above 0."""
     x = np.asarray(logits, dtype=np.float64)
     place = np.flatnonzero(x > -math.inf)          # neither NaN nor -infinity
-    if not len(place):
-        return -1, -math.inf
     place = place[np.lexsort((place, -x[place]))]
-    if not temperature > 0:
-        return int(place[0]), 0.0
+    if not len(place):
+        return place, np.zeros(0)
     top = x[place[0]]
     with np.errstate(over="ignore", invalid="ignore"):
         w = np.where(x[place] == top, 1.0, np.exp((x[place] - top) / float(temperature)))
@@ -82,7 +80,17 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         keep = w >= min(float(min_p), 1.0)
         place, w = place[keep], w[keep]
     order = np.argsort(place)
-    place, w = place[order], w[order]
+    return place[order], w[order]
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """One row -> (id, logprob)."""
+    x = np.asarray(logits, dtype=np.float64)
+    if not (x > -math.inf).any():
+        return -1, -math.inf
+    if not temperature > 0:
+        return int(np.argmax(np.where(np.isnan(x), -math.inf, x))), 0.0
+    place, w = kept(logits, temperature, top_k, top_p, min_p)
     up_to = np.cumsum(w)
     u = min(max(float(u), 0.0), 1.0) if u == u else 0.0
     i = min(int(np.searchsorted(up_to, u * up_to[-1], side="right")), int(np.flatnonzero(w)[-1]))

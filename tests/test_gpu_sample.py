@@ -136,6 +136,39 @@ def test_low_temperatures(temperature):
         check(x, rng.random(24).astype(np.float32), temperature=temperature, top_k=k, top_p=np.float32([1.0, 0.9] * 12))
 
 
+@pytest.mark.parametrize("powers", [(32.2, 33.0), (31.0, 36.0), (33.0, 43.0), (44.0, 52.0), (60.0, 90.0)])
+def test_cuts_among_small_weights(powers):
+    """One large weight, 8000 of 2^-31 to 2^-90 in two of the row's parts, cuts among them and the draw on both sides."""
+    rng = np.random.default_rng(int(powers[0] * 10))
+    x = np.full((4, 20000), -np.inf, np.float32)
+    x[:, 9000] = 3.0
+    x[:, 3000:7000] = 3.0 - math.log(2.0) * rng.uniform(*powers, (4, 4000))
+    x[:, 15000:19000] = 3.0 - math.log(2.0) * rng.uniform(*powers, (4, 4000))
+    x[3, 15000:19000] = x[3, 3000]   # equal ones
+    u = np.array([0.0, 0.5, 1 - 2.0 ** -15, 1 - 2.0 ** -18], np.float32)
+    for kw in (dict(top_k=1), dict(top_k=2), dict(top_k=50), dict(top_k=5000), dict(top_k=8001), dict(top_k=9000),
+               dict(top_p=1 - 2.0 ** -24), dict(top_p=1 - 2.0 ** -22), dict(min_p=2.0 ** -33.5), dict(min_p=1e-30),
+               dict(top_k=5000, top_p=1 - 2.0 ** -23), dict(top_k=8001, top_p=1 - 2.0 ** -24, min_p=2.0 ** -33),
+               dict(top_k=6000, min_p=1e-13)):
+        say("sample", powers, kw)
+        ids, logp = dq.wq_sample(dev(x), dev(u), **{n: dev(np.full(4, v, np.int32 if n == "top_k" else np.float32))
+                                                    for n, v in kw.items()})
+        kw = {n: v if n == "top_k" else float(np.float32(v)) for n, v in kw.items()}
+        for r, (i, lp) in enumerate(zip(ids.tolist(), logp.tolist())):
+            place, w = O.kept(x[r], **kw)
+            at = np.flatnonzero(place == i)
+            assert len(at) == 1, f"row {r}: token {i} is not kept ({kw})"
+            # A weight is off by 2^-34 of itself and half of 2^-44 of the
+            # largest at most, so a sum of the n kept by 2^-34 of itself and
+            # n 2^-45, and the draw, u of all of them, by as much: the token's
+            # share of the sum lies within twice that of the draw.
+            off = 2 * (2.0 ** -34 * w.sum() + len(w) * 2.0 ** -45)
+            draw, after = float(u[r]) * w.sum(), float(np.cumsum(w)[at[0]])
+            assert after - w[at[0]] - off <= draw <= after + off, f"row {r}: {i}, {after - draw} from the draw ({kw})"
+            want = math.log(w[at[0]] / w.sum())
+            assert abs(lp - want) <= abs(want) * 2.0 ** -23 + 1e-9, f"row {r}: {lp} for {want}"
+
+
 def test_wide_open():
     """Many tokens within a millionth of each other's chance: the borders need the sums' 64 bits."""
     rng = np.random.default_rng(2)
