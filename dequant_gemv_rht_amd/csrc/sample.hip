@@ -834,26 +834,14 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
             // one of each lane at a time (rarely more than a few)
 #pragma unroll 1
             for (uint64_t lanes; (lanes = __ballot(some)) != 0; some &= some - 1) {
-              const int place = from + __ffs((int)some) - 1;
-              const float l = logit<F32>(row, some ? place : 0);
               uint32_t to = 0;
               if (lane == 0) to = atomicAdd(&sh.list_size, (uint32_t)__popcll(lanes));
               const uint32_t i = (uint32_t)__builtin_amdgcn_readfirstlane((int)to) +
                                  __builtin_amdgcn_mbcnt_hi((uint32_t)(lanes >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)lanes, 0));
-              if (some && i < (uint32_t)kList) {
-                sh.list.keys[i] = __builtin_bit_cast(uint32_t, l);   // (the key later)
-                sh.list.places[i] = (uint32_t)place;
-              }
+              if (some && i < (uint32_t)kList) sh.list.places[i] = (uint32_t)(from + __ffs((int)some) - 1);
             }
           }
         }
-        __syncthreads();
-        if (sh.list_size <= (uint32_t)kList)
-          for (int i = tid; i < (int)sh.list_size; i += kRowThreads) {
-            const float l = __builtin_bit_cast(float, sh.list.keys[i]);
-            sh.list.keys[i] = key_of(l);
-            sh.list.weights[i] = weight_of(l);
-          }
         __syncthreads();
         if (sh.list_size > (uint32_t)kList) {
           passes = true;
@@ -861,6 +849,13 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
         }
         size = (int)sh.list_size;
         bin = at;
+#pragma unroll 1
+        for (int i = tid; i < size; i += kRowThreads) {
+          const float l = logit<F32>(row, (int64_t)sh.list.places[i]);
+          sh.list.keys[i] = key_of(l);
+          sh.list.weights[i] = weight_of(l);
+        }
+        __syncthreads();
       }
       if (stage == kMinP) continue;
       if (stage < kPlace && at == kBelow && (size == 0 || (stage == kTopK && want - above >= (uint64_t)size))) {

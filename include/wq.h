@@ -564,14 +564,14 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
  * Weights are counted in 2^-44 of a power of two near the largest (2^-43 for
  * vocab above 2^18, 2^-42 above 2^19), each within 2^-34 of itself, and added
  * as whole numbers in 64 bits: the same inputs give the same token, whatever
- * the timing and whatever the other rows are.  Two launches; a row
- * with logits beyond 2^13 T, or with a cut around which more than 8192 logits
- * lie within an eighth of a power of two of w (2^-31 of the largest w and
- * below: that far down to 2^-46) takes several passes over its logits (about 0.1 ms more).  rows 0 does
- * nothing.  Errors (before anything is launched): WQ_E_ARG (also an output
- * that overlaps another array), WQ_E_ALIGN (int32 and fp32 arrays other than
- * logits need 4-byte alignment), WQ_E_UNSUPPORTED (vocab above 2^20, rows
- * above 2^20), WQ_E_WORKSPACE; WQ_E_HIP. */
+ * the timing and whatever the other rows are.  Two launches; a row with
+ * logits beyond 2^13 T, or with a cut around which more than 8192 logits lie
+ * within an eighth of a power of two of w (from 2^-31 of the largest w down:
+ * within all that is left), takes several passes over its logits (about 0.1
+ * ms more).  rows 0 does nothing.  Errors (before anything is launched):
+ * WQ_E_ARG (also an output that overlaps another array), WQ_E_ALIGN (int32
+ * and fp32 arrays other than logits need 4-byte alignment), WQ_E_UNSUPPORTED
+ * (vocab above 2^20, rows above 2^20), WQ_E_WORKSPACE; WQ_E_HIP. */
 size_t wq_sample_workspace(int64_t rows, int64_t vocab);
 wq_status wq_sample(const void *logits, wq_dtype dtype, int64_t rows, int64_t vocab, int64_t ldl, const float *u,
                     const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
