@@ -1070,8 +1070,14 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   }
   a.ids[r] = id;
   if (a.logprobs) {
-    const double x = fma((double)logit<F32>(row, id), sc.per, -sc.power);
-    a.logprobs[r] = (float)(x * 0.69314718055994530942 - log(ldexp((double)all, -a.unit)));
+    const float l = logit<F32>(row, id);
+    const double x = fma((double)l, sc.per, -sc.power);
+    // more than half of the sum: from the others', whose digits the logarithm
+    // of the chance would lose
+    const uint64_t w = weight_of(l);
+    const bool most = w >= all / 2;
+    const double ln = log1p(most ? -(double)(w < all ? all - w : 0) / (double)all : ldexp((double)all, -a.unit) - 1.0);
+    a.logprobs[r] = (float)(most ? ln : x * 0.69314718055994530942 - ln);
   }
 }
 

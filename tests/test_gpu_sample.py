@@ -169,6 +169,33 @@ def test_cuts_among_small_weights(powers):
             assert abs(lp - want) <= abs(want) * 2.0 ** -23 + 1e-9, f"row {r}: {lp} for {want}"
 
 
+@pytest.mark.parametrize("gap", [2.0, 5.0, 9.0, 14.0, 18.0])
+def test_chances_near_one(gap):
+    """A token that is almost all of the sum: its log chance is as exact as the others' sum."""
+    rng = np.random.default_rng(int(gap))
+    x = rng.uniform(-1, 1, (12, 30000)).astype(np.float32) - 12
+    x[:, 5:9] += 12
+    x[np.arange(12), rng.integers(0, 30000, 12)] = np.float32(1 + gap)
+    u = np.full(12, 0.5, np.float32)
+    for kw in (dict(), dict(top_k=1), dict(top_k=3), dict(top_p=0.5), dict(top_p=0.99999), dict(min_p=0.5), dict(top_k=50, min_p=1e-9)):
+        ids, logp = dq.wq_sample(dev(x), dev(u), **{n: dev(np.full(12, v, np.int32 if n == "top_k" else np.float32))
+                                                    for n, v in kw.items()})
+        kw = {n: v if n == "top_k" else float(np.float32(v)) for n, v in kw.items()}
+        for r, (i, lp) in enumerate(zip(ids.tolist(), logp.tolist())):
+            place, w = O.kept(x[r], **kw)
+            at = np.flatnonzero(place == i)[0]
+            # The others' sum s is off by 2^-34 of itself and n 2^-45 (a
+            # weight: 2^-34 of itself, half of 2^-44 of the largest), ln(1 - s /
+            # all) by twice that at most while s is below half of all, and
+            # by 2^-33 of itself through all; then the rounding to 32 bits.
+            s = w.sum() - w[at] if len(w) > 1 else 0.0
+            want = math.log1p(-s / w.sum())
+            assert w[at] > s
+            assert abs(lp - want) <= 2 * (s * 2.0 ** -34 + (len(w) - 1) * 2.0 ** -45) + abs(want) * (2.0 ** -33 + 2.0 ** -24), \
+                f"row {r}: {lp} for {want} ({kw})"
+            assert len(w) > 1 or lp == 0
+
+
 def test_wide_open():
     """Many tokens within a millionth of each other's chance: the borders need the sums' 64 bits."""
     rng = np.random.default_rng(2)
