@@ -65,6 +65,12 @@ def test_pages_run_out(left):
     check(16, pages, table, lens, new, free[: left + 4], 4, int(new.sum()))
 
 
+def test_pages_not_given_out_stay_in_the_list():
+    """One page left: the first needs two, the second none and the third one; used counts what was given out."""
+    check(16, 8, [[0, -1, -1], [1, -1, -1], [2, -1, -1]], [16, 3, 16], [17, 1, 1], [5], 0, 19)
+    check(16, 8, [[1, -1, -1], [2, -1, -1], [0, -1, -1]], [3, 16, 16], [1, 1, 17], [5], 0, 19)
+
+
 @pytest.mark.parametrize("used", [-1, -2 ** 31, 11, 2 ** 31 - 1])
 def test_used_outside_the_list(used):
     check(16, 50, [[1, 2], [3, 4]], [16, 5], [1, 2], list(range(10, 20)), used, 3)

@@ -91,3 +91,10 @@ def test_sample_against_enumeration(seed):
     for u in (0.05, 0.5, 0.95):
         i, lp = O.sample(x, u, temperature=t, top_k=k, top_p=p, min_p=m)
         assert abs(lp - math.log(want[i])) < 1e-12
+
+
+def test_slots_used_counts_pages_given_out():
+    """One page left, asked for by a sequence that needs two, before one that needs none."""
+    out = O.kv_slots(16, 8, np.array([[0, -1, -1], [1, -1, -1]], np.int32), np.array([16, 3], np.int32),
+                     np.array([17, 1], np.int32), np.array([5], np.int32), 0, 18)
+    assert out[5].tolist() == [0] and out[3].tolist() == [16, 4] and out[6].tolist() == [[0, -1, -1], [1, -1, -1]]
