@@ -655,7 +655,10 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     for (int h = 0; h < 2; ++h) {
       const bool in = lane + 64 * h < parts && head[h].power != kFarPart && power - head[h].power < 64;
       by[h] = in ? power - head[h].power : 64;
-      whole[h] = in ? head[h].sum >> by[h] : 0;
+      // Under the row's power weights below half a unit are 0, the sum of
+      // thousands is not: it counts, but where top-k is asked for.  There only
+      // what is not 0 is sure to be kept, so a part needs a whole unit.
+      whole[h] = in && (by[h] <= a.unit || set.top_k >= n) ? head[h].sum >> by[h] : 0;
     }
     all = wave_sum(whole[0] + whole[1]);
   }
@@ -1004,15 +1007,26 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
     whole[1] = sh.kept[lane + 64];
   }
   // the part in which the sum passes the target
-  uint64_t up[2], start = 0;
+  uint64_t up[2], start;
   up[0] = wave_scan(whole[0], (uint64_t)0, Sum());
   up[1] = parts > 64 ? lane_value(up[0], 63) + wave_scan(whole[1], (uint64_t)0, Sum()) : 0;
   all = lane_value(parts > 64 ? up[1] : up[0], 63);
   uint64_t target = (uint64_t)floor(set.u * (double)all);
-  if (target >= all) target = all - 1;
+  const bool end = target >= all;   // u = 1: the last one kept
+  if (end) target = all - 1;
   const int h = parts > 64 && lane_value(up[0], 63) <= target ? 1 : 0;
   const int l = __ffsll((unsigned long long)__ballot(up[h] > target)) - 1, part = l + 64 * h;
   start = lane_value(up[h] - whole[h], l);
+  // In a row that is open to the end the part's logits are weighed as the first
+  // launch did, under the part's own power, which adds up to the sum that the
+  // part was chosen by: under the row's power each of them may be 0.  With a
+  // cut what it was chosen by are bins of 2^-32 and more and the list's weights
+  // under the row's power, with top-k alone a part's largest is a unit or more.
+  const int below = bin < kNoBin || set.top_k < n ? 0 : (int)lane_value((uint32_t)(h ? by[1] : by[0]), l);
+  Scale own = sc;
+  own.power -= below;
+  own.shift += below;
+  target = end ? ~0ull : (target - start) << below;
   __syncthreads();   // (the table, where no list was made)
   // its logits, some in a row to a thread
   const int first = part * kPart + kMine * tid, to = min(n, (part + 1) * kPart);
@@ -1030,21 +1044,21 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float x = i ? v[4 + e] : v[e];
-      const uint64_t w = weight_of(x);
+      const uint64_t w = counted(split(x, own), own, sh.table);
       const bool k = from + i + e >= first && from + i + e < to && taken(x, from + i + e) && w;
       sum += k ? w : 0;
       final = k ? from + i + e : final;
     }
   }
   // the wave and the thread in which the sum passes the target; where
-  // rounding at other places (of the parts' sums, of the weights) leaves none,
-  // the last kept
+  // rounding at other places (of the parts' sums, of the weights under the
+  // row's power) leaves none, or u is 1, the last kept
   uint64_t at = wave_scan(sum, (uint64_t)0, Sum());
   __syncthreads();
   if (lane == 63) sh.tmp[tid >> 6] = at;
   if (tid == 0) sh.found = -1;
   __syncthreads();
-  at += start - sum;
+  at -= sum;
 #pragma unroll 1
   for (int w = 0; w < tid >> 6; ++w) at += sh.tmp[w];
   const uint64_t owner = __ballot(at <= target && at + sum > target);
@@ -1053,17 +1067,19 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   const bool none = sh.found < 0;
   int id = -1;
   if (none) {
-    const uint64_t end = wave_max((uint32_t)(final + 1));
-    if (lane == 0) sh.tmp[tid >> 6] = end;
+    const uint64_t last_here = wave_max((uint32_t)(final + 1));
+    if (lane == 0) sh.tmp[tid >> 6] = last_here;
     __syncthreads();
     for (int w = 0; w < kRowThreads / 64; ++w) id = max(id, (int)sh.tmp[w] - 1);
+    if (id < 0) id = (int)~(uint32_t)best;   // no place outside the row, whatever the sums
     if (tid) return;
   } else {
     if (!owner) return;
     // the thread's logits, one to a lane
     const int o = __ffsll((unsigned long long)owner) - 1, place = __builtin_amdgcn_readlane(first, o) + lane;
     const float x = logit<F32>(row, min(place, n - 1));
-    const uint64_t w = lane < kMine && place < to && taken(x, place) ? weight_of(x) : 0, up = lane_value(at, o) + wave_scan(w, (uint64_t)0, Sum());
+    const uint64_t w = lane < kMine && place < to && taken(x, place) ? counted(split(x, own), own, sh.table) : 0;
+    const uint64_t up = lane_value(at, o) + wave_scan(w, (uint64_t)0, Sum());
     const uint64_t passed = __ballot(up > target);
     id = __builtin_amdgcn_readlane(place, __ffsll((unsigned long long)passed) - 1);
     if (lane) return;
