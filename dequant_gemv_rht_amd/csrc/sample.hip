@@ -45,7 +45,8 @@ constexpr int kPartThreads = 512;
 constexpr int kEach = kPart / kPartThreads;  // logits of a thread
 constexpr int kMaxParts = (1 << 20) / kPart;
 constexpr int kTable = 1024;
-constexpr double kFar = 8192.0;              // largest power of two that the bins take
+constexpr double kFar = 8192.0;              // largest power of two of a row's largest that the bins take
+constexpr double kFarOfPart = kFar + 64.0;   // of a part's: one further down has no weight beside a row's within kFar
 
 template <bool F32>
 __device__ __forceinline__ float logit(const void *row, int64_t i) {
@@ -144,7 +145,7 @@ __device__ __forceinline__ Scale scale(double per, double power, int unit) {
 
 // What scale() is for: x of the largest logit, and of -infinity's stand-in, in
 // the range of the low bits.
-__device__ __forceinline__ bool near(double per, double most) { return fabs(most) < kFar && per > 1e-30; }
+__device__ __forceinline__ bool near(double per, double most, double far) { return fabs(most) < far && per > 1e-30; }
 
 struct Split {
   uint32_t hi, lo;
@@ -268,7 +269,7 @@ __global__ __launch_bounds__(kPartThreads) void sample_parts_kernel(SampleArgs a
       atomicMin(&sh.where, __builtin_bit_cast(uint32_t, top));
     }
     const double per = 1.4426950408889634074 / (double)s.heat, power = (double)most * per;
-    const bool counts_in = !s.greedy && most > -INFINITY && near(per, power);
+    const bool counts_in = !s.greedy && most > -INFINITY && near(per, power, kFarOfPart);
     const Scale sc = scale(per, floor(power), a.unit);
     if (item + (int)gridDim.x < items) fetch(item + gridDim.x, next, next_s);
     if (counts_in) {
@@ -641,7 +642,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_rows_kernel(SampleArgs a) 
   const Scale sc = scale(per, floor(most), a.unit);
   // as the first launch counted it: borders of equal weights are exact
   const auto weight_of = [&](float l) { return counted(split(l, sc), sc, sh.table); };
-  bool passes = !near(per, most);
+  bool passes = !near(per, most, kFar);
 
   // what is kept: keys above `cut`, and of those at it the ones whose index's
   // complement is `last` or more; all of the bins before `bin` and, in the
