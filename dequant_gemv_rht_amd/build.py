@@ -64,7 +64,7 @@ def build_binding() -> str:
               "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
               *(a for i in inc for a in ("-isystem", i)), os.path.join(CSRC, BINDING), f"-L{lib}", "-ltorch_python",
-              "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_hip", f"-Wl,-rpath,{lib}"], BINDING_LIB, f"{BINDING}: g++")
+              "-ltorch", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip", f"-Wl,-rpath,{lib}"], BINDING_LIB, f"{BINDING}: g++")
     return BINDING_LIB
 
 

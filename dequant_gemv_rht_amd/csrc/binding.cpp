@@ -14,6 +14,8 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/csrc/utils/object_ptr.h>
 
+#include <ATen/EmptyTensor.h>
+#include <ATen/hip/HIPContextLight.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
@@ -327,8 +329,10 @@ class Place {
     TORCH_CHECK_VALUE(t.device() == device_, name, " must be on ", device_, ", got ", t.device());
     return t;
   }
+  // at::empty without its dispatch, on the device made current
   at::Tensor make(at::IntArrayRef sizes, at::ScalarType type) const {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(device_));
+    return at::Tensor(at::detail::empty_generic(sizes, at::cuda::getCUDADeviceAllocator(),
+                                                c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
   }
   void *stream() const { return c10::hip::getCurrentHIPStream(device_.index()).stream(); }
 
@@ -378,14 +382,6 @@ PyObject *tuple_of(at::Tensor *t, Py_ssize_t n) {
   return r.release();
 }
 
-// the n elements of a new vector from `from` on (a view without the dispatcher's cost)
-at::Tensor part_of(const at::Tensor &whole, int64_t from, int64_t n) {
-  auto impl = c10::make_intrusive<at::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
-  impl->set_sizes_contiguous(at::IntArrayRef(&n, 1));
-  impl->set_storage_offset(from);
-  return at::Tensor(std::move(impl));
-}
-
 // kv_slots(page_size, pages, table, lens, new_tokens, free_pages, used, tokens, out): out None or six tensors
 PyObject *kv_slots(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -415,15 +411,14 @@ PyObject *kv_slots(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!given) throw python_error();
     TORCH_CHECK_VALUE(PyTuple_GET_SIZE(given.get()) == 6, "out must be six tensors");
   }
-  int64_t total = 0, from[6];
   for (int i = 0; i < 6; ++i) {
-    from[i] = total;
-    total += (sizes[i] + 3) / 4 * 4;
-  }
-  const at::Tensor whole = given ? at::Tensor() : p.make({total}, at::kInt);   // new outputs share one allocation
-  for (int i = 0; i < 6; ++i) {
-    out[i] = given ? tensor(PyTuple_GET_ITEM(given.get(), i), names[i]) : part_of(whole, from[i], sizes[i]);
-    po[i] = static_cast<int32_t *>(vec(p, out[i], at::kInt, sizes[i], names[i]));
+    if (given) {
+      out[i] = tensor(PyTuple_GET_ITEM(given.get(), i), names[i]);
+      po[i] = static_cast<int32_t *>(vec(p, out[i], at::kInt, sizes[i], names[i]));
+    } else {   // a storage each: one that is resized later leaves the others alone
+      out[i] = p.make({sizes[i]}, at::kInt);
+      po[i] = static_cast<int32_t *>(out[i].data_ptr());
+    }
   }
   const wq_status st = slots_fn((int32_t)page_size, pages, static_cast<int32_t *>(table.data_ptr()),
                                 seqs > 1 ? table.stride(0) : table.size(1), table.size(1), plens, pnew, seqs, pfree, count,

@@ -1,0 +1,33 @@
+"""What the binding of the serving calls gives back: tensors of their own, and
+the library's status for what it refuses."""
+
+import pytest
+import torch
+
+import dequant_gemv_rht_amd as dq
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def slots(tokens=5, **kw):
+    args = dict(page_size=16, pages=9, table=torch.full((2, 3), -1, dtype=torch.int32, device="cuda"), lens=i32(0, 0),
+                new_tokens=i32(3, 2), free_pages=i32(4, 5, 6), used=i32(0), tokens=tokens)
+    return dq.wq_kv_slots(**{**args, **kw})
+
+
+WANT = [[64, 65, 66, 80, 81], [0, 1, 2, 0, 1], [0, 0, 0, 1, 1], [3, 2], [2, 4], [2]]
+
+
+@pytest.mark.parametrize("which", range(6))
+def test_slots_outputs_do_not_share_memory(which):
+    """One output that grows leaves the others alone."""
+    got = slots()
+    assert [t.tolist() for t in got] == WANT
+    assert len({t.untyped_storage().data_ptr() for t in got}) == 6
+    assert all(t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.nbytes for t in got)
+    got[which].resize_(40).fill_(-9)
+    assert [t.tolist() for i, t in enumerate(got) if i != which] == [w for i, w in enumerate(WANT) if i != which]
