@@ -382,6 +382,8 @@ PyObject *tuple_of(at::Tensor *t, Py_ssize_t n) {
   return r.release();
 }
 
+constexpr int64_t kMostRows = (int64_t)1 << 30;   // of a step (wq_kv_slots)
+
 // kv_slots(page_size, pages, table, lens, new_tokens, free_pages, used, tokens, out): out None or six tensors
 PyObject *kv_slots(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -415,6 +417,8 @@ PyObject *kv_slots(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (given) {
       out[i] = tensor(PyTuple_GET_ITEM(given.get(), i), names[i]);
       po[i] = static_cast<int32_t *>(vec(p, out[i], at::kInt, sizes[i], names[i]));
+    } else if (tokens > kMostRows) {   // the library refuses them: no memory for that
+      po[i] = nullptr;
     } else {   // a storage each: one that is resized later leaves the others alone
       out[i] = p.make({sizes[i]}, at::kInt);
       po[i] = static_cast<int32_t *>(out[i].data_ptr());

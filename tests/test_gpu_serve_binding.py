@@ -31,3 +31,13 @@ def test_slots_outputs_do_not_share_memory(which):
     assert all(t.storage_offset() == 0 and t.untyped_storage().nbytes() == t.nbytes for t in got)
     got[which].resize_(40).fill_(-9)
     assert [t.tolist() for i, t in enumerate(got) if i != which] == [w for i, w in enumerate(WANT) if i != which]
+
+
+@pytest.mark.parametrize("tokens", [(1 << 30) + 1, 1 << 40, 1 << 61, 1 << 62, (1 << 63) - 1])
+def test_slots_of_too_many_rows_are_refused_before_any_memory(tokens):
+    table, lens, free, used = torch.full((2, 3), -1, dtype=torch.int32, device="cuda"), i32(0, 0), i32(1), i32(0)
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    with pytest.raises(dq.WqError, match="tokens above 2") as e:
+        dq.wq_kv_slots(16, 9, table, lens, lens, free, used, tokens)
+    assert e.value.status == dq.WQ_E_UNSUPPORTED
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
