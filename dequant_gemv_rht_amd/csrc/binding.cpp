@@ -508,7 +508,7 @@ PyObject *lora(PyObject *, PyObject *const *a, Py_ssize_t n) {
   size_t bytes = 0;
   if (a[6] == Py_None) {
     bytes = lora_workspace_fn((int32_t)count, w, m);
-    if (bytes == (size_t)-1) return PyLong_FromLong(WQ_E_ARG);
+    if (bytes == (size_t)-1) bytes = 0;   // the call says what is wrong
     if (bytes) ws = p->make({(int64_t)bytes}, at::kByte);
   } else {
     ws = p->check(tensor(a[6], "workspace"), "workspace");
@@ -560,7 +560,7 @@ PyObject *sample(PyObject *, PyObject *const *a, Py_ssize_t n) {
   size_t bytes = 0;
   if (a[6] == Py_None) {
     bytes = sample_workspace_fn(l.rows, l.cols);
-    if (bytes == (size_t)-1) return PyLong_FromLong(WQ_E_UNSUPPORTED);
+    if (bytes == (size_t)-1) bytes = 0;   // the call says what is wrong
     if (bytes) ws = p.make({(int64_t)bytes}, at::kByte);
   } else {
     ws = p.check(tensor(a[6], "workspace"), "workspace");

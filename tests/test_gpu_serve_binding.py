@@ -41,3 +41,19 @@ def test_slots_of_too_many_rows_are_refused_before_any_memory(tokens):
         dq.wq_kv_slots(16, 9, table, lens, lens, free, used, tokens)
     assert e.value.status == dq.WQ_E_UNSUPPORTED
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+
+
+@pytest.mark.parametrize("rank,k,n,status,text", [(12, 128, 8, dq.WQ_E_UNSUPPORTED, "rank"), (136, 128, 8, dq.WQ_E_UNSUPPORTED, "rank"),
+                                                  (8, 192, 8, dq.WQ_E_ARG, "128"), (8, 128, 0, dq.WQ_E_ARG, "n=0")])
+def test_status_of_refused_adapters(rank, k, n, status, text):
+    half = lambda *s: torch.zeros(s, dtype=torch.float16, device="cuda")  # noqa: E731
+    with pytest.raises(dq.WqError, match=text) as e:
+        dq.wq_lora([half(2, rank, k)], [half(2, n, rank)], [half(3, k)], i32(0, 1, 1), [half(3, n)])
+    assert e.value.status == status
+
+
+@pytest.mark.parametrize("vocab,status,text", [(0, dq.WQ_E_ARG, "vocab=0"), ((1 << 20) + 1, dq.WQ_E_UNSUPPORTED, "2^20")])
+def test_status_of_refused_sampling(vocab, status, text):
+    with pytest.raises(dq.WqError) as e:
+        dq.wq_sample(torch.zeros((2, vocab), device="cuda"), torch.zeros(2, device="cuda"))
+    assert e.value.status == status and text in str(e.value)
