@@ -79,11 +79,12 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 }
 
 // exp(z) in fp64: 2^n exp(r), |r| <= ln 2 / 2, the series of exp up to
-// r^12 / 12! (its next term is below 2^-57 of the sum)
+// r^12 / 12! (its next term is below 2^-57 of the sum).  r takes off n ln 2 in
+// two parts: ln 2 rounded to fp32, n times which is exact, and what is left.
 __device__ __forceinline__ double exp64(double z) {
   if (!(z > -100.0)) return 0.0;   // below any unit
   const double n = rint(z * 1.4426950408889634074);
-  const double r = fma(-n, 1.9082149292705877e-10, fma(-n, 0.69314718036912381649, z));
+  const double r = fma(n, 1.904654299957767878e-9, fma(-n, (double)0.69314718055994530942f, z));
   double p = 1.0 / 479001600.0;
   p = fma(p, r, 1.0 / 39916800.0);
   p = fma(p, r, 1.0 / 3628800.0);
