@@ -16,8 +16,8 @@ from gpu_util import dev, say
 pytestmark = pytest.mark.gpu
 
 
-def check_near(x, u, **kw):
-    """Every row's token and log chance against what is kept in 64 bits."""
+def check_near(x, u, unit=44, **kw):
+    """Every row's token and log chance against what is kept in 64 bits; weights are counted in 2^-unit."""
     rows = len(x)
     ids, logp = dq.wq_sample(dev(x), dev(u), **{n: dev(np.full(rows, v, np.int32 if n == "top_k" else np.float32))
                                                 for n, v in kw.items()})
@@ -29,16 +29,16 @@ def check_near(x, u, **kw):
             up_to, total = np.cumsum(w), w.sum()
         at = np.flatnonzero(place == i)
         assert len(at) == 1, f"row {r}: token {i} is not kept ({kw})"
-        # A weight is off by 2^-34 of itself and half of 2^-44 of the largest
-        # at most, so a sum of the n kept by 2^-34 of itself and n 2^-45, and
-        # the draw, u of all of them, by as much; the log of a share by both
+        # A weight is off by 2^-34 of itself and half of a unit at most (the
+        # largest is one or more of 2^unit), so a sum of the n kept by 2^-34 of
+        # itself and n 2^-45 (unit 44), and the draw, u of all of them, by as much; the log of a share by both
         # sums' relative errors (all is at least 1), then a 32-bit rounding.
-        off = 2 * (2.0 ** -34 * total + len(w) * 2.0 ** -45)
+        off = 2 * (2.0 ** -34 * total + len(w) * 2.0 ** -(unit + 1))
         draw = (min(max(float(u[r]), 0.0), 1.0) if u[r] == u[r] else 0.0) * total
         mine, after = w[at[0]], float(up_to[at[0]])
         assert after - mine - off <= draw <= after + off, f"row {r}: {i}, {after - draw} from the draw ({kw})"
         want = math.log1p(-(total - mine) / total) if mine > total - mine else math.log(mine / total)
-        assert abs(lp - want) <= 2 * (2.0 ** -34 + len(w) * 2.0 ** -45) + abs(want) * (2.0 ** -33 + 2.0 ** -24), \
+        assert abs(lp - want) <= 2 * (2.0 ** -34 + len(w) * 2.0 ** -(unit + 1)) + abs(want) * (2.0 ** -33 + 2.0 ** -24), \
             f"row {r}: {lp} for {want} ({kw})"
     return ids.tolist()
 
@@ -58,7 +58,7 @@ def test_whole_parts_far_below_the_largest(powers, vocab, half):
         x[:, place] = 3.0
         say("sample", powers, vocab, half, place)
         ids = check_near(x, DRAWS)
-        if powers <= 54:   # 8192 of them are 2^13 of 2^-54 and more, a unit's 8: the ends of the row are drawn
+        if powers <= 54:   # 8192 of 2^-54 are 8 units: the ends of the row are drawn
             if place >= 8192:
                 assert ids[:3] == [0, 0, 0]
             if place < 8192:
@@ -80,6 +80,22 @@ def test_parts_each_at_a_power_of_its_own(powers):
     for kw in (dict(), dict(top_k=1), dict(top_k=30000), dict(top_k=vocab - 1), dict(min_p=1e-13)):
         say("sample", powers, kw)
         check_near(x, DRAWS, **kw)
+
+
+@pytest.mark.parametrize("powers", [43.0, 44.0, 47.0, 52.0])
+@pytest.mark.parametrize("place", [77, 600000, (1 << 20) - 1])
+def test_longest_row(place, powers):
+    """128 parts, weights in 2^-42: the large one in the first, in between and in the last."""
+    rows, vocab = len(DRAWS), 1 << 20
+    x = np.full((rows, vocab), np.float32(-math.log(2.0) * powers), np.float32)
+    x[:, place] = 0.0
+    say("sample", place, powers)
+    ids = check_near(x, DRAWS, 42)
+    if place >= 8192:   # 8192 of 2^-52 are 8 units
+        assert ids[:3] == [0, 0, 0]
+    if place < vocab - 8192:
+        assert ids[-2:] == [vocab - 1] * 2
+    check_near(x, DRAWS, 42, top_k=5)
 
 
 def test_low_temperatures_and_random_draws():
