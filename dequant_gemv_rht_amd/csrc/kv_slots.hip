@@ -2,13 +2,13 @@
 // sums over the sequences (rows, then pages), then one look-up for each row.
 //
 // Nothing to compute and little to move (12 bytes a row): the time is the
-// launch and three round trips to memory, 4.7 us for 64 sequences of one new
-// token and 5.9 for 1024 sequences with 44000 rows (an empty kernel takes
-// 2.2).  So it is one launch without anything between workgroups: a workgroup
-// takes kRows rows, adds up the sequences before them for itself (1024
-// sequences a turn, 8 KB from the caches), keeps a record for each sequence
-// that has rows among its own, and a maximum over the rows spreads the
-// records.  Sums in 32 bits that stop past the step's rows, by DPP moves: in
+// launch and three round trips to memory, 4.6 us for 64 sequences of one new
+// token and 5.9 for 1024 sequences with 44000 rows in a kernel trace (an empty
+// kernel takes 2.2).  So it is one launch without anything between workgroups:
+// a workgroup takes kRows rows, adds up the sequences before them for itself
+// (1024 sequences a turn, 8 KB from the caches), keeps a record for each
+// sequence that has rows among its own, and a maximum over the rows spreads
+// the records.  Sums in 32 bits that stop past the step's rows, by DPP moves: in
 // 64 bits and by shuffles the first of these took 5.6 us.  A new page's entry
 // of the table is written by the row that opens the page, and no workgroup
 // reads an entry that another writes: pages from the free list are looked up

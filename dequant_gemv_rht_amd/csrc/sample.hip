@@ -16,7 +16,7 @@
 // sum of what is kept; the part in which the sum passes u times all of it is
 // read again, token by token.  A cut below the bins lies in one more, of all
 // weights that are left (2^-32 to 2^-45 of the largest).  Rows for which that
-// does not do (more logits in a cut's bin than fit in LDS, logits beyond 2^13
+// does not do (more logits in a cut's bin than fit in LDS, a largest beyond 2^13
 // powers of two, temperatures near infinity) take several passes over all.
 //
 // The first launch is bound by vector instructions, 33 for each 64 logits,
@@ -26,8 +26,8 @@
 // once through its code, most of which then comes from the L2 line by line
 // (92 KB of unrolled code took 49 us for one row where 45 KB take 30): loops
 // there stay rolled, each piece of work has one place, and what a wave can
-// find out alone every wave does, without waiting for the others.  45 us for
-// 64 rows, 50 for 256: the row with the most open top-p, whose cut's bin holds
+// find out alone every wave does, without waiting for the others.  43 us for
+// 64 rows, 54 for 256: the row with the most open top-p, whose cut's bin holds
 // thousands of logits in all parts, which one CU reads again.
 #include "wq_internal.h"
 
@@ -166,7 +166,8 @@ __device__ __forceinline__ uint64_t counted(const Split &p, const Scale &s, cons
   return __builtin_bit_cast(uint64_t, c) - 0x4330000000000000ull;
 }
 
-// Eighths of a power of two: 0 and 1 are the largest's
+// Eighths of a power of two, downwards: the largest, x in [0, 1), is in one of
+// 1 to 8 (by rounding up to 1 in 0)
 __device__ __forceinline__ int bin_of(const Split &p) { return 8 - ((int)(p.hi - kShiftHigh) >> 5); }
 
 __device__ __forceinline__ double table_entry(int j) { return exp64((double)j * (0.69314718055994530942 / kTable)); }

@@ -514,9 +514,11 @@ typedef struct wq_adapters {
  * power of two of its row (22 bits), and y is rounded once.  Up to 32 rows,
  * or 256 with more than 8 adapters, rows with one adapter share its weights,
  * 16 at a time, wherever they stand; above, those among 32 (A) or 64 (B) rows
- * in succession do, so rows of one request should then stand together.  An infinity or a NaN in a row of x or
- * base reaches that row of y only; weights of adapters that no row names are
- * not met.  Results do not depend on timing.
+ * in succession do, so rows of one request should then stand together.  An
+ * infinity or a NaN in a row of x or base reaches that row of y only, as an
+ * infinity or a NaN; weights of adapters that no row names are not met, those
+ * of the others are finite (an infinite one may give NaN).  Results do not
+ * depend on timing.
  *   w          host array [count] of descriptors
  *   x          fp16 [m][ldx[i]]
  *   ids        device int32 [m], one for all linears
@@ -526,10 +528,10 @@ typedef struct wq_adapters {
  *              ldb and ldy at least n, of any alignment
  *   workspace  device scratch of wq_lora_workspace bytes (A x of every row),
  *              apart from every other array
- * m 0 does nothing.  Errors (before anything is launched): WQ_E_ARG,
- * WQ_E_ALIGN (also ldx not a multiple of 8; ids need 4-byte alignment),
- * WQ_E_UNSUPPORTED (rank or k as above, m of 2^24, n of 2^30, k of 2^27 or
- * more), WQ_E_WORKSPACE; WQ_E_HIP. */
+ * m 0 does nothing.  Errors (before anything is launched): WQ_E_ARG
+ * (also k not a multiple of 128), WQ_E_ALIGN (also ldx not a multiple of 8;
+ * ids need 4-byte alignment), WQ_E_UNSUPPORTED (rank as above, m of 2^24, n of
+ * 2^30, k of 2^27 or more), WQ_E_WORKSPACE; WQ_E_HIP. */
 size_t wq_lora_workspace(int32_t count, const wq_adapters *w, int64_t m);
 wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x, const int64_t *ldx, int64_t m,
                   const int32_t *ids, const void *const *base, const int64_t *ldb, void *const *y,
@@ -562,13 +564,14 @@ wq_status wq_lora(int32_t count, const wq_adapters *w, const uint16_t *const *x,
  *   workspace  device scratch of wq_sample_workspace bytes, apart from
  *            every other array; no initialisation needed
  * Weights are counted in 2^-44 of a power of two near the largest (2^-43 for
- * vocab above 2^18, 2^-42 above 2^19), each within 2^-34 of itself, and added
- * as whole numbers in 64 bits: the same inputs give the same token, whatever
- * the timing and whatever the other rows are.  Two launches; a row with
- * logits beyond 2^13 T, or with a cut around which more than 8192 logits lie
- * within an eighth of a power of two of w (from 2^-31 of the largest w down:
- * within all that is left), takes several passes over its logits (about 0.1
- * ms more).  rows 0 does nothing.  Errors (before anything is launched):
+ * vocab above 2^18, 2^-42 above 2^19), each within 2^-34 of itself and half
+ * of that unit (smaller ones may count as 0), and added as whole numbers in 64
+ * bits: the same inputs give the same token, whatever the timing and whatever
+ * the other rows are.  Two launches; a row whose largest logit is 2^13 T ln 2
+ * (5678 T) or more from zero, or with a cut around which more than 8192 logits
+ * lie within an eighth of a power of two of w (from 2^-31 of the largest w
+ * down: within all that is left), takes several passes over its logits (about
+ * 0.1 ms more).  rows 0 does nothing.  Errors (before anything is launched):
  * WQ_E_ARG (also an output that overlaps another array), WQ_E_ALIGN (int32
  * and fp32 arrays other than logits need 4-byte alignment), WQ_E_UNSUPPORTED
  * (vocab above 2^20, rows above 2^20), WQ_E_WORKSPACE; WQ_E_HIP. */
