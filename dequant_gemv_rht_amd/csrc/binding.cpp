@@ -1,9 +1,10 @@
 // The Python side of the calls that a decode step issues every few
 // microseconds (wq_kv_write, wq_kv_read, wq_attn_decode, wq_rope, wq_kv_slots,
 // wq_lora, wq_sample): asks the tensors for types, shapes and strides,
-// allocates outputs, and calls the C ABI with the current stream.  In the interpreter the same questions and the
-// marshalling cost more than the kernels (a decode step's rotary positions:
-// 9 us there, 4.6 here, of which the launch is 2.3).
+// allocates outputs, and calls the C ABI with the current stream.  In the
+// interpreter the same questions and the marshalling cost more than the
+// kernels (a decode step's rotary positions: 9 us there, 4.6 here, of which
+// the launch is 2.3).
 //
 // Every function returns its result, or the library's status (a negative
 // int), which the caller turns into an exception with the library's message.
